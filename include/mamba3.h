@@ -405,6 +405,243 @@ typedef struct {
 mamba3_status mamba3_decode_validate(const mamba3_decode_args *args);
 mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
 
+/* ---- Operators of the layers around the recurrence -------------------------
+ *
+ * A layer of the selective (per channel and state) kind that runs next to the
+ * recurrence above, and the norm between layers: the short causal
+ * convolution, the selective scan, both for whole sequences, backwards and
+ * for one token, and the RMS norm with the residual's addition. They follow
+ * the conventions above (device pointers, host validation, no allocation, the
+ * given stream, one token dtype, fp32 states, weights and sums). No argument
+ * struct above changed with them.
+ *
+ * Token rows. Token arrays are [batch, seqlen, n] with n innermost. Those with
+ * a `_row` field may be views of wider rows (the halves of one projection's
+ * output): `_row` is the number of elements from one token to the next, n at
+ * least, or 0 for dense rows. Tokens of a padded batch lie at one distance
+ * across sequences too. Any element alignment is accepted; rows and pointers
+ * that are multiples of 16 bytes are read fastest. Arrays without a `_row`
+ * field are dense.
+ * cu_seqlens, nseq and packed batches are as for mamba3_scan_fwd (entries
+ * clamped to [0, seqlen]; batch 1); S = batch (padded) or nseq (packed);
+ * batch * seqlen <= INT32_MAX.
+ */
+
+/* Short causal convolution over every channel by itself, width W = 2..8:
+ *   p_t[d] = bias[d] + sum_{j < W} weight[d, j] x_{t - W + 1 + j}[d]
+ *   y_t[d] = p_t[d], or p_t[d] / (1 + exp(-p_t[d])) with silu = 1
+ * Inputs before a sequence's start are conv_in's rows (the W - 1 inputs
+ * before it, oldest first) or zero.
+ * x, y      [batch, seqlen, D] token dtype
+ * weight    [D, W] fp32;  bias [D] fp32 or NULL
+ * conv_in   [S, W-1, D] token dtype or NULL
+ * conv_out  [S, W-1, D] or NULL: the last W - 1 inputs of every sequence, those
+ *           of conv_in (or zeros) among them where the sequence is shorter.
+ * y and conv_out overlap neither each other nor any input. */
+typedef struct {
+    int32_t batch, seqlen, dim, width;
+    int32_t dtype;
+    int32_t silu;
+    const int32_t *cu_seqlens;
+    int32_t nseq;
+    int64_t x_row;
+    const void *x;
+    const float *weight, *bias;
+    const void *conv_in;
+    void *y;
+    void *conv_out;
+} mamba3_conv_args;
+
+mamba3_status mamba3_conv_validate(const mamba3_conv_args *args);
+mamba3_status mamba3_conv_fwd(const mamba3_conv_args *args, void *stream);
+
+/* Its backward. fwd is the forward call's (y and conv_out are ignored); dy [batch,
+ * seqlen, D] (dy_row as x_row), dconv_out [S, W-1, D] or NULL (zero).
+ * Outputs, overwritten: dx [batch, seqlen, D] (dense), dweight [D, W] fp32,
+ * dbias [D] fp32 or NULL, dconv_in [S, W-1, D] or NULL (only with conv_in).
+ * No output overlaps an input or another output. workspace: at least
+ * mamba3_conv_bwd_workspace_size(args) bytes, 256-byte aligned: partial sums
+ * of dweight and dbias, added in a fixed order (bitwise reproducible). */
+typedef struct {
+    mamba3_conv_args fwd;
+    int64_t dy_row;
+    const void *dy;
+    const void *dconv_out;
+    void *dx;
+    float *dweight, *dbias;
+    void *dconv_in;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_conv_bwd_args;
+
+mamba3_status mamba3_conv_bwd_validate(const mamba3_conv_bwd_args *args);
+size_t mamba3_conv_bwd_workspace_size(const mamba3_conv_bwd_args *args);
+mamba3_status mamba3_conv_bwd(const mamba3_conv_bwd_args *args, void *stream);
+
+/* One token: y from conv's W - 1 rows and x, and conv moved on by one input, in
+ * place. x, y [batch, D]; conv [batch, W-1, D], or [nslots, W-1, D] with slots
+ * (as in mamba3_decode_step: a row with a slot outside 0 .. nslots - 1 is
+ * skipped, its y row left as it was; active rows name different slots). */
+typedef struct {
+    int32_t batch, dim, width;
+    int32_t dtype;
+    int32_t silu;
+    int64_t x_row;
+    const void *x;
+    const float *weight, *bias;
+    void *conv;
+    void *y;
+    const int32_t *slots;
+    int32_t nslots;
+} mamba3_conv_step_args;
+
+mamba3_status mamba3_conv_step_validate(const mamba3_conv_step_args *args);
+mamba3_status mamba3_conv_step(const mamba3_conv_step_args *args, void *stream);
+
+/* Selective scan: per sequence, channel d (B/C group g = d / (D/G)), state n
+ *   s_t[d]   = dt_t[d] + dt_bias[d], softplus of it with dt_softplus = 1
+ *   h_t[d,n] = exp(s_t[d] A[d,n]) h_{t-1}[d,n] + s_t[d] x_t[d] B_t[g,n]
+ *   y_t[d]   = sum_n C_t[g,n] h_t[d,n] + D[d] x_t[d], times SiLU(z_t[d]) with z
+ * x, dt, z, y  [batch, seqlen, D] token dtype; z may be NULL
+ * B, C         [batch, seqlen, G, N] token dtype, N = 1..128
+ * A            [D, N] fp32, 16-byte aligned;  D, dt_bias [D] fp32 or NULL
+ * h_in, h_out  [S, D, N] fp32, 16-byte aligned, or NULL (zero, not written)
+ * softplus(v) = log(1 + e^v), v itself above 20. y overlaps no input; h_out
+ * may be h_in exactly. workspace: at least
+ * mamba3_selective_scan_workspace_size(args) bytes (0 for many shapes),
+ * 256-byte aligned: where a few long sequences would leave the GPU empty, they
+ * run as independent segments and it holds their states and token ranges. */
+typedef struct {
+    int32_t batch, seqlen, dim, dstate, ngroups;
+    int32_t dtype;
+    int32_t dt_softplus;
+    const int32_t *cu_seqlens;
+    int32_t nseq;
+    int64_t x_row, dt_row, B_row, C_row, z_row;
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *dt_bias;
+    const float *h_in;
+    void *y;
+    float *h_out;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_selective_scan_args;
+
+mamba3_status mamba3_selective_scan_validate(const mamba3_selective_scan_args *args);
+size_t mamba3_selective_scan_workspace_size(const mamba3_selective_scan_args *args);
+mamba3_status mamba3_selective_scan_fwd(const mamba3_selective_scan_args *args, void *stream);
+
+/* Its backward. fwd is the forward call's (y, h_out and workspace are ignored;
+ * nothing of the forward pass needs to be kept). dy [batch, seqlen, D] (dy_row
+ * as x_row), dh_out [S, D, N] fp32 or NULL (zero).
+ * Outputs, overwritten, dense: dx, ddt, dz (only with z, or NULL) [batch,
+ * seqlen, D] and dB, dC [batch, seqlen, G, N] token dtype; dA [D, N] fp32;
+ * dD, ddt_bias [D] fp32 or NULL; dh_in [S, D, N] fp32 or NULL. dh_in and
+ * dh_out are 16-byte aligned. No output overlaps an input or another output.
+ * workspace: at least mamba3_selective_scan_bwd_workspace_size(args) bytes,
+ * 256-byte aligned: the states at the start of every tile of tokens and partial
+ * sums, added in a fixed order (bitwise reproducible). */
+typedef struct {
+    mamba3_selective_scan_args fwd;
+    int64_t dy_row;
+    const void *dy;
+    const float *dh_out;
+    void *dx, *ddt, *dB, *dC, *dz;
+    float *dA, *dD, *ddt_bias;
+    float *dh_in;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_selective_scan_bwd_args;
+
+mamba3_status mamba3_selective_scan_bwd_validate(const mamba3_selective_scan_bwd_args *args);
+size_t mamba3_selective_scan_bwd_workspace_size(const mamba3_selective_scan_bwd_args *args);
+mamba3_status mamba3_selective_scan_bwd(const mamba3_selective_scan_bwd_args *args, void *stream);
+
+/* One token of the selective scan for a batch, states updated in place. x, dt, z,
+ * y [batch, D]; B, C [batch, G, N]; h [batch, D, N] fp32, 16-byte aligned, or
+ * [nslots, D, N] with slots (as in mamba3_conv_step). */
+typedef struct {
+    int32_t batch, dim, dstate, ngroups;
+    int32_t dtype;
+    int32_t dt_softplus;
+    int64_t x_row, dt_row, B_row, C_row, z_row;
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *dt_bias;
+    float *h;
+    void *y;
+    const int32_t *slots;
+    int32_t nslots;
+} mamba3_selective_step_args;
+
+mamba3_status mamba3_selective_step_validate(const mamba3_selective_step_args *args);
+mamba3_status mamba3_selective_step(const mamba3_selective_step_args *args, void *stream);
+
+/* RMS norm of rows with the residual's addition, in fp32:
+ *   s = x + residual (x without one),  v = s / sqrt(mean(s^2) + eps) * weight
+ * x            [rows, dim] token dtype (x_row as above)
+ * residual     [rows, dim] in residual_dtype (the token dtype or fp32) or NULL
+ * residual_out [rows, dim] in residual_dtype or NULL: s (it may be residual
+ *              exactly; the norm uses s before this rounding)
+ * weight       [dim] fp32 or NULL (ones)
+ * y            [rows, dim] token dtype or NULL: v
+ * q, qscale    8-bit output or both NULL: q [rows, dim] bytes and qscale [rows,
+ *              ceil(dim / qblock)] fp32, v = q * qscale up to q's rounding.
+ *              qtype MAMBA3_E4M3 (OCP e4m3, largest value 448) or MAMBA3_INT8
+ *              (-127 .. 127); qblock = 32, 64, 128 or 256 channels a scale, or
+ *              0 or at least dim for one scale a row. qscale = largest |v| of
+ *              the block / largest value, 2^-126 at least (so a block of zeros
+ *              has zeros for q). Both round from fp32 to the nearest, ties to
+ *              even.
+ * At least one of y and q is given. eps is finite and >= 0. Outputs overlap
+ * neither each other nor any input, residual_out = residual aside. */
+typedef enum { MAMBA3_E4M3 = 0, MAMBA3_INT8 = 1 } mamba3_qtype;
+
+typedef struct {
+    int64_t rows;
+    int32_t dim;
+    int32_t dtype, residual_dtype;
+    int32_t qtype, qblock;
+    float eps;
+    int64_t x_row;
+    const void *x, *residual;
+    const float *weight;
+    void *residual_out;
+    void *y;
+    void *q;
+    float *qscale;
+} mamba3_rmsnorm_args;
+
+mamba3_status mamba3_rmsnorm_validate(const mamba3_rmsnorm_args *args);
+mamba3_status mamba3_rmsnorm_fwd(const mamba3_rmsnorm_args *args, void *stream);
+
+/* Its backward, from s (the forward's residual_out, or its x without one):
+ *   ds = dresidual_out + r (w dy - sh mean(w dy sh)),  r = 1 / sqrt(mean(s^2) +
+ *   eps), sh = r s;   dweight = sum over rows of dy sh
+ * s, dresidual_out [rows, dim] in residual_dtype (dresidual_out may be NULL:
+ * zero); dy [rows, dim] token dtype (dy_row as x_row). Outputs: ds as dresidual
+ * (residual_dtype) and as dx (token dtype), one of them at least; dweight
+ * [dim] fp32 or NULL. dresidual may be dresidual_out exactly; otherwise no
+ * output overlaps an input or another output. workspace: at least
+ * mamba3_rmsnorm_bwd_workspace_size(args) bytes, 256-byte aligned: partial sums
+ * of dweight, added in a fixed order (bitwise reproducible). */
+typedef struct {
+    int64_t rows;
+    int32_t dim;
+    int32_t dtype, residual_dtype;
+    float eps;
+    int64_t dy_row;
+    const void *s, *dy, *dresidual_out;
+    const float *weight;
+    void *dx, *dresidual;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_rmsnorm_bwd_args;
+
+mamba3_status mamba3_rmsnorm_bwd_validate(const mamba3_rmsnorm_bwd_args *args);
+size_t mamba3_rmsnorm_bwd_workspace_size(const mamba3_rmsnorm_bwd_args *args);
+mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *args, void *stream);
+
 /* Static description of a status code. */
 const char *mamba3_status_string(mamba3_status status);
 

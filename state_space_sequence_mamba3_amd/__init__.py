@@ -133,6 +133,7 @@ def lib():
         l.mamba3_status_string.argtypes = [ctypes.c_int]
         l.mamba3_status_string.restype = ctypes.c_char_p
         l.mamba3_version.restype = ctypes.c_int32
+        layer.declare(l)
         _lib = l
     return _lib
 
@@ -417,3 +418,12 @@ def mamba3_decode_step(x, dt, lam, theta, B, C, A, D=None, *, h, y=None, Bprev=N
     if st != MAMBA3_OK:
         raise Mamba3Error(st, "mamba3_decode_step")
     return y
+
+
+from . import layer  # noqa: E402  (the layer operators' bindings use the names above)
+from .layer import (LAYER_EXPORTS, MAMBA3_E4M3, MAMBA3_INT8, ConvArgs, ConvBwdArgs, ConvStepArgs,  # noqa: E402, F401
+                    RmsnormArgs, RmsnormBwdArgs, SelectiveScanArgs, SelectiveScanBwdArgs, SelectiveStepArgs,
+                    mamba3_conv_bwd, mamba3_conv_fwd, mamba3_conv_step, mamba3_rmsnorm_bwd, mamba3_rmsnorm_fwd,
+                    mamba3_selective_scan_bwd, mamba3_selective_scan_fwd, mamba3_selective_step)
+
+EXPORTS += LAYER_EXPORTS

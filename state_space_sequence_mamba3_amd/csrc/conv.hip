@@ -1,0 +1,488 @@
+// Short causal convolution (width 2..8) over every channel by itself, with SiLU: whole sequences,
+// their backward, and one token with the state in place.
+//
+// Two products a tap and a byte or two a product: HBM-bound, so the kernels stream. A thread holds
+// V consecutive channels (16 bytes of a token row) and walks kTok tokens of the flat token axis with
+// the last W - 1 inputs in registers; its rows are loaded together before they are worked on. The W
+// - 1 rows before a thread's first token are read twice (mostly from the caches): 3 of 16 at width 4.
+// Sequence starts inside a thread's tokens reset the registers to conv_in's rows (a branch that is
+// uniform across the wave, which shares its tokens).
+#include "layer.h"
+
+namespace m3 {
+
+struct ConvParams {
+    const void *x, *conv_in, *dy, *dconv_out;
+    const float *w, *bias;
+    void *y, *conv_out, *dx, *dconv_in;
+    float *part;                        // partial sums of dweight and dbias: [blocks][W + 1][dim]
+    int64_t x_row, dy_row;
+    const int32_t *cu;
+    int32_t nseq, seqlen, total, dim, silu;
+    int32_t main_blocks, chan_blocks;   // workgroups that walk tokens; those that cover the channels
+};
+
+constexpr int kTok = 16;                // tokens of a thread
+
+// The sequence that holds token t, and its tokens [a, b).
+struct SeqAt {
+    int s, a, b;
+};
+__device__ __forceinline__ SeqAt seq_of(const ConvParams &p, int t) {
+    SeqAt q;
+    if (!p.cu) {
+        q.s = t / p.seqlen;
+        q.a = q.s * p.seqlen;
+        q.b = q.a + p.seqlen;
+        return q;
+    }
+    int lo = 0, hi = p.nseq - 1;        // the last sequence that starts at or before t
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (p.cu[m] <= t) lo = m;
+        else hi = m - 1;
+    }
+    q.s = lo;
+    packed_bounds(p.cu, lo, p.total, q.a, q.b);
+    return q;
+}
+__device__ __forceinline__ SeqAt bounds_of(const ConvParams &p, int s) {
+    SeqAt q;
+    q.s = s;
+    if (p.cu) {
+        packed_bounds(p.cu, s, p.total, q.a, q.b);
+    } else {
+        q.a = s * p.seqlen;
+        q.b = q.a + p.seqlen;
+    }
+    return q;
+}
+// The sequence after token t reached the end of q (the next one that is not empty).
+__device__ __forceinline__ void next_seq(const ConvParams &p, int t, SeqAt &q) {
+    while (t >= q.b) {
+        if (q.s + 1 >= p.nseq) {        // no token lies there in a valid table
+            q.a = t;
+            q.b = INT32_MAX;
+            return;
+        }
+        q = bounds_of(p, q.s + 1);
+    }
+    q.a = min(q.a, t);
+}
+
+// V elements of a row, as fp32
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(float (&o)[V], const T *row) {
+    if constexpr (V == 1) {
+        o[0] = to_f(row[0]);
+    } else {
+        typedef T vec __attribute__((ext_vector_type(V)));
+        const vec v = *(const vec *)row;
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] = to_f(v[e]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *row, const float (&o)[V]) {
+    if constexpr (V == 1) {
+        row[0] = from_f<T>(o[0]);
+    } else {
+        typedef T vec __attribute__((ext_vector_type(V)));
+        vec v;
+#pragma unroll
+        for (int e = 0; e < V; e++) v[e] = from_f<T>(o[e]);
+        *(vec *)row = v;
+    }
+}
+template <typename T, int V> struct RawVec { typedef T type __attribute__((ext_vector_type(V))); };
+template <typename T> struct RawVec<T, 1> { typedef T type; };
+template <typename T, int V>
+__device__ __forceinline__ float raw_f(const typename RawVec<T, V>::type &v, int e) {
+    if constexpr (V == 1) return to_f(v);
+    else return to_f(v[e]);
+}
+
+// Input tau of sequence q, channels c ..: its token, or a row of conv_in before the start.
+template <typename T, int W, int V>
+__device__ __forceinline__ void hist_vec(const ConvParams &p, const SeqAt &q, int tau, int c, float (&o)[V]) {
+    const int j = W - 1 + tau - q.a;
+    if (tau >= q.a) {
+        load_vec<T, V>(o, (const T *)p.x + (int64_t)tau * p.x_row + c);
+    } else if (p.conv_in && j >= 0) {
+        load_vec<T, V>(o, (const T *)p.conv_in + ((int64_t)q.s * (W - 1) + j) * p.dim + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] = 0.f;
+    }
+}
+
+// conv_out: element i of [S, W-1, D]
+template <typename T, int W>
+__device__ __forceinline__ void conv_state(const ConvParams &p, int64_t i) {
+    const int c = (int)(i % p.dim), j = (int)(i / p.dim % (W - 1)), s = (int)(i / p.dim / (W - 1));
+    const SeqAt q = bounds_of(p, s);
+    float o[1];
+    hist_vec<T, W, 1>(p, q, q.b - (W - 1) + j, c, o);
+    ((T *)p.conv_out)[i] = from_f<T>(o[0]);
+}
+
+// 4 waves, each with its own tokens, the same 64 * V channels; the blocks behind the main ones write
+// conv_out.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void k_conv(ConvParams p) {
+    if ((int)blockIdx.x >= p.main_blocks) {
+        const int64_t n = (int64_t)p.nseq * (W - 1) * p.dim;
+        const int64_t i = (int64_t)(blockIdx.x - p.main_blocks) * 256 + threadIdx.x;
+        if (i < n) conv_state<T, W>(p, i);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = (int)(blockIdx.x % p.chan_blocks) * 64 * V + lane * V;
+    const int64_t first = ((int64_t)(blockIdx.x / p.chan_blocks) * 4 + wave) * kTok;
+    if (first >= p.total || c >= p.dim) return;
+    const int t0 = __builtin_amdgcn_readfirstlane((int)first);
+    const T *x = (const T *)p.x + c;
+    typename RawVec<T, V>::type raw[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; i++)
+        raw[i] = *(const typename RawVec<T, V>::type *)(x + (int64_t)min(t0 + i, p.total - 1) * p.x_row);
+    SeqAt q = seq_of(p, t0);
+    next_seq(p, t0, q);
+    float w[W][V], bias[V], win[W][V];   // win[j]: input t - W + 1 + j
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        bias[e] = p.bias ? p.bias[c + e] : 0.f;
+#pragma unroll
+        for (int j = 0; j < W; j++) w[j][e] = p.w[(int64_t)(c + e) * W + j];
+    }
+#pragma unroll
+    for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t0 - W + j, c, win[j]);
+#pragma unroll
+    for (int i = 0; i < kTok; i++) {
+        const int t = t0 + i;
+        if (t >= p.total) break;
+        if (t >= q.b) {
+            next_seq(p, t, q);
+#pragma unroll
+            for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
+        }
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+#pragma unroll
+            for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
+            win[W - 1][e] = raw_f<T, V>(raw[i], e);
+            float v = bias[e];
+#pragma unroll
+            for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
+            o[e] = p.silu ? v * sigmoid_hw(v) : v;
+        }
+        store_vec<T, V>((T *)p.y + (int64_t)t * p.dim + c, o);
+    }
+}
+
+// SiLU's derivative at v
+__device__ __forceinline__ float silu_grad(float v) {
+    const float s = sigmoid_hw(v);
+    return s + v * s * (1.f - s);
+}
+
+// dconv_in, element i of [S, W-1, D]: place k of the history reaches the outputs 0 .. k.
+template <typename T, int W>
+__device__ __forceinline__ void conv_state_grad(const ConvParams &p, int64_t i) {
+    const int c = (int)(i % p.dim), k = (int)(i / p.dim % (W - 1)), s = (int)(i / p.dim / (W - 1));
+    const SeqAt q = bounds_of(p, s);
+    const int len = q.b - q.a;
+    float g = 0.f;
+    for (int t = 0; t <= k && t < len; t++) {
+        float v = p.bias ? p.bias[c] : 0.f, h[1];
+        for (int j = 0; j < W; j++) {
+            hist_vec<T, W, 1>(p, q, q.a + t - W + 1 + j, c, h);
+            v += p.w[(int64_t)c * W + j] * h[0];
+        }
+        const float dy = to_f(((const T *)p.dy)[(int64_t)(q.a + t) * p.dy_row + c]);
+        g += p.w[(int64_t)c * W + k - t] * (p.silu ? dy * silu_grad(v) : dy);
+    }
+    if (k >= len && p.dconv_out)
+        g += to_f(((const T *)p.dconv_out)[((int64_t)s * (W - 1) + k - len) * p.dim + c]);
+    ((T *)p.dconv_in)[i] = from_f<T>(g);
+}
+
+// The backward walks the same tokens plus W - 1 behind them: with e_t = dy_t act'(p_t),
+// dx_tau = sum_j w[j] e_{tau + W - 1 - j}, so dx of a token is complete W - 1 tokens later and waits
+// in registers until then. dweight's and dbias' sums over a workgroup's tokens go to `part`.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
+    if ((int)blockIdx.x >= p.main_blocks) {
+        const int64_t n = (int64_t)p.nseq * (W - 1) * p.dim;
+        const int64_t i = (int64_t)(blockIdx.x - p.main_blocks) * 256 + threadIdx.x;
+        if (i < n) conv_state_grad<T, W>(p, i);
+        return;
+    }
+    __shared__ float red[4][64 * V];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = (int)(blockIdx.x % p.chan_blocks) * 64 * V + lane * V;
+    const int blk = blockIdx.x / p.chan_blocks;
+    const int64_t first = ((int64_t)blk * 4 + wave) * kTok;
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; j++) dw[j][e] = 0.f;
+    }
+    if (first < p.total && c < p.dim) {
+        const int t0 = __builtin_amdgcn_readfirstlane((int)first);
+        const int t1 = min(t0 + kTok, p.total);
+        SeqAt q = seq_of(p, t0);
+        next_seq(p, t0, q);
+        float w[W][V], bias[V], win[W][V], pend[W][V];   // pend[j]: dx of token t - W + 1 + j so far
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            bias[e] = p.bias ? p.bias[c + e] : 0.f;
+#pragma unroll
+            for (int j = 0; j < W; j++) {
+                w[j][e] = p.w[(int64_t)(c + e) * W + j];
+                pend[j][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t0 - W + j, c, win[j]);
+        for (int t = t0; t < t1 + W - 1; t++) {
+            float e_t[V], xin[V];
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+#pragma unroll
+                for (int j = 0; j + 1 < W; j++) pend[j][e] = pend[j + 1][e];
+                pend[W - 1][e] = 0.f;
+                e_t[e] = 0.f;
+            }
+            if (t < p.total) {
+                if (t >= q.b) {
+                    next_seq(p, t, q);
+#pragma unroll
+                    for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
+                }
+                load_vec<T, V>(xin, (const T *)p.x + (int64_t)t * p.x_row + c);
+                load_vec<T, V>(e_t, (const T *)p.dy + (int64_t)t * p.dy_row + c);
+#pragma unroll
+                for (int e = 0; e < V; e++) {
+#pragma unroll
+                    for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
+                    win[W - 1][e] = xin[e];
+                    if (p.silu) {
+                        float v = bias[e];
+#pragma unroll
+                        for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
+                        e_t[e] *= silu_grad(v);
+                    }
+                }
+                const int pos = t - q.a;
+#pragma unroll
+                for (int j = 0; j < W; j++)
+                    if (pos >= W - 1 - j) {           // tap j's input is a token of this sequence
+#pragma unroll
+                        for (int e = 0; e < V; e++) pend[j][e] += w[j][e] * e_t[e];
+                    }
+                if (t < t1) {
+#pragma unroll
+                    for (int e = 0; e < V; e++) {
+                        db[e] += e_t[e];
+#pragma unroll
+                        for (int j = 0; j < W; j++) dw[j][e] += e_t[e] * win[j][e];
+                    }
+                    const int k = t - q.b + (W - 1);  // the token's row of conv_out, if it has one
+                    if (p.dconv_out && k >= 0) {
+                        float o[V];
+                        load_vec<T, V>(o, (const T *)p.dconv_out + ((int64_t)q.s * (W - 1) + k) * p.dim + c);
+#pragma unroll
+                        for (int e = 0; e < V; e++) pend[W - 1][e] += o[e];
+                    }
+                }
+            }
+            const int tau = t - (W - 1);
+            if (tau >= t0) store_vec<T, V>((T *)p.dx + (int64_t)tau * p.dim + c, pend[0]);
+        }
+    }
+    // the four waves' sums, in order
+#pragma unroll
+    for (int j = 0; j <= W; j++) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; e++) red[wave][lane * V + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        __syncthreads();
+        const int c0 = (int)(blockIdx.x % p.chan_blocks) * 64 * V;
+        for (int i = threadIdx.x; i < 64 * V; i += 256)
+            if (c0 + i < p.dim)
+                p.part[((int64_t)blk * (W + 1) + j) * p.dim + c0 + i] =
+                    (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+    }
+}
+
+// dweight [D, W] and dbias [D] from the partial sums of `blocks` workgroups.
+__global__ __launch_bounds__(256) void k_conv_reduce(const float *part, int blocks, int dim, int W, float *dweight,
+                                                     float *dbias) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= dim * (W + 1)) return;
+    const int j = i / dim, c = i % dim;
+    float s = 0.f;
+    for (int b = 0; b < blocks; b++) s += part[((int64_t)b * (W + 1) + j) * dim + c];
+    if (j < W) dweight[(int64_t)c * W + j] = s;
+    else if (dbias) dbias[c] = s;
+}
+
+struct ConvStepParams {
+    const void *x;
+    const float *w, *bias;
+    void *conv, *y;
+    const int32_t *slots;
+    int64_t x_row;
+    int32_t batch, nslots, dim, silu;
+};
+
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void k_conv_step(ConvStepParams p, int chan_blocks) {
+    const int b = blockIdx.x / chan_blocks, c = ((int)(blockIdx.x % chan_blocks) * 256 + threadIdx.x) * V;
+    int64_t slot = b;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.nslots) return;
+    }
+    if (c >= p.dim) return;
+    T *st = (T *)p.conv + slot * (W - 1) * p.dim + c;
+    float h[W][V], o[V];
+#pragma unroll
+    for (int j = 0; j + 1 < W; j++) load_vec<T, V>(h[j], st + (int64_t)j * p.dim);
+    load_vec<T, V>(h[W - 1], (const T *)p.x + b * p.x_row + c);
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        float v = p.bias ? p.bias[c + e] : 0.f;
+#pragma unroll
+        for (int j = 0; j < W; j++) v += p.w[(int64_t)(c + e) * W + j] * h[j][e];
+        o[e] = p.silu ? v * sigmoid_hw(v) : v;
+    }
+#pragma unroll
+    for (int j = 0; j + 1 < W; j++) store_vec<T, V>(st + (int64_t)j * p.dim, h[j + 1]);
+    store_vec<T, V>((T *)p.y + (int64_t)b * p.dim + c, o);
+}
+
+namespace {
+
+// 16-byte pieces: channels, rows and pointers multiples of them
+bool wide(int64_t es, int32_t dim, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> rows) {
+    const int64_t v = 16 / es;
+    if (dim % v) return false;
+    for (const void *q : ptrs)
+        if ((uintptr_t)q & 15u) return false;
+    for (int64_t r : rows)
+        if (r % v) return false;
+    return true;
+}
+
+ConvParams conv_params(const mamba3_conv_args *a) {
+    ConvParams p{};
+    p.x = a->x; p.conv_in = a->conv_in; p.w = a->weight; p.bias = a->bias;
+    p.y = a->y; p.conv_out = a->conv_out;
+    p.x_row = a->x_row ? a->x_row : a->dim;
+    p.cu = a->cu_seqlens;
+    p.nseq = a->cu_seqlens ? a->nseq : a->batch;
+    p.seqlen = a->seqlen;
+    p.total = (int32_t)((int64_t)a->batch * a->seqlen);
+    p.dim = a->dim; p.silu = a->silu;
+    return p;
+}
+
+int64_t token_blocks(int64_t total) { return (total + 4 * kTok - 1) / (4 * kTok); }
+
+#define M3_CONV_WIDTHS(W, CALL)     \
+    switch (W) {                    \
+        case 2: CALL(2); break;     \
+        case 3: CALL(3); break;     \
+        case 4: CALL(4); break;     \
+        case 5: CALL(5); break;     \
+        case 6: CALL(6); break;     \
+        case 7: CALL(7); break;     \
+        default: CALL(8); break;    \
+    }
+
+template <typename T, int V>
+void conv_go(ConvParams p, int width, bool back, hipStream_t st) {
+    p.chan_blocks = (p.dim + 64 * V - 1) / (64 * V);
+    p.main_blocks = (int32_t)(token_blocks(p.total) * p.chan_blocks);
+    const bool state = back ? p.dconv_in != nullptr : p.conv_out != nullptr;
+    const int64_t extra = state ? ((int64_t)p.nseq * (width - 1) * p.dim + 255) / 256 : 0;
+    const dim3 grid((uint32_t)(p.main_blocks + extra));
+    if (grid.x == 0) return;
+#define M3_GO(W)                                                                                  \
+    if (back) hipLaunchKernelGGL((k_conv_bwd<T, W, V>), grid, dim3(256), 0, st, p);               \
+    else hipLaunchKernelGGL((k_conv<T, W, V>), grid, dim3(256), 0, st, p)
+    M3_CONV_WIDTHS(width, M3_GO)
+#undef M3_GO
+}
+
+template <typename T, int V>
+void conv_step_go(const ConvStepParams &p, int width, hipStream_t st) {
+    const int chan_blocks = (p.dim + 256 * V - 1) / (256 * V);
+    const dim3 grid((uint32_t)((int64_t)p.batch * chan_blocks));
+#define M3_GO(W) hipLaunchKernelGGL((k_conv_step<T, W, V>), grid, dim3(256), 0, st, p, chan_blocks)
+    M3_CONV_WIDTHS(width, M3_GO)
+#undef M3_GO
+}
+
+}  // namespace
+
+mamba3_status launch_conv(const mamba3_conv_args *a, hipStream_t st) {
+    const ConvParams p = conv_params(a);
+    if (a->dtype == MAMBA3_F32) {
+        if (wide(4, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<float, 4>(p, a->width, false, st);
+        else conv_go<float, 1>(p, a->width, false, st);
+    } else {
+        if (wide(2, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<bf16, 8>(p, a->width, false, st);
+        else conv_go<bf16, 1>(p, a->width, false, st);
+    }
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+size_t conv_bwd_workspace_bytes(const mamba3_conv_bwd_args *b) {
+    const int64_t total = (int64_t)b->fwd.batch * b->fwd.seqlen;
+    return (size_t)(token_blocks(total) * (b->fwd.width + 1) * b->fwd.dim * 4);
+}
+
+mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st) {
+    const mamba3_conv_args *a = &b->fwd;
+    ConvParams p = conv_params(a);
+    p.dy = b->dy; p.dconv_out = b->dconv_out; p.dx = b->dx; p.dconv_in = b->dconv_in;
+    p.dy_row = b->dy_row ? b->dy_row : a->dim;
+    p.part = (float *)b->workspace;
+    const int64_t es = a->dtype == MAMBA3_BF16 ? 2 : 4;
+    const bool wd = wide(es, p.dim, {p.x, p.conv_in, p.dy, p.dconv_out, p.dx}, {p.x_row, p.dy_row});
+    if (a->dtype == MAMBA3_F32) {
+        if (wd) conv_go<float, 4>(p, a->width, true, st);
+        else conv_go<float, 1>(p, a->width, true, st);
+    } else {
+        if (wd) conv_go<bf16, 8>(p, a->width, true, st);
+        else conv_go<bf16, 1>(p, a->width, true, st);
+    }
+    const int64_t n = (int64_t)p.dim * (a->width + 1);
+    hipLaunchKernelGGL(k_conv_reduce, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, p.part,
+                       (int)token_blocks(p.total), p.dim, a->width, b->dweight, b->dbias);
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+mamba3_status launch_conv_step(const mamba3_conv_step_args *a, hipStream_t st) {
+    ConvStepParams p{};
+    p.x = a->x; p.w = a->weight; p.bias = a->bias; p.conv = a->conv; p.y = a->y;
+    p.slots = a->slots; p.nslots = a->nslots;
+    p.x_row = a->x_row ? a->x_row : a->dim;
+    p.batch = a->batch; p.dim = a->dim; p.silu = a->silu;
+    if (a->dtype == MAMBA3_F32) {
+        if (wide(4, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<float, 4>(p, a->width, st);
+        else conv_step_go<float, 1>(p, a->width, st);
+    } else {
+        if (wide(2, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<bf16, 8>(p, a->width, st);
+        else conv_step_go<bf16, 1>(p, a->width, st);
+    }
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+}  // namespace m3

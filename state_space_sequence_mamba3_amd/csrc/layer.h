@@ -1,0 +1,115 @@
+// Shared device helpers of the layer operators (short convolution, selective scan, residual RMS norm).
+#pragma once
+
+#include "m3_common.h"
+
+namespace m3 {
+
+// Four consecutive elements of a token array as one load (8 bytes of bf16, 16 of fp32).
+template <typename T> struct QuadOf;
+template <> struct QuadOf<float> { typedef f32x4 type; };
+template <> struct QuadOf<bf16> { typedef bf16x4 type; };
+template <typename T> using quad = typename QuadOf<T>::type;
+
+// Elements c0 .. c0 + 3 of a row of n elements. VEC: n and c0 are multiples of 4 and the row is
+// aligned to a quad. Places behind the row's end repeat its last element (or quad), so that every
+// lane loads from inside the row; their results are never stored.
+template <typename T, bool VEC>
+__device__ __forceinline__ quad<T> load_quad(const T *row, int c0, int n) {
+    quad<T> v;
+    if constexpr (VEC) {
+        v = *(const quad<T> *)(row + min(c0, n - 4));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = row[min(c0 + e, n - 1)];
+    }
+    return v;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_quad(T *row, int c0, int n, f32x4 v) {
+    if constexpr (VEC) {
+        if (c0 < n) {
+            quad<T> o;
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[e] = from_f<T>(v[e]);
+            *(quad<T> *)(row + c0) = o;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (c0 + e < n) row[c0 + e] = from_f<T>(v[e]);
+    }
+}
+
+// e^v, log(1 + e^v) and 1 / (1 + e^-v) on the hardware's exp2, log2 and reciprocal (about one unit
+// in the last place each). log1p by its series where e^v < 1/16: 1 + e^v would round the small
+// term's low bits away, and the step sizes of a layer lie there.
+__device__ __forceinline__ float exp_hw(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
+__device__ __forceinline__ float softplus_hw(float v) {
+    const float w = exp_hw(v);
+    const float series =
+        w * (1.f + w * (-0.5f + w * (0.33333333f + w * (-0.25f + w * (0.2f + w * (-0.16666667f + w * 0.14285715f))))));
+    const float big = __builtin_amdgcn_logf(1.f + w) * 0.69314718056f;
+    return v > 20.f ? v : w < 0.0625f ? series : big;
+}
+__device__ __forceinline__ float sigmoid_hw(float v) { return __builtin_amdgcn_rcpf(1.f + exp_hw(-v)); }
+
+// One wave's LDS traffic is in order: the barrier only keeps the compiler from moving accesses
+// across it.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// DPP move into the lanes of `BANKS` (4-lane banks of every 16-lane row) of `keep`; the other lanes keep.
+template <int CTRL, int BANKS>
+__device__ __forceinline__ float dpp_into(float keep, float from) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_int(keep), __float_as_int(from), CTRL, 0xF, BANKS, false));
+}
+
+// K values a lane, summed over each group of K consecutive lanes; lane i of a group gets the sum of
+// value i. Every level halves the values: a lane keeps the half that its bit names and hands the
+// other half to the lane across, so K values cost about 3 (K - 1) operations instead of K log2(K)
+// additions and K selections.
+template <int K>
+__device__ __forceinline__ float transpose_sum(float (&p)[K], int lane) {
+    static_assert(K == 1 || K == 2 || K == 4 || K == 8 || K == 16, "groups inside a 16-lane row");
+    if constexpr (K >= 2) {
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int i = 0; i < K / 2; i++) {
+            const float keep = odd ? p[2 * i + 1] : p[2 * i], send = odd ? p[2 * i] : p[2 * i + 1];
+            p[i] = keep + dpp_move<0xB1>(send);                 // lane ^ 1
+        }
+    }
+    if constexpr (K >= 4) {
+        const bool up = lane & 2;
+#pragma unroll
+        for (int i = 0; i < K / 4; i++) {
+            const float keep = up ? p[2 * i + 1] : p[2 * i], send = up ? p[2 * i] : p[2 * i + 1];
+            p[i] = keep + dpp_move<0x4E>(send);                 // lane ^ 2
+        }
+    }
+    if constexpr (K >= 8) {
+#pragma unroll
+        for (int i = 0; i < K / 8; i++) {                       // lane ^ 4: shifts by 4 into alternate banks
+            const float a = p[2 * i], b = p[2 * i + 1];
+            p[i] = dpp_into<0x104, 0x5>(b, a) + dpp_into<0x114, 0xA>(a, b);
+        }
+    }
+    if constexpr (K >= 16) {                                    // lane ^ 8: a rotation of the row by 8
+        const float a = p[0], b = p[1];
+        p[0] = dpp_into<0x128, 0x3>(b, a) + dpp_into<0x128, 0xC>(a, b);
+    }
+    return p[0];
+}
+
+// Sequence s of a packed batch: its tokens [a, b), entries clamped to [0, total].
+__device__ __forceinline__ void packed_bounds(const int32_t *cu, int s, int total, int &a, int &b) {
+    a = min(max(cu[s], 0), total);
+    b = min(max(cu[s + 1], a), total);
+}
+
+}  // namespace m3

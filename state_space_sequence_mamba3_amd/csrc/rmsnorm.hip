@@ -1,0 +1,440 @@
+// RMS norm of rows with the residual's addition, its 8-bit output with scales, and its backward.
+//
+//   s = x + residual,  v = s rsqrt(mean(s^2) + eps) w,  q = round(v / scale)
+//   ds = dresidual_out + r (w dy - sh mean(w dy sh)),  dw = sum over rows of dy sh
+//
+// A few operations a value, so HBM-bound: every row is read once, kept in registers as fp32 between its
+// sum and its outputs (rows of more than 8192 values are read twice), and everything a row needs
+// is written in the same pass. A lane holds 8 consecutive values, so a wave's load covers 1 KB of
+// bf16, and a scale's block of 32 .. 256 values lies in 4 .. 32 consecutive lanes.
+#include "layer.h"
+
+namespace m3 {
+
+constexpr int kNV = 8;    // consecutive values of a lane
+
+struct NormParams {
+    const void *x, *res, *dy, *dres;     // (backward: x is s)
+    const float *w;
+    void *res_out, *y, *q, *dx;
+    float *scale, *part, *dw;
+    int64_t rows, x_row, dy_row;
+    int32_t dim, qtype, qblock, nblocks;
+    float eps;
+};
+
+// 8 values of a row from column c on; zeros behind the row's end
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(float (&o)[kNV], const T *row, int c, int n) {
+    if constexpr (VEC) {
+        if (c < n) {
+            if constexpr (sizeof(T) == 2) {
+                const bf16x8 v = *(const bf16x8 *)(row + c);
+#pragma unroll
+                for (int e = 0; e < 8; e++) o[e] = to_f(v[e]);
+            } else {
+                const f32x4 a = *(const f32x4 *)(row + c), b = *(const f32x4 *)(row + c + 4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    o[e] = a[e];
+                    o[e + 4] = b[e];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) o[e] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) o[e] = c + e < n ? to_f(row[c + e]) : 0.f;
+    }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T *row, int c, int n, const float (&o)[kNV]) {
+    if constexpr (VEC) {
+        if (c < n) {
+            if constexpr (sizeof(T) == 2) {
+                bf16x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = from_f<bf16>(o[e]);
+                *(bf16x8 *)(row + c) = v;
+            } else {
+                *(f32x4 *)(row + c) = f32x4{o[0], o[1], o[2], o[3]};
+                *(f32x4 *)(row + c + 4) = f32x4{o[4], o[5], o[6], o[7]};
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (c + e < n) row[c + e] = from_f<T>(o[e]);
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_move<0xB1>(v);
+    v += dpp_move<0x4E>(v);
+    v += dpp_move<0x141>(v);    // half-row mirror: the other quad of 8
+    v += dpp_move<0x140>(v);    // row mirror: the other 8 of 16
+    return sum_across_rows(v);
+}
+// The larger of two values, NaN if either is (a NaN in a block shows in its scale).
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+
+// The sum over the WPR waves that share a row (every lane gets it).
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = wave_sum(v);
+    if constexpr (WPR > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; i++) v += red[i];
+    }
+    return v;
+}
+template <int WPR>
+__device__ __forceinline__ float row_max(float v, float *red) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v = max_nan(v, __shfl_xor(v, o, 64));
+    if constexpr (WPR > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < WPR; i++) v = max_nan(v, red[i]);
+    }
+    return v;
+}
+
+constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126: a block of zeros divides by it
+
+// q = round(v / scale). One Newton step makes the quotient by the reciprocal the correctly rounded
+// one in all but rare cases, so q is the nearest 8-bit value of the true quotient.
+__device__ __forceinline__ float quotient(float v, float scale, float r) {
+    const float q = v * r;
+    const float f = fmaf(fmaf(-scale, q, v), r, q);
+    return f == f ? f : q;      // infinities: the correction is not a number where the quotient is
+}
+template <bool VEC>
+__device__ __forceinline__ void store_q(const NormParams &p, int64_t row, int c, const float (&v)[kNV], float scale) {
+    if (c >= p.dim) return;
+    const float r = 1.f / scale;
+    uint32_t w[2] = {0, 0};
+    if (p.qtype == MAMBA3_E4M3) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            int t = 0;
+            t = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * h], scale, r), quotient(v[4 * h + 1], scale, r), t, false);
+            t = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * h + 2], scale, r), quotient(v[4 * h + 3], scale, r), t, true);
+            w[h] = (uint32_t)t;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kNV; e++) {
+            const float f = fminf(fmaxf(rintf(quotient(v[e], scale, r)), -127.f), 127.f);
+            w[e >> 2] |= ((uint32_t)(int)f & 255u) << (8 * (e & 3));
+        }
+    }
+    uint8_t *q = (uint8_t *)p.q + row * p.dim + c;
+    if constexpr (VEC) {
+        *(uint2 *)q = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kNV; e++)
+            if (c + e < p.dim) q[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    }
+}
+
+// WPR waves share a row (a workgroup holds 4 / WPR rows); NCH > 0: a lane keeps NCH pieces of 8
+// values in registers; NCH = 0: rows of any length, read again for the outputs.
+template <typename T, typename RT, int WPR, int NCH, bool VEC>
+__global__ __launch_bounds__(256) void k_norm(NormParams p) {
+    __shared__ float red[4];
+    constexpr int STEP = WPR * 64 * kNV;
+    const int64_t row = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= p.rows) return;                       // (whole waves; WPR = 4: never)
+    const int t = WPR == 4 ? threadIdx.x : threadIdx.x & 63;
+    const T *x = (const T *)p.x + row * p.x_row;
+    const RT *res = p.res ? (const RT *)p.res + row * p.dim : nullptr;
+    RT *ro = p.res_out ? (RT *)p.res_out + row * p.dim : nullptr;
+    const int nch = NCH ? NCH : (p.dim + STEP - 1) / STEP;
+    float keep[NCH ? NCH : 1][kNV];
+    auto sum_of = [&](int c, float (&s)[kNV]) {
+        load8<T, VEC>(s, x, c, p.dim);
+        if (res) {
+            float r[kNV];
+            load8<RT, VEC>(r, res, c, p.dim);
+#pragma unroll
+            for (int e = 0; e < kNV; e++) s[e] += r[e];
+        }
+    };
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < nch; i++) {
+        float(&s)[kNV] = keep[NCH ? i : 0];
+        sum_of(i * STEP + t * kNV, s);
+#pragma unroll
+        for (int e = 0; e < kNV; e++) ss += s[e] * s[e];
+    }
+    const float rms = __builtin_amdgcn_rsqf(row_sum<WPR>(ss, red) / (float)p.dim + p.eps);
+    const bool one = p.q && p.nblocks == 1;          // one scale a row
+    const float qmax = p.qtype == MAMBA3_E4M3 ? 448.f : 127.f;
+    auto normed = [&](int c, const float (&s)[kNV], float (&v)[kNV]) {
+        float w[kNV];
+        if (p.w) load8<float, VEC>(w, p.w, c, p.dim);
+#pragma unroll
+        for (int e = 0; e < kNV; e++) v[e] = s[e] * rms * (p.w ? w[e] : 1.f);
+    };
+    float whole = 1.f;
+    if (one) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < nch; i++) {
+            const int c = i * STEP + t * kNV;
+            float s[kNV], v[kNV];
+            if constexpr (NCH == 0) sum_of(c, s);
+            normed(c, NCH ? keep[NCH ? i : 0] : s, v);
+#pragma unroll
+            for (int e = 0; e < kNV; e++) m = max_nan(m, c + e < p.dim ? fabsf(v[e]) : 0.f);
+        }
+        const float top = row_max<WPR>(m, red) / qmax;
+        whole = top < kTinyScale ? kTinyScale : top;
+        if (t == 0) p.scale[row] = whole;
+    }
+#pragma unroll
+    for (int i = 0; i < nch; i++) {
+        const int c = i * STEP + t * kNV;
+        float again[kNV], v[kNV];
+        if constexpr (NCH == 0) sum_of(c, again);
+        const float(&s)[kNV] = NCH ? keep[NCH ? i : 0] : again;
+        if (ro) store8<RT, VEC>(ro, c, p.dim, s);
+        normed(c, s, v);
+        if (p.y) store8<T, VEC>((T *)p.y + row * p.dim, c, p.dim, v);
+        if (p.q) {
+            float sc = whole;
+            if (!one) {
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < kNV; e++) m = max_nan(m, c + e < p.dim ? fabsf(v[e]) : 0.f);
+                for (int o = 1; o < p.qblock / kNV; o <<= 1) m = max_nan(m, __shfl_xor(m, o, 64));
+                sc = m / qmax;
+                sc = sc < kTinyScale ? kTinyScale : sc;
+                if (c < p.dim && c % p.qblock == 0) p.scale[row * p.nblocks + c / p.qblock] = sc;
+            }
+            store_q<VEC>(p, row, c, v, sc);
+        }
+    }
+}
+
+// Backward: as the forward; a workgroup walks several rows, so that dweight's partial sums stay in
+// registers (NCH = 0: dweight's columns are added by k_norm_dw).
+template <typename T, typename RT, int WPR, int NCH, bool VEC>
+__global__ __launch_bounds__(256) void k_norm_bwd(NormParams p) {
+    __shared__ float red[4];
+    constexpr int STEP = WPR * 64 * kNV;
+    const int t = WPR == 4 ? threadIdx.x : threadIdx.x & 63;
+    const int64_t first = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t step = (int64_t)gridDim.x * (4 / WPR);
+    const int nch = NCH ? NCH : (p.dim + STEP - 1) / STEP;
+    float dw[NCH ? NCH : 1][kNV];
+#pragma unroll
+    for (int i = 0; i < (NCH ? NCH : 1); i++)
+#pragma unroll
+        for (int e = 0; e < kNV; e++) dw[i][e] = 0.f;
+    for (int64_t row = first; row < p.rows; row += step) {
+        const RT *s = (const RT *)p.x + row * p.dim;
+        const T *dy = (const T *)p.dy + row * p.dy_row;
+        float ks[NCH ? NCH : 1][kNV], kd[NCH ? NCH : 1][kNV];
+        float ss = 0.f, sd = 0.f;
+        auto fetch = [&](int c, float (&a)[kNV], float (&b)[kNV]) {   // s and dy
+            load8<RT, VEC>(a, s, c, p.dim);
+            load8<T, VEC>(b, dy, c, p.dim);
+        };
+        auto weigh = [&](int c, float (&w)[kNV]) {
+            if (p.w) {
+                load8<float, VEC>(w, p.w, c, p.dim);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kNV; e++) w[e] = 1.f;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < nch; i++) {
+            const int c = i * STEP + t * kNV, k = NCH ? i : 0;
+            float w[kNV];
+            fetch(c, ks[k], kd[k]);
+            weigh(c, w);
+#pragma unroll
+            for (int e = 0; e < kNV; e++) {
+                ss += ks[k][e] * ks[k][e];
+                sd += ks[k][e] * (c + e < p.dim ? w[e] * kd[k][e] : 0.f);
+            }
+        }
+        const float r = __builtin_amdgcn_rsqf(row_sum<WPR>(ss, red) / (float)p.dim + p.eps);
+        const float m = row_sum<WPR>(sd, red) / (float)p.dim * r * r * r;   // ds = r w dy - m s
+        if (NCH == 0 && t == 0 && p.part) p.part[row] = r;
+#pragma unroll
+        for (int i = 0; i < nch; i++) {
+            const int c = i * STEP + t * kNV, k = NCH ? i : 0;
+            float w[kNV], o[kNV];
+            if constexpr (NCH == 0) fetch(c, ks[0], kd[0]);
+            weigh(c, w);
+            if (p.dres) load8<RT, VEC>(o, (const RT *)p.dres + row * p.dim, c, p.dim);
+#pragma unroll
+            for (int e = 0; e < kNV; e++) {
+                o[e] = (p.dres ? o[e] : 0.f) + (r * w[e] * kd[k][e] - m * ks[k][e]);
+                if constexpr (NCH > 0) dw[k][e] += kd[k][e] * ks[k][e] * r;
+            }
+            if (p.res_out) store8<RT, VEC>((RT *)p.res_out + row * p.dim, c, p.dim, o);
+            if (p.dx) store8<T, VEC>((T *)p.dx + row * p.dim, c, p.dim, o);
+        }
+    }
+    if constexpr (NCH > 0) {
+        if (p.part) {
+            // one row of partial sums a workgroup (WPR = 4) or a wave (WPR = 1)
+            float *out = p.part + (WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * p.dim;
+#pragma unroll
+            for (int i = 0; i < NCH; i++) store8<float, VEC>(out, i * STEP + t * kNV, p.dim, dw[i]);
+        }
+    }
+}
+
+// dweight from `n` rows of partial sums: 64 columns a workgroup, 4 waves over the rows.
+__global__ __launch_bounds__(256) void k_norm_reduce(const float *part, int64_t n, int dim, float *dw) {
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < dim)
+        for (int64_t i = wave; i < n; i += 4) s += part[i * dim + c];
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < dim) dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+// dweight of long rows: 64 columns a workgroup over all rows, with the rows' 1 / rms from k_norm_bwd.
+template <typename T, typename RT>
+__global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < p.dim)
+        for (int64_t i = wave; i < p.rows; i += 4)
+            s += to_f(((const T *)p.dy)[i * p.dy_row + c]) * to_f(((const RT *)p.x)[i * p.dim + c]) * p.part[i];
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < p.dim) p.dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+namespace {
+
+bool wide(const void *q, int64_t row, int64_t es) { return ((uintptr_t)q & 15u) == 0 && row * es % 16 == 0; }
+
+// Rows of up to 2048 values fit one wave's registers; one wave a row needs no barrier, four waves a
+// row spread few rows over more of the GPU.
+bool one_wave(int64_t rows, int dim) { return dim <= 512 || (dim <= 2048 && rows >= 2048); }
+
+constexpr int kBwdBlocks = 1024;
+
+int64_t bwd_parts(int64_t rows, int dim) {   // rows of partial sums
+    if (dim > 8192) return 0;
+    return one_wave(rows, dim) ? 4 * std::min<int64_t>((rows + 3) / 4, kBwdBlocks) : std::min<int64_t>(rows, kBwdBlocks);
+}
+
+template <typename T, typename RT, int WPR, int NCH>
+void norm_launch(const NormParams &p, bool vec, bool back, hipStream_t st) {
+    const int64_t per = 4 / WPR, blocks = (p.rows + per - 1) / per;
+    const dim3 grid((uint32_t)(back ? std::min<int64_t>(blocks, kBwdBlocks) : blocks));
+    if (back) {
+        if (vec) hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, NCH, true>), grid, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, NCH, false>), grid, dim3(256), 0, st, p);
+    } else {
+        if (vec) hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, true>), grid, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, false>), grid, dim3(256), 0, st, p);
+    }
+}
+
+template <typename T, typename RT>
+void norm_go(const NormParams &p, bool vec, bool back, hipStream_t st) {
+    if (one_wave(p.rows, p.dim)) {
+        if (p.dim <= 512) norm_launch<T, RT, 1, 1>(p, vec, back, st);
+        else if (p.dim <= 1024) norm_launch<T, RT, 1, 2>(p, vec, back, st);
+        else norm_launch<T, RT, 1, 4>(p, vec, back, st);
+    } else if (p.dim <= 2048) {
+        norm_launch<T, RT, 4, 1>(p, vec, back, st);
+    } else if (p.dim <= 4096) {
+        norm_launch<T, RT, 4, 2>(p, vec, back, st);
+    } else if (p.dim <= 8192) {
+        norm_launch<T, RT, 4, 4>(p, vec, back, st);
+    } else {
+        norm_launch<T, RT, 4, 0>(p, vec, back, st);
+    }
+}
+
+template <typename T, typename RT>
+void dw_go(const NormParams &p, hipStream_t st) {
+    hipLaunchKernelGGL((k_norm_dw<T, RT>), dim3((p.dim + 63) / 64), dim3(256), 0, st, p);
+}
+
+}  // namespace
+
+mamba3_status launch_rmsnorm(const mamba3_rmsnorm_args *a, hipStream_t st) {
+    NormParams p{};
+    const int64_t es = a->dtype == MAMBA3_BF16 ? 2 : 4, rs = a->residual_dtype == MAMBA3_BF16 ? 2 : 4;
+    p.x = a->x; p.res = a->residual; p.w = a->weight;
+    p.res_out = a->residual_out; p.y = a->y; p.q = a->q; p.scale = a->qscale;
+    p.rows = a->rows; p.dim = a->dim; p.x_row = a->x_row ? a->x_row : a->dim;
+    p.qtype = a->qtype;
+    const bool whole = a->qblock == 0 || a->qblock >= a->dim;
+    p.qblock = whole ? a->dim : a->qblock;
+    p.nblocks = whole ? 1 : (a->dim + a->qblock - 1) / a->qblock;
+    p.eps = a->eps;
+    const bool vec = a->dim % 8 == 0 && wide(p.x, p.x_row, es) && wide(p.res, p.dim, rs) && wide(p.w, p.dim, 4) &&
+                     wide(p.res_out, p.dim, rs) && wide(p.y, p.dim, es) && ((uintptr_t)p.q & 7u) == 0;
+    if (a->dtype == MAMBA3_F32) norm_go<float, float>(p, vec, false, st);
+    else if (a->residual_dtype == MAMBA3_F32) norm_go<bf16, float>(p, vec, false, st);
+    else norm_go<bf16, bf16>(p, vec, false, st);
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+size_t rmsnorm_bwd_workspace_bytes(const mamba3_rmsnorm_bwd_args *b) {
+    if (!b->dweight) return 0;
+    // rows longer than the registers leave their 1 / rms instead
+    return (size_t)(b->dim > 8192 ? b->rows * 4 : bwd_parts(b->rows, b->dim) * b->dim * 4);
+}
+
+mamba3_status launch_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *b, hipStream_t st) {
+    NormParams p{};
+    const int64_t es = b->dtype == MAMBA3_BF16 ? 2 : 4, rs = b->residual_dtype == MAMBA3_BF16 ? 2 : 4;
+    p.x = b->s; p.dy = b->dy; p.dres = b->dresidual_out; p.w = b->weight;
+    p.res_out = b->dresidual; p.dx = b->dx; p.dw = b->dweight;
+    p.part = b->dweight ? (float *)b->workspace : nullptr;
+    p.rows = b->rows; p.dim = b->dim; p.dy_row = b->dy_row ? b->dy_row : b->dim;
+    p.eps = b->eps;
+    const bool vec = b->dim % 8 == 0 && wide(p.x, p.dim, rs) && wide(p.dy, p.dy_row, es) && wide(p.dres, p.dim, rs) &&
+                     wide(p.w, p.dim, 4) && wide(p.res_out, p.dim, rs) && wide(p.dx, p.dim, es);
+    if (p.rows > 0) {
+        if (b->dtype == MAMBA3_F32) norm_go<float, float>(p, vec, true, st);
+        else if (b->residual_dtype == MAMBA3_F32) norm_go<bf16, float>(p, vec, true, st);
+        else norm_go<bf16, bf16>(p, vec, true, st);
+    }
+    if (b->dweight) {
+        if (b->dim <= 8192) {
+            hipLaunchKernelGGL(k_norm_reduce, dim3((b->dim + 63) / 64), dim3(256), 0, st, p.part,
+                               bwd_parts(b->rows, b->dim), b->dim, b->dweight);
+        } else if (b->dtype == MAMBA3_F32) {
+            dw_go<float, float>(p, st);
+        } else if (b->residual_dtype == MAMBA3_F32) {
+            dw_go<bf16, float>(p, st);
+        } else {
+            dw_go<bf16, bf16>(p, st);
+        }
+    }
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+}  // namespace m3
