@@ -178,7 +178,8 @@ static mamba3_status sel_shape(const mamba3_selective_scan_args *a, int64_t *S, 
     if (a->dstate > 128) return MAMBA3_EUNSUPPORTED;
     // workgroups of 16 channels of a group at least; the backward's sums
     const int64_t tiles = ((int64_t)a->dim / a->ngroups + 15) / 16 * a->ngroups;
-    if (*S * tiles > kMaxBlocks || (*T * 2 * gn + (int64_t)a->dim * (a->dstate + 2)) / 256 + 2 > kMaxBlocks)
+    if ((*S + *T / 64 + 1) * tiles > kMaxBlocks || *S * (((int64_t)a->dim * a->dstate + 255) / 256) > kMaxBlocks ||
+         (*T * 2 * gn + (int64_t)a->dim * (a->dstate + 2)) / 256 + 2 > kMaxBlocks)
         return MAMBA3_EINVAL;
     return MAMBA3_OK;
 }

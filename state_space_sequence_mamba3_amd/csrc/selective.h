@@ -24,31 +24,58 @@ struct SelParams {
     int32_t dim, dpg, N, G;  // channels, channels of a B/C group, states a channel, groups
     int32_t tiles;           // workgroups that cover a group's channels
     int32_t softplus;
-    float *ckpt;             // the states before every tile of a row (the backward's first pass), or NULL
+    // Rows: a sequence each (nseg 1), or its segments of seg_tokens tokens: nseg a sequence of a padded
+    // batch, or those of the table of a packed one.
+    int32_t rows, nseg, seg_tokens;
+    const int4 *table;       // t0, t1, sequence (-1: no segment), 1 first | 2 last of its sequence
+    const int32_t *seq_row;  // [nseq + 1] a sequence's first row in the table
+    float *seg_h;            // [rows][D][N] a segment's last state from zero, then the state entering it
+    float *seg_s;            // [rows][D] the sum of a segment's steps
+    // the backward's first pass
+    const void *dy;
+    int64_t dy_row;
+    float *seg_g;            // [rows][D][N] the segment's share of the gradient that enters the one before,
+                             // then the gradient that enters the segment at its end
+    float *ckpt;             // the states before every tile of a row
+    float *ckpt_s;           // the sums of the steps before them (segments only)
 };
 
 // A row of tokens that one workgroup walks: [t0, t1) of sequence seq.
 struct SelRow {
     int t0, t1, seq;
+    bool first, last;
 };
 
 __device__ __forceinline__ SelRow sel_row(const SelParams &p, int r) {
     SelRow o;
-    o.seq = r;
-    if (p.cu) {
+    o.first = o.last = true;
+    if (p.table) {
+        const int4 e = p.table[r];
+        o.t0 = e.x;
+        o.t1 = e.y;
+        o.seq = e.z;
+        o.first = e.w & 1;
+        o.last = e.w & 2;
+    } else if (p.cu) {
+        o.seq = r;
         packed_bounds(p.cu, r, p.total, o.t0, o.t1);
     } else {
-        o.t0 = r * p.seqlen;
-        o.t1 = o.t0 + p.seqlen;
+        const int k = r % p.nseg, a = r / p.nseg * p.seqlen;
+        o.seq = r / p.nseg;
+        o.t0 = a + min(k * p.seg_tokens, p.seqlen);
+        o.t1 = min(o.t0 + min(p.seg_tokens, p.seqlen), a + p.seqlen);
+        o.first = k == 0;
+        o.last = k == p.nseg - 1;
     }
     return o;
 }
 
-// Tokens between two stored states: as many as the backward keeps in registers (64 states a lane).
-template <int NPL> constexpr int kSelStored = 64 / NPL;
-// The stored states of a row that starts at token t0 begin at this index (a row of len tokens takes
-// ceil(len / every) of them, at most len / every + 1, so that rows never overlap).
-__device__ __forceinline__ int64_t stored_base(const SelRow &row, int every) { return row.t0 / every + row.seq; }
+// Tokens between two states that the backward's first pass stores: its second pass computes the states
+// and decays between them again and keeps both in registers, 4 or 8 of each a lane and token.
+constexpr int kSelStored = 8;
+// The stored states of row r begin at this index (a row of len tokens takes ceil(len / every) of them,
+// at most len / every + 1, so that rows, which lie in the order of their tokens, never overlap).
+__device__ __forceinline__ int64_t stored_base(int t0, int r, int every) { return (int64_t)t0 / every + r; }
 // The lane's place in stored state k: workgroup column gt of `per`, four states of 64 lanes together.
 __device__ __forceinline__ int64_t stored_at(int64_t k, int per, int gt, int wave, int lane, int npl) {
     return (((k * per + gt) * kSelWaves + wave) * (npl / 4)) * 256 + lane * 4;
@@ -95,9 +122,24 @@ __device__ __forceinline__ void store_states(const float (&h)[NPL], float *row, 
         else CALL(8, 16);                     \
     } while (0)
 
+// Lanes a channel and states a lane of the arrangement above.
+inline void sel_shape(int N, int &npl, int &lpc) {
+#define M3_GO(NPL, LPC) npl = NPL, lpc = LPC
+    M3_SEL_DISPATCH(N, M3_GO);
+#undef M3_GO
+}
+
 SelParams sel_params(const mamba3_selective_scan_args *a);
 bool sel_vec(const SelParams &p, int64_t es);
-// Enqueue the scan that writes p.ckpt and no outputs.
+// Rows of a call (p.rows, nseg, seg_tokens): whole sequences, or segments where those leave the GPU
+// empty. True if segments; they need seg_bytes of workspace for the parts that `sel_segments` lays out.
+bool sel_plan(SelParams &p);
+size_t sel_segment_bytes(const SelParams &p);
+void sel_segments(SelParams &p, char *ws);
+// Enqueue: a packed batch's segment table; the scan that writes p.ckpt (and segments' ends) and no
+// outputs; the chain over the segments of a sequence, forward and (p.seg_g) backward.
+void launch_sel_table(const SelParams &p, hipStream_t st);
 void launch_sel_stored(const SelParams &p, int32_t dtype, bool vec, hipStream_t st);
+void launch_sel_chain(const SelParams &p, const float *dh_out, hipStream_t st);
 
 }  // namespace m3

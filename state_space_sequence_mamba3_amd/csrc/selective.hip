@@ -26,8 +26,13 @@ struct SelLds {
 // workgroup whole 128-byte lines), prepared there (softplus, dt' x, fp32) and laid into the wave's
 // own LDS; the recurrence then reads them as broadcasts. No wave waits for another.
 //
-// STORE: the backward's first pass. No outputs; the states before every kSelStored tokens go to p.ckpt.
-template <typename T, int NPL, int LPC, bool VEC, bool STORE>
+// FULL writes y and h_out. PART is a segment's first pass: its last state from a zero state and the sum
+// of its steps, no outputs. STORE is the backward's first pass: the states before every kSelStored
+// tokens; STORE_PART the same for segments, with PART's results and the segment's share of the
+// gradient that flows on to the one before it, sum_t (prod_{s <= t} a_s) C_t r_t.
+enum SelMode { FULL, PART, STORE, STORE_PART };
+
+template <typename T, int NPL, int LPC, bool VEC, int MODE>
 __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     constexpr int CW = 64 / LPC, NP = NPL * LPC, TT = kSelTile;
     constexpr int XQ = TT * CW / 4, XE = (XQ + 63) / 64;      // quads of a channel tile, and of a lane
@@ -40,6 +45,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     const int c0 = ((gt % p.tiles) * kSelWaves + wave) * CW;  // the wave's first channel in its group
     if (c0 >= p.dpg) return;
     const SelRow row = sel_row(p, r);
+    if (row.seq < 0 || (MODE == PART && row.last)) return;    // (nothing takes up a last segment's end)
+    constexpr bool CKPT = MODE == STORE || MODE == STORE_PART, ENDS = MODE == PART || MODE == STORE_PART;
+    constexpr bool NEEDC = MODE == FULL || MODE == STORE_PART;
     const int ch = lane / LPC, sub = lane % LPC, n0 = sub * NPL;
     const bool real = c0 + ch < p.dpg;
     const int d = g * p.dpg + min(c0 + ch, p.dpg - 1);        // the lane's channel in the recurrence
@@ -50,7 +58,14 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     for (int i = 0; i < NPL; i++) A2[i] *= kLog2e;
 #pragma unroll
     for (int i = 0; i < NPL; i++) h[i] = 0.f;
-    if (p.h_in) load_states<NPL, VEC>(h, p.h_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    if (MODE == FULL && p.seg_h) load_states<NPL, VEC>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+    else if (!ENDS && p.h_in) load_states<NPL, VEC>(h, p.h_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    float sum = 0.f, prod[NPL], share[NPL];             // of the steps; of the decays; see STORE_PART
+#pragma unroll
+    for (int i = 0; i < NPL; i++) {
+        prod[i] = 1.f;
+        share[i] = 0.f;
+    }
 
     // the lane's quads of a tile: token xt, channels xc .. xc + 3 of the group
     int xt[XE], xc[XE], bt[BE], bn[BE];
@@ -74,11 +89,12 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
         bn[i] = q % (NP / 4) * 4;
     }
     const T *x = (const T *)p.x + g * p.dpg, *dt = (const T *)p.dt + g * p.dpg;
-    const T *z = p.z && !STORE ? (const T *)p.z + g * p.dpg : nullptr;
+    const T *z = p.z && NEEDC ? (const T *)p.z + g * p.dpg : nullptr;
+    const T *dy = (const T *)p.dy + g * p.dpg;
     const T *B = (const T *)p.B + g * p.N, *C = (const T *)p.C + g * p.N;
     T *y = (T *)p.y + g * p.dpg;
 
-    quad<T> rx[XE], rd[XE], rz[XE], rB[BE], rC[BE];
+    quad<T> rx[XE], rd[XE], rz[XE], ry[XE], rB[BE], rC[BE];
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < XE; i++) {
@@ -86,15 +102,16 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
             rx[i] = load_quad<T, VEC>(x + t * p.x_row, xc[i], p.dpg);
             rd[i] = load_quad<T, VEC>(dt + t * p.dt_row, xc[i], p.dpg);
             if (z) rz[i] = load_quad<T, VEC>(z + t * p.z_row, xc[i], p.dpg);
+            if (MODE == STORE_PART) ry[i] = load_quad<T, VEC>(dy + t * p.dy_row, xc[i], p.dpg);
         }
 #pragma unroll
         for (int i = 0; i < BE; i++) {
             const int64_t t = min(t0 + bt[i], row.t1 - 1);
             rB[i] = load_quad<T, VEC>(B + t * p.B_row, bn[i], p.N);
-            if (!STORE) rC[i] = load_quad<T, VEC>(C + t * p.C_row, bn[i], p.N);
+            if (NEEDC) rC[i] = load_quad<T, VEC>(C + t * p.C_row, bn[i], p.N);
         }
     };
-    const int64_t stored = stored_base(row, kSelStored<NPL>);
+    const int64_t stored = stored_base(row.t0, r, kSelStored);
     if (row.t0 < row.t1) fetch(row.t0);
     for (int t0 = row.t0; t0 < row.t1; t0 += TT) {
         f32x4 xv[XE], zv[XE];
@@ -116,6 +133,16 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                 f32x4 *to = (f32x4 *)&S.u[xt[i]][xc[i] - c0][0];
                 to[0] = u[0];
                 to[1] = u[1];
+                if (MODE == STORE_PART) {                   // r = dy SiLU(z), in y's place
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        v[e] = to_f(ry[i][e]);
+                        if (z) v[e] *= zv[i][e] * sigmoid_hw(zv[i][e]);
+                        v[e] = t0 + xt[i] < row.t1 ? v[e] : 0.f;
+                    }
+                    *(f32x4 *)&S.y[xt[i]][xc[i] - c0] = v;
+                }
             }
         }
 #pragma unroll
@@ -127,10 +154,10 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                     // places behind the last state or token hold zero, whatever lies there
                     const bool in = bn[i] + e < p.N && t0 + bt[i] < row.t1;
                     b[e] = in ? to_f(rB[i][e]) : 0.f;
-                    c[e] = in && !STORE ? to_f(rC[i][e]) : 0.f;
+                    c[e] = in && NEEDC ? to_f(rC[i][e]) : 0.f;
                 }
                 *(f32x4 *)&S.B[bt[i]][bn[i]] = b;
-                if (!STORE) *(f32x4 *)&S.C[bt[i]][bn[i]] = c;
+                if (NEEDC) *(f32x4 *)&S.C[bt[i]][bn[i]] = c;
             }
         }
         wave_lds_fence();
@@ -141,26 +168,35 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
 #pragma unroll
             for (int j = 0; j < LPC; j++) {
                 const int t = tg + j;
-                if (STORE && t % kSelStored<NPL> == 0 && t0 + t < row.t1) {
-                    float *to = p.ckpt + stored_at(stored + (t0 - row.t0 + t) / kSelStored<NPL>, per, gt, wave, lane, NPL);
+                if (CKPT && t % kSelStored == 0 && t0 + t < row.t1) {
+                    const int64_t k = stored + (t0 - row.t0 + t) / kSelStored;
+                    float *to = p.ckpt + stored_at(k, per, gt, wave, lane, NPL);
 #pragma unroll
                     for (int i = 0; i < NPL; i += 4)
                         *(f32x4 *)(to + i * 64) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+                    if (MODE == STORE_PART && sub == 0)
+                        p.ckpt_s[((k * per + gt) * kSelWaves + wave) * CW + ch] = sum;
                 }
                 const float s = S.u[t][ch][0], u = S.u[t][ch][1];
+                const float rr = MODE == STORE_PART ? S.y[t][ch] : 0.f;
+                if (ENDS) sum += s;
                 float acc = 0.f;
 #pragma unroll
                 for (int i = 0; i < NPL; i++) {
                     const float a = __builtin_amdgcn_exp2f(s * A2[i]);
                     h[i] = a * h[i] + u * S.B[t][n0 + i];
-                    if (!STORE) acc += h[i] * S.C[t][n0 + i];
+                    if (MODE == FULL) acc += h[i] * S.C[t][n0 + i];
+                    if (MODE == STORE_PART) {
+                        prod[i] *= a;
+                        share[i] += prod[i] * (rr * S.C[t][n0 + i]);
+                    }
                 }
                 part[j] = acc;
             }
-            if (!STORE) S.y[tg + sub][ch] = transpose_sum<LPC>(part, lane);
+            if (MODE == FULL) S.y[tg + sub][ch] = transpose_sum<LPC>(part, lane);
         }
         wave_lds_fence();
-        if (STORE) continue;
+        if (MODE != FULL) continue;
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const int t = t0 + xt[i];
@@ -176,7 +212,105 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
         }
         wave_lds_fence();
     }
-    if (!STORE && p.h_out && real) store_states<NPL, VEC>(h, p.h_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    if (!real) return;
+    if (MODE == FULL && p.h_out && row.last)
+        store_states<NPL, VEC>(h, p.h_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    if (ENDS) {
+        store_states<NPL, VEC>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+        if (sub == 0) p.seg_s[(int64_t)r * p.dim + d] = sum;
+    }
+    if (MODE == STORE_PART) store_states<NPL, VEC>(share, p.seg_g + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+}
+
+// The segments of a packed batch in the order of their tokens, one at least a sequence; entries behind
+// the last have no sequence. One workgroup.
+constexpr int kSelTabThreads = 256;
+__global__ __launch_bounds__(kSelTabThreads) void k_seltable(SelParams p, int4 *table, int32_t *seq_row) {
+    __shared__ int wsum[kSelTabThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t carry = 0;
+    for (int s0 = 0; s0 < p.nseq; s0 += kSelTabThreads) {
+        const int s = s0 + tid;
+        int a = 0, b = 0, n = 0;
+        if (s < p.nseq) {
+            packed_bounds(p.cu, s, p.total, a, b);
+            n = max(1, (b - a + p.seg_tokens - 1) / p.seg_tokens);
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 63) wsum[wave] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kSelTabThreads / 64; w++) {
+            before += w < wave ? wsum[w] : 0;
+            all += wsum[w];
+        }
+        // (a table whose entries decrease may count more rows than there are: none lies outside)
+        const int64_t first = min(carry + before + incl - n, (int64_t)p.rows);
+        if (s < p.nseq) seq_row[s] = (int)first;
+        for (int k = 0; k < n && first + k < p.rows; k++)
+            table[first + k] = make_int4(a + k * p.seg_tokens, (int)min((int64_t)a + (int64_t)(k + 1) * p.seg_tokens, (int64_t)b),
+                                         s, (k == 0 ? 1 : 0) | (k == n - 1 ? 2 : 0));
+        carry = min(carry + all, (int64_t)p.rows);
+        __syncthreads();
+    }
+    if (tid == 0) seq_row[p.nseq] = (int)carry;
+    for (int64_t r = carry + tid; r < p.rows; r += kSelTabThreads) table[r] = make_int4(0, 0, -1, 0);
+}
+
+// The chain over a sequence's segments, a thread for each channel and state: the state that enters a
+// segment replaces its own end in seg_h, H_{k+1} = exp(A sum_k) H_k + U_k; the gradient that enters it at
+// its end replaces its share in seg_g, G_{k-1} = exp(A sum_k) G_k + V_k from dh_out on. Loads of eight
+// segments are in flight together.
+constexpr int kSelChain = 8;
+__global__ __launch_bounds__(256) void k_selchain(SelParams p, const float *dh_out) {
+    const int64_t dn = (int64_t)p.dim * p.N, blocks = (dn + 255) / 256;
+    const int s = (int)(blockIdx.x / blocks);
+    const int64_t i = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
+    if (i >= dn) return;
+    const int64_t d = i / p.N;
+    const int r0 = p.table ? p.seq_row[s] : s * p.nseg, r1 = p.table ? p.seq_row[s + 1] : r0 + p.nseg;
+    const float A2 = p.A[i] * kLog2e;
+    if (blockIdx.y == 0) {
+        float H = p.h_in ? p.h_in[s * dn + i] : 0.f;
+        for (int r = r0; r < r1; r += kSelChain) {
+            float U[kSelChain], S[kSelChain];
+#pragma unroll
+            for (int k = 0; k < kSelChain; k++) {
+                const int64_t q = min(r + k, r1 - 1);
+                const bool in = r + k < r1 - 1;             // (a last segment's end is not there)
+                U[k] = in ? p.seg_h[q * dn + i] : 0.f;
+                S[k] = in ? p.seg_s[q * p.dim + d] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kSelChain; k++)
+                if (r + k < r1) {
+                    p.seg_h[(int64_t)(r + k) * dn + i] = H;
+                    H = __builtin_amdgcn_exp2f(S[k] * A2) * H + U[k];
+                }
+        }
+    } else {
+        float G = dh_out ? dh_out[s * dn + i] : 0.f;
+        for (int r = r1 - 1; r >= r0; r -= kSelChain) {
+            float V[kSelChain], S[kSelChain];
+#pragma unroll
+            for (int k = 0; k < kSelChain; k++) {
+                const int64_t q = max(r - k, r0);
+                V[k] = p.seg_g[q * dn + i];
+                S[k] = p.seg_s[q * p.dim + d];
+            }
+#pragma unroll
+            for (int k = 0; k < kSelChain; k++)
+                if (r - k >= r0) {
+                    p.seg_g[(int64_t)(r - k) * dn + i] = G;
+                    G = __builtin_amdgcn_exp2f(S[k] * A2) * G + V[k];
+                }
+        }
+    }
 }
 
 // One token: LPC lanes a channel as in the scan; the states stream through once.
@@ -275,35 +409,105 @@ bool sel_vec(const SelParams &p, int64_t es) {
            quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es) && quads(p.z, p.z_row, es) && quads(p.y, p.dim, es);
 }
 
-template <typename T, bool STORE>
-static void scan_go(const SelParams &p0, bool vec, hipStream_t st) {
-    SelParams p = p0;
-#define M3_GO(NPL, LPC)                                                                                        \
-    do {                                                                                                       \
-        p.tiles = (p.dpg + kSelWaves * (64 / LPC) - 1) / (kSelWaves * (64 / LPC));                             \
-        const dim3 grid((uint32_t)p.nseq * p.tiles * p.G);                                                     \
-        if (vec) hipLaunchKernelGGL((k_selscan<T, NPL, LPC, true, STORE>), grid, dim3(64 * kSelWaves), 0, st, p);     \
-        else hipLaunchKernelGGL((k_selscan<T, NPL, LPC, false, STORE>), grid, dim3(64 * kSelWaves), 0, st, p);        \
+template <typename T, int MODE>
+static void scan_go(const SelParams &p, bool vec, hipStream_t st) {
+#define M3_GO(NPL, LPC)                                                                                          \
+    do {                                                                                                         \
+        const dim3 grid((uint32_t)p.rows * p.tiles * p.G);                                                       \
+        if (vec) hipLaunchKernelGGL((k_selscan<T, NPL, LPC, true, MODE>), grid, dim3(64 * kSelWaves), 0, st, p); \
+        else hipLaunchKernelGGL((k_selscan<T, NPL, LPC, false, MODE>), grid, dim3(64 * kSelWaves), 0, st, p);    \
     } while (0)
     M3_SEL_DISPATCH(p.N, M3_GO);
 #undef M3_GO
 }
 
+// A wave's instructions issue every second slot at best when it is alone on its SIMD, so fewer than
+// 1024 waves (one a SIMD) run at less than half the vector unit's rate. Segments cost a first pass of
+// about three quarters of the scan and the chain, and pay below that. They are as long as leave 4096
+// waves, 64 tokens at least. Packed sequences are of unknown lengths, and the longest one decides
+// when nothing else is left to run: they are cut below 4096 waves.
+bool sel_plan(SelParams &p) {
+    int npl, lpc;
+    sel_shape(p.N, npl, lpc);
+    const int cw = kSelWaves * (64 / lpc);
+    p.tiles = (p.dpg + cw - 1) / cw;
+    p.rows = p.nseq;
+    p.nseg = 1;
+    p.seg_tokens = p.seqlen;
+    const int64_t waves = (int64_t)p.tiles * p.G * kSelWaves;
+    if (p.nseq * waves >= (p.cu ? 4096 : 1024)) return false;
+    const int64_t want = (4096 + waves - 1) / waves;                  // segments of the batch
+    int64_t len = ((int64_t)p.total + want - 1) / want;
+    len = std::max<int64_t>((len + 15) / 16 * 16, 64);
+    if (p.cu) {
+        if (len >= p.total) return false;
+        p.rows = (int32_t)(p.nseq + (p.total + len - 1) / len);
+    } else {
+        if (len >= p.seqlen) return false;
+        p.nseg = (int32_t)((p.seqlen + len - 1) / len);
+        p.rows = p.nseq * p.nseg;
+    }
+    p.seg_tokens = (int32_t)len;
+    return true;
+}
+
+static size_t al256(int64_t v) { return (size_t)((v + 255) / 256 * 256); }
+
+size_t sel_segment_bytes(const SelParams &p) {
+    return al256((int64_t)p.rows * p.dim * p.N * 4) + al256((int64_t)p.rows * p.dim * 4) +
+           (p.cu ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0);
+}
+
+void sel_segments(SelParams &p, char *ws) {
+    p.seg_h = (float *)ws;
+    ws += al256((int64_t)p.rows * p.dim * p.N * 4);
+    p.seg_s = (float *)ws;
+    ws += al256((int64_t)p.rows * p.dim * 4);
+    if (p.cu) {
+        p.table = (const int4 *)ws;
+        p.seq_row = (const int32_t *)(ws + al256((int64_t)p.rows * 16));
+    }
+}
+
+void launch_sel_table(const SelParams &p, hipStream_t st) {
+    if (p.table)
+        hipLaunchKernelGGL(k_seltable, dim3(1), dim3(kSelTabThreads), 0, st, p, (int4 *)p.table, (int32_t *)p.seq_row);
+}
+
+void launch_sel_chain(const SelParams &p, const float *dh_out, hipStream_t st) {
+    const int64_t blocks = ((int64_t)p.dim * p.N + 255) / 256;
+    hipLaunchKernelGGL(k_selchain, dim3((uint32_t)(blocks * p.nseq), p.seg_g ? 2 : 1), dim3(256), 0, st, p, dh_out);
+}
+
 mamba3_status launch_selective_scan(const mamba3_selective_scan_args *a, hipStream_t st) {
-    const SelParams p = sel_params(a);
-    if (a->dtype == MAMBA3_F32) scan_go<float, false>(p, sel_vec(p, 4), st);
-    else scan_go<bf16, false>(p, sel_vec(p, 2), st);
+    SelParams p = sel_params(a);
+    const bool segments = sel_plan(p), f32 = a->dtype == MAMBA3_F32, vec = sel_vec(p, f32 ? 4 : 2);
+    if (segments) {
+        sel_segments(p, (char *)a->workspace);
+        launch_sel_table(p, st);
+        if (f32) scan_go<float, PART>(p, vec, st);
+        else scan_go<bf16, PART>(p, vec, st);
+        launch_sel_chain(p, nullptr, st);
+    }
+    if (f32) scan_go<float, FULL>(p, vec, st);
+    else scan_go<bf16, FULL>(p, vec, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 
 size_t selective_workspace_bytes(const mamba3_selective_scan_args *a) {
-    (void)a;
-    return 0;
+    SelParams p = sel_params(a);
+    return sel_plan(p) ? sel_segment_bytes(p) : 0;
 }
 
 void launch_sel_stored(const SelParams &p, int32_t dtype, bool vec, hipStream_t st) {
-    if (dtype == MAMBA3_F32) scan_go<float, true>(p, vec, st);
-    else scan_go<bf16, true>(p, vec, st);
+    const bool f32 = dtype == MAMBA3_F32;
+    if (p.seg_h) {
+        if (f32) scan_go<float, STORE_PART>(p, vec, st);
+        else scan_go<bf16, STORE_PART>(p, vec, st);
+    } else {
+        if (f32) scan_go<float, STORE>(p, vec, st);
+        else scan_go<bf16, STORE>(p, vec, st);
+    }
 }
 
 template <typename T>

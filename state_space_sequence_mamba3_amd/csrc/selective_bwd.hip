@@ -4,10 +4,10 @@
 //   du_t = sum_n g_t B_t,  ds_t = du_t x_t + sum_n g_t a_t h_{t-1} A,   dA = sum_t g_t a_t h_{t-1} s_t
 //   dx_t = du_t s_t + D r_t,  ddt_t = ds_t softplus'(dt_t + bias),  dz_t = dy_t y_t SiLU'(z_t)
 //
-// The forward pass keeps nothing: a first pass (k_selscan's STORE form) writes the state before every
-// kSelStored tokens in fp32 (4 N / 16 bytes a token and channel at N = 16: as much as two bf16 token
-// arrays), and this pass walks those tiles backwards. A tile's states and decays are computed again
-// and stay in registers, 64 of each a lane, while its tokens are taken in reverse. The vector unit
+// The forward pass keeps nothing: a first pass (k_selscan's STORE form) writes the state before every 8
+// tokens in fp32 (N / 2 bytes a token and channel: at N = 16 as much as four bf16 token arrays), and
+// this pass walks those pieces backwards. A piece's states and decays are computed again and stay in
+// registers while its tokens are taken in reverse. The vector unit
 // bounds it: about 20 issue slots for every token, channel and state.
 #include "selective.h"
 
@@ -15,15 +15,12 @@ namespace m3 {
 
 struct SelBwdParams {
     SelParams f;
-    const void *dy;
     const float *dh_out;
     void *dx, *ddt, *dB, *dC, *dz;
     float *dA, *dD, *dbias, *dh_in;
-    int64_t dy_row;
     float *part_bc;     // [G * tiles][total][2][N]: dB and dC of one workgroup's channels
     float *part_a;      // [rows][D][N]
     float *part_d;      // [rows][2][D]: dD, ddt_bias
-    int32_t rows;
 };
 
 template <int NP, int CW, int TT>
@@ -79,12 +76,12 @@ template <int LPC> constexpr int kLow = LPC == 1 ? 0 : LPC == 2 ? 1 : LPC == 4 ?
 // The workgroups and their channels are k_selscan's; its four waves keep step, because dB and dC are
 // summed over them before they leave the workgroup.
 template <typename T, int NPL, int LPC, bool VEC>
-__global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
-    constexpr int CW = 64 / LPC, NP = NPL * LPC, TT = kSelStored<NPL>;
+__global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void k_selbwd(SelBwdParams q) {
+    constexpr int CW = 64 / LPC, NP = NPL * LPC, SUB = kSelStored, TT = 64 / NPL, NSUB = TT / SUB;
     constexpr int XQ = TT * CW / 4, XE = (XQ + 63) / 64;
     constexpr int BQ = TT * NP / 4, BE = (BQ + 63) / 64;
     constexpr int LOW = kLow<LPC>;
-    constexpr int GS = LPC < TT ? LPC : TT;                     // tokens of one transposed sum
+    constexpr int GS = LPC < SUB ? LPC : SUB;                     // tokens of one transposed sum
     constexpr int VT = 2 * NPL;                                 // values a token to sum over channels
     constexpr int TV = (1 << (6 - LOW)) > VT ? (1 << (6 - LOW)) / VT : 1;   // tokens of one channel sum
     constexpr int V = VT * TV;
@@ -96,6 +93,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
     const int rw = blockIdx.x / per, gt = blockIdx.x % per, g = gt / p.tiles;
     const int c0 = ((gt % p.tiles) * kSelWaves + wave) * CW;
     const SelRow row = sel_row(p, rw);
+    if (row.seq < 0) return;
     const int ch = lane / LPC, sub = lane % LPC, n0 = sub * NPL;
     const bool real = c0 + ch < p.dpg;
     const int d = g * p.dpg + min(c0 + ch, p.dpg - 1);
@@ -104,7 +102,13 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
     load_states<NPL, VEC>(A, p.A + (int64_t)d * p.N, n0, p.N);
 #pragma unroll
     for (int i = 0; i < NPL; i++) G[i] = dA[i] = 0.f;
-    if (q.dh_out) load_states<NPL, VEC>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    if (p.seg_g) load_states<NPL, VEC>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
+    else if (q.dh_out) load_states<NPL, VEC>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+
+    float H[NPL];                                               // the state that enters the segment
+#pragma unroll
+    for (int i = 0; i < NPL; i++) H[i] = 0.f;
+    if (p.seg_h) load_states<NPL, VEC>(H, p.seg_h + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
 
     int xt[XE], xc[XE], bt[BE], bn[BE];
     f32x4 biasv[XE], Dv[XE], dDv[XE], dbv[XE];
@@ -128,12 +132,14 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
         bn[i] = k % (NP / 4) * 4;
     }
     const T *x = (const T *)p.x + g * p.dpg, *dt = (const T *)p.dt + g * p.dpg;
-    const T *z = p.z ? (const T *)p.z + g * p.dpg : nullptr, *dy = (const T *)q.dy + g * p.dpg;
+    const T *z = p.z ? (const T *)p.z + g * p.dpg : nullptr, *dy = (const T *)p.dy + g * p.dpg;
     const T *B = (const T *)p.B + g * p.N, *C = (const T *)p.C + g * p.N;
-    const int64_t stored = stored_base(row, TT);
+    const int64_t stored = stored_base(row.t0, rw, SUB);
 
     quad<T> rx[XE], rd[XE], rz[XE], ry[XE], rB[BE], rC[BE];
-    float h0n[NPL];
+    float h0n[NSUB][NPL], s0n[NSUB];
+#pragma unroll
+    for (int b = 0; b < NSUB; b++) s0n[b] = 0.f;
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < XE; i++) {
@@ -141,7 +147,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
             rx[i] = load_quad<T, VEC>(x + t * p.x_row, xc[i], p.dpg);
             rd[i] = load_quad<T, VEC>(dt + t * p.dt_row, xc[i], p.dpg);
             if (z) rz[i] = load_quad<T, VEC>(z + t * p.z_row, xc[i], p.dpg);
-            ry[i] = load_quad<T, VEC>(dy + t * q.dy_row, xc[i], p.dpg);
+            ry[i] = load_quad<T, VEC>(dy + t * p.dy_row, xc[i], p.dpg);
         }
 #pragma unroll
         for (int i = 0; i < BE; i++) {
@@ -149,12 +155,18 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
             rB[i] = load_quad<T, VEC>(B + t * p.B_row, bn[i], p.N);
             rC[i] = load_quad<T, VEC>(C + t * p.C_row, bn[i], p.N);
         }
-        const float *from = p.ckpt + stored_at(stored + (t0 - row.t0) / TT, per, gt, wave, lane, NPL);
 #pragma unroll
-        for (int i = 0; i < NPL; i += 4) {
-            const f32x4 v = *(const f32x4 *)(from + i * 64);
+        for (int b = 0; b < NSUB; b++) {
+            if (t0 + b * SUB >= row.t1) continue;
+            const int64_t k = stored + (t0 - row.t0) / SUB + b;
+            const float *from = p.ckpt + stored_at(k, per, gt, wave, lane, NPL);
+            if (p.seg_h) s0n[b] = p.ckpt_s[((k * per + gt) * kSelWaves + wave) * CW + ch];
 #pragma unroll
-            for (int e = 0; e < 4; e++) h0n[i + e] = v[e];
+            for (int i = 0; i < NPL; i += 4) {
+                const f32x4 v = *(const f32x4 *)(from + i * 64);
+#pragma unroll
+                for (int e = 0; e < 4; e++) h0n[b][i + e] = v[e];
+            }
         }
     };
     const int last = row.t0 + (row.t1 - row.t0 - 1) / TT * TT;   // the last tile's first token
@@ -162,9 +174,12 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
     int buf = 0;
     for (int t0 = last; t0 >= row.t0 && row.t0 < row.t1; t0 -= TT, buf ^= 1) {
         f32x4 xv[XE], zv[XE], ov[XE], rv[XE], sv[XE], gv[XE];   // x, z, dy, r, s, softplus'
-        float h0[NPL];
+        float h0s[NSUB][NPL];
 #pragma unroll
-        for (int i = 0; i < NPL; i++) h0[i] = h0n[i];
+        for (int b = 0; b < NSUB; b++)
+#pragma unroll
+            for (int i = 0; i < NPL; i++)       // a segment's states were stored as from zero
+                h0s[b][i] = p.seg_h ? h0n[b][i] + __builtin_amdgcn_exp2f(s0n[b] * (A[i] * kLog2e)) * H[i] : h0n[b][i];
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const bool in = t0 + xt[i] < row.t1;
@@ -204,77 +219,82 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
         }
         wave_lds_fence();
         if (t0 > row.t0) fetch(t0 - TT);
-        float hs[TT][NPL], as[TT][NPL];
+#pragma unroll 1
+        for (int b0 = NSUB > 1 && t0 + SUB < row.t1 ? SUB : 0; b0 >= 0; b0 -= SUB) {
+            float hs[SUB][NPL], as[SUB][NPL], h0[NPL];
 #pragma unroll
-        for (int tg = 0; tg < TT; tg += GS) {
-            float part[GS];
+            for (int i = 0; i < NPL; i++) h0[i] = b0 ? h0s[NSUB - 1][i] : h0s[0][i];
 #pragma unroll
-            for (int j = 0; j < GS; j++) {
-                const int t = tg + j;
-                const float s = S.u[t][ch][0], u = S.u[t][ch][1];
-                float acc = 0.f;
+            for (int tg = 0; tg < SUB; tg += GS) {
+                float part[GS];
 #pragma unroll
-                for (int i = 0; i < NPL; i++) {
-                    const float a = __builtin_amdgcn_exp2f(s * (A[i] * kLog2e));
-                    as[t][i] = a;
-                    hs[t][i] = a * (t ? hs[t ? t - 1 : 0][i] : h0[i]) + u * S.B[t][n0 + i];
-                    acc += hs[t][i] * S.C[t][n0 + i];
+                for (int j = 0; j < GS; j++) {
+                    const int t = tg + j;
+                    const float s = S.u[b0 + t][ch][0], u = S.u[b0 + t][ch][1];
+                    float acc = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPL; i++) {
+                        const float a = __builtin_amdgcn_exp2f(s * (A[i] * kLog2e));
+                        as[t][i] = a;
+                        hs[t][i] = a * (t ? hs[t ? t - 1 : 0][i] : h0[i]) + u * S.B[b0 + t][n0 + i];
+                        acc += hs[t][i] * S.C[b0 + t][n0 + i];
+                    }
+                    part[j] = acc;
                 }
-                part[j] = acc;
+                float v = transpose_sum<GS>(part, lane);
+                if constexpr (LPC > GS) v += dpp_move<0x128>(v);
+                S.y[b0 + tg + sub % GS][ch] = v;
             }
-            float v = transpose_sum<GS>(part, lane);
-            if constexpr (LPC > GS) v += dpp_move<0x128>(v);
-            S.y[tg + sub % GS][ch] = v;
-        }
 #pragma unroll
-        for (int tg = TT - GS; tg >= 0; tg -= GS) {
-            float pu[GS], ps[GS];
+            for (int tg = SUB - GS; tg >= 0; tg -= GS) {
+                float pu[GS], ps[GS];
 #pragma unroll
-            for (int j = GS - 1; j >= 0; j--) {
-                const int t = tg + j;
-                const float s = S.u[t][ch][0], u = S.u[t][ch][1], r = S.u[t][ch][2];
-                float du = 0.f, ds = 0.f;
+                for (int j = GS - 1; j >= 0; j--) {
+                    const int t = tg + j;
+                    const float s = S.u[b0 + t][ch][0], u = S.u[b0 + t][ch][1], r = S.u[b0 + t][ch][2];
+                    float du = 0.f, ds = 0.f;
 #pragma unroll
-                for (int i = 0; i < NPL; i++) {
-                    G[i] += r * S.C[t][n0 + i];
-                    du += G[i] * S.B[t][n0 + i];
-                    const float ga = G[i] * as[t][i];
-                    const float w = ga * (t ? hs[t ? t - 1 : 0][i] : h0[i]);
-                    dA[i] += w * s;
-                    ds += w * A[i];
-                    as[t][i] = u * G[i];            // dB's share, in the decay's place
-                    hs[t][i] = r * hs[t][i];        // dC's, in the state's
-                    G[i] = ga;
+                    for (int i = 0; i < NPL; i++) {
+                        G[i] += r * S.C[b0 + t][n0 + i];
+                        du += G[i] * S.B[b0 + t][n0 + i];
+                        const float ga = G[i] * as[t][i];
+                        const float w = ga * (t ? hs[t ? t - 1 : 0][i] : h0[i]);
+                        dA[i] += w * s;
+                        ds += w * A[i];
+                        as[t][i] = u * G[i];            // dB's share, in the decay's place
+                        hs[t][i] = r * hs[t][i];        // dC's, in the state's
+                        G[i] = ga;
+                    }
+                    pu[j] = du;
+                    ps[j] = ds;
                 }
-                pu[j] = du;
-                ps[j] = ds;
-            }
-            float v = transpose_sum<GS>(pu, lane), w = transpose_sum<GS>(ps, lane);
-            if constexpr (LPC > GS) {
-                v += dpp_move<0x128>(v);
-                w += dpp_move<0x128>(w);
-            }
-            S.du[tg + sub % GS][ch] = v;
-            S.ds[tg + sub % GS][ch] = w;
-        }
-        // dB and dC: the sum over the wave's channels
-        const bool live = real;
-#pragma unroll
-        for (int tb = 0; tb < TT; tb += TV) {
-            float vals[V];
-#pragma unroll
-            for (int t = 0; t < TV; t++)
-#pragma unroll
-                for (int i = 0; i < NPL; i++) {
-                    vals[t * VT + i] = live ? as[tb + t][i] : 0.f;
-                    vals[t * VT + NPL + i] = live ? hs[tb + t][i] : 0.f;
+                float v = transpose_sum<GS>(pu, lane), w = transpose_sum<GS>(ps, lane);
+                if constexpr (LPC > GS) {
+                    v += dpp_move<0x128>(v);
+                    w += dpp_move<0x128>(w);
                 }
-            channel_sum<V, 5, LOW>(vals, lane);
+                S.du[b0 + tg + sub % GS][ch] = v;
+                S.ds[b0 + tg + sub % GS][ch] = w;
+            }
+            // dB and dC: the sum over the wave's channels
+            const bool live = real;
 #pragma unroll
-            for (int f = 0; f < (V >> (6 - LOW)); f++) {
-                const int k = f << (6 - LOW) | channel_value<LOW>(lane);
-                const int t = tb + k / VT, which = k % VT / NPL, i = k % NPL;
-                S.bc[buf][t][which][n0 + i] = vals[f];
+            for (int tb = 0; tb < SUB; tb += TV) {
+                float vals[V];
+#pragma unroll
+                for (int t = 0; t < TV; t++)
+#pragma unroll
+                    for (int i = 0; i < NPL; i++) {
+                        vals[t * VT + i] = live ? as[tb + t][i] : 0.f;
+                        vals[t * VT + NPL + i] = live ? hs[tb + t][i] : 0.f;
+                    }
+                channel_sum<V, 5, LOW>(vals, lane);
+#pragma unroll
+                for (int f = 0; f < (V >> (6 - LOW)); f++) {
+                    const int k = f << (6 - LOW) | channel_value<LOW>(lane);
+                    const int t = b0 + tb + k / VT, which = k % VT / NPL, i = k % NPL;
+                    S.bc[buf][t][which][n0 + i] = vals[f];
+                }
             }
         }
         __syncthreads();
@@ -313,7 +333,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selbwd(SelBwdParams q) {
     }
     if (real) {
         store_states<NPL, VEC>(dA, q.part_a + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
-        if (q.dh_in) store_states<NPL, VEC>(G, q.dh_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+        if (q.dh_in && row.first) store_states<NPL, VEC>(G, q.dh_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
     }
     // dD and ddt_bias: the sum over the lanes that hold the same channels (token lanes), in LDS
     __syncthreads();
@@ -343,19 +363,23 @@ __global__ __launch_bounds__(256) void k_selbwd_reduce(SelBwdParams q, int bc_bl
         if (i >= n) return;
         const int64_t each = (int64_t)p.total * 2 * p.N, g = i / each, o = i % each;
         float s = 0.f;
+#pragma unroll 8
         for (int k = 0; k < p.tiles; k++) s += q.part_bc[(g * p.tiles + k) * each + o];
         const int64_t t = o / (2 * p.N), which = o / p.N % 2, m = o % p.N;
         ((T *)(which ? q.dC : q.dB))[(t * p.G + g) * p.N + m] = from_f<T>(s);
         return;
     }
     const int64_t i = (int64_t)(blockIdx.x - bc_blocks) * 256 + threadIdx.x, dn = (int64_t)p.dim * p.N;
+    const int rows = p.table ? p.seq_row[p.nseq] : p.rows;     // (the table's rows behind hold nothing)
     float s = 0.f;
     if (i < dn) {
-        for (int r = 0; r < q.rows; r++) s += q.part_a[r * dn + i];
+#pragma unroll 8
+        for (int r = 0; r < rows; r++) s += q.part_a[r * dn + i];
         q.dA[i] = s;
     } else if (i < dn + 2 * p.dim) {
         const int64_t k = i - dn;
-        for (int r = 0; r < q.rows; r++) s += q.part_d[(int64_t)r * 2 * p.dim + k];
+#pragma unroll 8
+        for (int r = 0; r < rows; r++) s += q.part_d[(int64_t)r * 2 * p.dim + k];
         if (k < p.dim) {
             if (q.dD) q.dD[k] = s;
         } else if (q.dbias) {
@@ -367,24 +391,22 @@ __global__ __launch_bounds__(256) void k_selbwd_reduce(SelBwdParams q, int bc_bl
 namespace {
 
 struct SelWs {
-    size_t ckpt, bc, a, d, total;
-    int tiles;
+    size_t seg, seg_g, ckpt, ckpt_s, bc, a, d, total;
 };
-SelWs sel_ws(const SelParams &p) {
+SelWs sel_ws(const SelParams &p, bool segments) {
     SelWs w{};
-    int npl = 4, lpc = 1;
-#define M3_GO(NPL, LPC) npl = NPL, lpc = LPC
-    M3_SEL_DISPATCH(p.N, M3_GO);
-#undef M3_GO
-    const int cw = kSelWaves * (64 / lpc);
-    w.tiles = (p.dpg + cw - 1) / cw;
-    const int64_t per = (int64_t)w.tiles * p.G, every = 64 / npl;
+    int npl, lpc;
+    sel_shape(p.N, npl, lpc);
+    const int64_t per = (int64_t)p.tiles * p.G, stored = p.total / kSelStored + p.rows;
     auto al = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
     size_t o = 0;
-    w.ckpt = o; o += al((p.total / every + p.nseq) * per * kSelWaves * 64 * npl * 4);
+    w.seg = o; o += segments ? sel_segment_bytes(p) : 0;
+    w.seg_g = o; o += segments ? al((int64_t)p.rows * p.dim * p.N * 4) : 0;
+    w.ckpt = o; o += al(stored * per * kSelWaves * 64 * npl * 4);
+    w.ckpt_s = o; o += segments ? al(stored * per * kSelWaves * (64 / lpc) * 4) : 0;
     w.bc = o; o += al(per * p.total * 2 * p.N * 4);
-    w.a = o; o += al((int64_t)p.nseq * p.dim * p.N * 4);
-    w.d = o; o += al((int64_t)p.nseq * 2 * p.dim * 4);
+    w.a = o; o += al((int64_t)p.rows * p.dim * p.N * 4);
+    w.d = o; o += al((int64_t)p.rows * 2 * p.dim * 4);
     w.total = o;
     return w;
 }
@@ -394,11 +416,11 @@ void bwd_go(SelBwdParams &q, bool vec, hipStream_t st) {
     SelParams &p = q.f;
 #define M3_GO(NPL, LPC)                                                                                             \
     do {                                                                                                            \
-        const dim3 grid((uint32_t)q.rows * p.tiles * p.G);                                                          \
+        const dim3 grid((uint32_t)p.rows * p.tiles * p.G);                                                          \
         if (vec) hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, true>), grid, dim3(64 * kSelWaves), 0, st, q);           \
         else hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, false>), grid, dim3(64 * kSelWaves), 0, st, q);              \
     } while (0)
-    if (q.rows > 0) M3_SEL_DISPATCH(p.N, M3_GO);
+    if (p.rows > 0) M3_SEL_DISPATCH(p.N, M3_GO);
 #undef M3_GO
     const int64_t bc = ((int64_t)p.total * p.G * 2 * p.N + 255) / 256, a = ((int64_t)p.dim * (p.N + 2) + 255) / 256;
     hipLaunchKernelGGL((k_selbwd_reduce<T>), dim3((uint32_t)(bc + a)), dim3(256), 0, st, q, (int)bc);
@@ -407,7 +429,9 @@ void bwd_go(SelBwdParams &q, bool vec, hipStream_t st) {
 }  // namespace
 
 size_t selective_bwd_workspace_bytes(const mamba3_selective_scan_bwd_args *b) {
-    return sel_ws(sel_params(&b->fwd)).total;
+    SelParams p = sel_params(&b->fwd);
+    const bool segments = sel_plan(p);
+    return sel_ws(p, segments).total;
 }
 
 mamba3_status launch_selective_scan_bwd(const mamba3_selective_scan_bwd_args *b, hipStream_t st) {
@@ -416,22 +440,31 @@ mamba3_status launch_selective_scan_bwd(const mamba3_selective_scan_bwd_args *b,
     SelParams &p = q.f;
     p.y = nullptr;
     p.h_out = nullptr;
-    const SelWs w = sel_ws(p);
+    const bool segments = sel_plan(p);
+    const SelWs w = sel_ws(p, segments);
     char *ws = (char *)b->workspace;
-    p.tiles = w.tiles;
+    if (segments) {
+        sel_segments(p, ws + w.seg);
+        p.seg_g = (float *)(ws + w.seg_g);
+        p.ckpt_s = (float *)(ws + w.ckpt_s);
+    }
     p.ckpt = (float *)(ws + w.ckpt);
     q.part_bc = (float *)(ws + w.bc);
     q.part_a = (float *)(ws + w.a);
     q.part_d = (float *)(ws + w.d);
-    q.dy = b->dy; q.dh_out = b->dh_out;
-    q.dy_row = b->dy_row ? b->dy_row : p.dim;
+    p.dy = b->dy;
+    p.dy_row = b->dy_row ? b->dy_row : p.dim;
+    q.dh_out = b->dh_out;
     q.dx = b->dx; q.ddt = b->ddt; q.dB = b->dB; q.dC = b->dC; q.dz = b->dz;
     q.dA = b->dA; q.dD = b->dD; q.dbias = b->ddt_bias; q.dh_in = b->dh_in;
-    q.rows = p.nseq;
     const int64_t es = b->fwd.dtype == MAMBA3_BF16 ? 2 : 4;
     auto quads = [&](const void *a, int64_t row) { return ((uintptr_t)a % (4 * es)) == 0 && row % 4 == 0; };
-    const bool vec = sel_vec(p, es) && quads(q.dy, q.dy_row) && quads(q.dx, 0) && quads(q.ddt, 0) && quads(q.dz, 0);
-    if (q.rows > 0) launch_sel_stored(p, b->fwd.dtype, vec, st);
+    const bool vec = sel_vec(p, es) && quads(p.dy, p.dy_row) && quads(q.dx, 0) && quads(q.ddt, 0) && quads(q.dz, 0);
+    if (p.rows > 0) {
+        launch_sel_table(p, st);
+        launch_sel_stored(p, b->fwd.dtype, vec, st);
+        if (segments) launch_sel_chain(p, b->dh_out, st);
+    }
     if (b->fwd.dtype == MAMBA3_F32) bwd_go<float>(q, vec, st);
     else bwd_go<bf16>(q, vec, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;

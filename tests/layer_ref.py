@@ -40,6 +40,13 @@ def dsilu(v):
     return s + v * s * (1 - s)
 
 
+def dsilu_terms(v):
+    """The size of the terms that dsilu adds: near v = -1.278 they cancel, and a computed dsilu is off by
+    roundings of s and |v| s (1 - s), not of their difference."""
+    s = 1 / (1 + torch.exp(-v))
+    return s + v.abs() * s * (1 - s)
+
+
 def spans(lead, cu):
     """[(first, last)] of the sequences in token rows laid end to end."""
     b, L = lead
@@ -67,7 +74,7 @@ def conv(x, w, bias, act, conv_in, cu, dy=None, dconv_out=None, mag=False):
             if dy is not None:
                 e = f(dy.reshape(-1, D)[a + t])
                 if act:     # SiLU'' is at most 0.5: an error of p moves e by as much
-                    e = e * (dsilu(tp).abs() + 0.5 * p) if mag else e * dsilu(tp)
+                    e = e * (dsilu_terms(tp) + 0.5 * p) if mag else e * dsilu(tp)
                 db += e
                 for j in range(W):
                     dw[:, j] += e * h[t + j]
@@ -121,7 +128,7 @@ def scan(x, dt, A, B, C, D, z, bias, softplus, h_in, cu, dy=None, dh_out=None, m
             r = f(nd[t] * silu(zd[t])) if zd is not None else f(nd[t])
             g = g + r[:, None] * fC[t][of]
             if zd is not None:
-                out["dz"][t] = f(nd[t] * dsilu(zd[t])) * yt
+                out["dz"][t] = (nd[t].abs() * dsilu_terms(zd[t]) if mag else nd[t] * dsilu(zd[t])) * yt
             out["dC"][t] = (r[:, None] * ht).view(G, -1, N).sum(1)
             out["dB"][t] = (g * (sf[t] * fx[t])[:, None]).view(G, -1, N).sum(1)
             gb = (g * fB[t][of]).sum(-1)

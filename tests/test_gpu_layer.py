@@ -102,6 +102,10 @@ SCAN = [  # batch, seqlen, dim, N, G, cu
     (1, 31, 12, 128, 1, None), (1, 29, 15, 7, 3, None), (1, 23, 10, 50, 2, None), (1, 20, 6, 100, 2, None),
     (1, 90, 72, 16, 1, [0, 0, 1, 3, 3, 40, 41, 90, 90]), (1, 34, 9, 13, 1, [0, 17, 17, 34]),
     (1, 0, 8, 16, 1, [0, 0, 0]), (2, 0, 8, 16, 1, None),
+    # long enough to run as segments, and enough sequences not to
+    (1, 300, 40, 16, 1, None), (3, 200, 9, 16, 1, None), (2, 129, 36, 24, 2, None), (1, 150, 8, 128, 1, None),
+    (1, 400, 20, 16, 1, [0, 0, 64, 65, 65, 300, 399, 400]), (1, 333, 6, 5, 2, [0, 200, 333]),
+    (64, 70, 256, 16, 1, None),
 ]
 
 
