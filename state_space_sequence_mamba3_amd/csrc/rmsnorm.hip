@@ -229,90 +229,153 @@ __global__ __launch_bounds__(256) void k_norm(NormParams p) {
     }
 }
 
-// Backward: as the forward; a workgroup walks several rows, so that dweight's partial sums stay in
-// registers (NCH = 0: dweight's columns are added by k_norm_dw).
-template <typename T, typename RT, int WPR, int NCH, bool VEC>
-__global__ __launch_bounds__(256) void k_norm_bwd(NormParams p) {
-    __shared__ float red[4];
+// 8 values as loaded, converted where they are used: the next row's loads are in flight while a row is
+// worked on.
+template <typename T> struct Raw8 { typedef T type __attribute__((ext_vector_type(8), aligned(16))); };
+template <typename T, bool VEC>
+__device__ __forceinline__ typename Raw8<T>::type raw8(const T *row, int c, int n) {
+    typename Raw8<T>::type v;
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = from_f<T>(0.f);
+    if constexpr (VEC) {
+        if (c < n) v = *(const typename Raw8<T>::type *)(row + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (c + e < n) v[e] = row[c + e];
+    }
+    return v;
+}
+// Two sums over the waves of a row, with one barrier: `red` is the row's half of two, used in turn.
+template <int WPR>
+__device__ __forceinline__ void row_sums(float &a, float &b, float2 *red) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (WPR > 1) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; i++) {
+            a += red[i].x;
+            b += red[i].y;
+        }
+    }
+}
+
+// Backward. WPR waves share a row, 8 values a lane (1, 4, 8 or 16 waves: rows of up to 512, 2048, 4096
+// and 8192 values; WPR = 1: four rows a workgroup); a workgroup walks several rows, so that dweight's
+// partial sums stay in registers. LONG: rows of any length, read twice, and k_norm_dw for dweight.
+template <typename T, typename RT, int WPR, bool LONG, bool VEC>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_norm_bwd(NormParams p) {
     constexpr int STEP = WPR * 64 * kNV;
-    const int t = WPR == 4 ? threadIdx.x : threadIdx.x & 63;
-    const int64_t first = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t step = (int64_t)gridDim.x * (4 / WPR);
-    const int nch = NCH ? NCH : (p.dim + STEP - 1) / STEP;
-    float dw[NCH ? NCH : 1][kNV];
+    __shared__ float2 red[2][WPR];
+    __shared__ float4 join[WPR == 1 ? 2 * 256 : 1];
+    const int t = WPR > 1 ? threadIdx.x : threadIdx.x & 63;
+    const int64_t first = WPR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t step = (int64_t)gridDim.x * (WPR > 1 ? 1 : 4);
+    const int nch = LONG ? (p.dim + STEP - 1) / STEP : 1;
+    typename Raw8<RT>::type rs, rr;
+    typename Raw8<T>::type rd;
+    auto fetch = [&](int64_t row, int i) {
+        const int c = i * STEP + t * kNV;
+        rs = raw8<RT, VEC>((const RT *)p.x + row * p.dim, c, p.dim);
+        rd = raw8<T, VEC>((const T *)p.dy + row * p.dy_row, c, p.dim);
+        if (p.dres) rr = raw8<RT, VEC>((const RT *)p.dres + row * p.dim, c, p.dim);
+    };
+    float w[kNV], dw[kNV];
+    auto weigh = [&](int i) {
+        if (p.w) {
+            load8<float, VEC>(w, p.w, i * STEP + t * kNV, p.dim);
+        } else {
 #pragma unroll
-    for (int i = 0; i < (NCH ? NCH : 1); i++)
+            for (int e = 0; e < kNV; e++) w[e] = 1.f;
+        }
+    };
+    weigh(0);
 #pragma unroll
-        for (int e = 0; e < kNV; e++) dw[i][e] = 0.f;
-    for (int64_t row = first; row < p.rows; row += step) {
-        const RT *s = (const RT *)p.x + row * p.dim;
-        const T *dy = (const T *)p.dy + row * p.dy_row;
-        float ks[NCH ? NCH : 1][kNV], kd[NCH ? NCH : 1][kNV];
+    for (int e = 0; e < kNV; e++) dw[e] = 0.f;
+    if (!LONG && first < p.rows) fetch(first, 0);
+    int turn = 0;
+    for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
+        float ks[kNV], kd[kNV], kr[kNV];
         float ss = 0.f, sd = 0.f;
-        auto fetch = [&](int c, float (&a)[kNV], float (&b)[kNV]) {   // s and dy
-            load8<RT, VEC>(a, s, c, p.dim);
-            load8<T, VEC>(b, dy, c, p.dim);
-        };
-        auto weigh = [&](int c, float (&w)[kNV]) {
-            if (p.w) {
-                load8<float, VEC>(w, p.w, c, p.dim);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kNV; e++) w[e] = 1.f;
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < nch; i++) {
-            const int c = i * STEP + t * kNV, k = NCH ? i : 0;
-            float w[kNV];
-            fetch(c, ks[k], kd[k]);
-            weigh(c, w);
+        auto unpack = [&]() {
 #pragma unroll
             for (int e = 0; e < kNV; e++) {
-                ss += ks[k][e] * ks[k][e];
-                sd += ks[k][e] * (c + e < p.dim ? w[e] * kd[k][e] : 0.f);
+                ks[e] = to_f(rs[e]);
+                kd[e] = to_f(rd[e]);
+                kr[e] = p.dres ? to_f(rr[e]) : 0.f;
+            }
+        };
+        for (int i = 0; i < nch; i++) {
+            if (LONG) {
+                fetch(row, i);
+                weigh(i);
+            }
+            unpack();
+#pragma unroll
+            for (int e = 0; e < kNV; e++) {
+                ss += ks[e] * ks[e];
+                sd += ks[e] * w[e] * kd[e];
             }
         }
-        const float r = __builtin_amdgcn_rsqf(row_sum<WPR>(ss, red) / (float)p.dim + p.eps);
-        const float m = row_sum<WPR>(sd, red) / (float)p.dim * r * r * r;   // ds = r w dy - m s
-        if (NCH == 0 && t == 0 && p.part) p.part[row] = r;
-#pragma unroll
+        if (!LONG && row + step < p.rows) fetch(row + step, 0);
+        row_sums<WPR>(ss, sd, red[turn]);
+        const float r = __builtin_amdgcn_rsqf(ss / (float)p.dim + p.eps);
+        const float m = sd / (float)p.dim * r * r * r;                      // ds = r w dy - m s
+        if (LONG && t == 0 && p.part) p.part[row] = r;
         for (int i = 0; i < nch; i++) {
-            const int c = i * STEP + t * kNV, k = NCH ? i : 0;
-            float w[kNV], o[kNV];
-            if constexpr (NCH == 0) fetch(c, ks[0], kd[0]);
-            weigh(c, w);
-            if (p.dres) load8<RT, VEC>(o, (const RT *)p.dres + row * p.dim, c, p.dim);
+            const int c = i * STEP + t * kNV;
+            float o[kNV];
+            if (LONG) {
+                fetch(row, i);
+                weigh(i);
+                unpack();
+            }
 #pragma unroll
             for (int e = 0; e < kNV; e++) {
-                o[e] = (p.dres ? o[e] : 0.f) + (r * w[e] * kd[k][e] - m * ks[k][e]);
-                if constexpr (NCH > 0) dw[k][e] += kd[k][e] * ks[k][e] * r;
+                o[e] = kr[e] + (r * w[e] * kd[e] - m * ks[e]);
+                if (!LONG) dw[e] += kd[e] * ks[e] * r;
             }
             if (p.res_out) store8<RT, VEC>((RT *)p.res_out + row * p.dim, c, p.dim, o);
             if (p.dx) store8<T, VEC>((T *)p.dx + row * p.dim, c, p.dim, o);
         }
     }
-    if constexpr (NCH > 0) {
-        if (p.part) {
-            // one row of partial sums a workgroup (WPR = 4) or a wave (WPR = 1)
-            float *out = p.part + (WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * p.dim;
+    if (LONG || !p.part) return;
+    // one row of partial sums a workgroup: with a wave a row, those of its four waves in order
+    if constexpr (WPR == 1) {
+        join[2 * threadIdx.x] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+        join[2 * threadIdx.x + 1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+        __syncthreads();
+        if (threadIdx.x >= 64) return;
 #pragma unroll
-            for (int i = 0; i < NCH; i++) store8<float, VEC>(out, i * STEP + t * kNV, p.dim, dw[i]);
+        for (int v = 1; v < 4; v++) {
+            const float4 a = join[2 * (t + 64 * v)], b = join[2 * (t + 64 * v) + 1];
+            dw[0] += a.x; dw[1] += a.y; dw[2] += a.z; dw[3] += a.w;
+            dw[4] += b.x; dw[5] += b.y; dw[6] += b.z; dw[7] += b.w;
         }
     }
+    store8<float, VEC>(p.part + (int64_t)blockIdx.x * p.dim, t * kNV, p.dim, dw);
 }
 
-// dweight from `n` rows of partial sums: 64 columns a workgroup, 4 waves over the rows.
-__global__ __launch_bounds__(256) void k_norm_reduce(const float *part, int64_t n, int dim, float *dw) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+// dweight from `n` rows of partial sums: 16 columns a workgroup, 16 threads over the rows of each.
+__global__ __launch_bounds__(256) void k_norm_reduce(const float *part, int n, int dim, float *dw) {
+    __shared__ float red[16][17];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, c = blockIdx.x * 16 + x;
     float s = 0.f;
-    if (c < dim)
-        for (int64_t i = wave; i < n; i += 4) s += part[i * dim + c];
-    red[wave][lane] = s;
+    if (c < dim) {
+#pragma unroll 8
+        for (int i = y; i < n; i += 16) s += part[(int64_t)i * dim + c];
+    }
+    red[y][x] = s;
     __syncthreads();
-    if (wave == 0 && c < dim) dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (y == 0 && c < dim) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) s += red[i][x];
+        dw[c] = s;
+    }
 }
 
 // dweight of long rows: 64 columns a workgroup over all rows, with the rows' 1 / rms from k_norm_bwd.
@@ -338,41 +401,53 @@ bool wide(const void *q, int64_t row, int64_t es) { return ((uintptr_t)q & 15u) 
 // row spread few rows over more of the GPU.
 bool one_wave(int64_t rows, int dim) { return dim <= 512 || (dim <= 2048 && rows >= 2048); }
 
-constexpr int kBwdBlocks = 1024;
-
-int64_t bwd_parts(int64_t rows, int dim) {   // rows of partial sums
-    if (dim > 8192) return 0;
-    return one_wave(rows, dim) ? 4 * std::min<int64_t>((rows + 3) / 4, kBwdBlocks) : std::min<int64_t>(rows, kBwdBlocks);
+// The backward's waves a row, and its workgroups: 16 waves a CU for all (each workgroup leaves a row of
+// partial sums).
+int bwd_waves(int dim) { return dim <= 512 ? 1 : dim <= 2048 ? 4 : dim <= 4096 ? 8 : dim <= 8192 ? 16 : 4; }
+int64_t bwd_blocks(int64_t rows, int dim) {
+    const int w = bwd_waves(dim);
+    return std::min<int64_t>(w == 1 ? (rows + 3) / 4 : rows, w <= 4 ? 1024 : 4096 / w);
 }
 
 template <typename T, typename RT, int WPR, int NCH>
-void norm_launch(const NormParams &p, bool vec, bool back, hipStream_t st) {
-    const int64_t per = 4 / WPR, blocks = (p.rows + per - 1) / per;
-    const dim3 grid((uint32_t)(back ? std::min<int64_t>(blocks, kBwdBlocks) : blocks));
-    if (back) {
-        if (vec) hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, NCH, true>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, NCH, false>), grid, dim3(256), 0, st, p);
-    } else {
-        if (vec) hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, true>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, false>), grid, dim3(256), 0, st, p);
-    }
+void norm_launch(const NormParams &p, bool vec, hipStream_t st) {
+    const int64_t per = 4 / WPR;
+    const dim3 grid((uint32_t)((p.rows + per - 1) / per));
+    if (vec) hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, true>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((k_norm<T, RT, WPR, NCH, false>), grid, dim3(256), 0, st, p);
 }
 
 template <typename T, typename RT>
-void norm_go(const NormParams &p, bool vec, bool back, hipStream_t st) {
+void norm_go(const NormParams &p, bool vec, hipStream_t st) {
     if (one_wave(p.rows, p.dim)) {
-        if (p.dim <= 512) norm_launch<T, RT, 1, 1>(p, vec, back, st);
-        else if (p.dim <= 1024) norm_launch<T, RT, 1, 2>(p, vec, back, st);
-        else norm_launch<T, RT, 1, 4>(p, vec, back, st);
+        if (p.dim <= 512) norm_launch<T, RT, 1, 1>(p, vec, st);
+        else if (p.dim <= 1024) norm_launch<T, RT, 1, 2>(p, vec, st);
+        else norm_launch<T, RT, 1, 4>(p, vec, st);
     } else if (p.dim <= 2048) {
-        norm_launch<T, RT, 4, 1>(p, vec, back, st);
+        norm_launch<T, RT, 4, 1>(p, vec, st);
     } else if (p.dim <= 4096) {
-        norm_launch<T, RT, 4, 2>(p, vec, back, st);
+        norm_launch<T, RT, 4, 2>(p, vec, st);
     } else if (p.dim <= 8192) {
-        norm_launch<T, RT, 4, 4>(p, vec, back, st);
+        norm_launch<T, RT, 4, 4>(p, vec, st);
     } else {
-        norm_launch<T, RT, 4, 0>(p, vec, back, st);
+        norm_launch<T, RT, 4, 0>(p, vec, st);
     }
+}
+
+template <typename T, typename RT, int WPR, bool LONG>
+void bwd_launch(const NormParams &p, bool vec, hipStream_t st) {
+    const dim3 grid((uint32_t)bwd_blocks(p.rows, p.dim)), block(WPR == 1 ? 256 : 64 * WPR);
+    if (vec) hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, LONG, true>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((k_norm_bwd<T, RT, WPR, LONG, false>), grid, block, 0, st, p);
+}
+
+template <typename T, typename RT>
+void norm_bwd_go(const NormParams &p, bool vec, hipStream_t st) {
+    if (p.dim > 8192) bwd_launch<T, RT, 4, true>(p, vec, st);
+    else if (p.dim <= 512) bwd_launch<T, RT, 1, false>(p, vec, st);
+    else if (p.dim <= 2048) bwd_launch<T, RT, 4, false>(p, vec, st);
+    else if (p.dim <= 4096) bwd_launch<T, RT, 8, false>(p, vec, st);
+    else bwd_launch<T, RT, 16, false>(p, vec, st);
 }
 
 template <typename T, typename RT>
@@ -395,16 +470,16 @@ mamba3_status launch_rmsnorm(const mamba3_rmsnorm_args *a, hipStream_t st) {
     p.eps = a->eps;
     const bool vec = a->dim % 8 == 0 && wide(p.x, p.x_row, es) && wide(p.res, p.dim, rs) && wide(p.w, p.dim, 4) &&
                      wide(p.res_out, p.dim, rs) && wide(p.y, p.dim, es) && ((uintptr_t)p.q & 7u) == 0;
-    if (a->dtype == MAMBA3_F32) norm_go<float, float>(p, vec, false, st);
-    else if (a->residual_dtype == MAMBA3_F32) norm_go<bf16, float>(p, vec, false, st);
-    else norm_go<bf16, bf16>(p, vec, false, st);
+    if (a->dtype == MAMBA3_F32) norm_go<float, float>(p, vec, st);
+    else if (a->residual_dtype == MAMBA3_F32) norm_go<bf16, float>(p, vec, st);
+    else norm_go<bf16, bf16>(p, vec, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 
 size_t rmsnorm_bwd_workspace_bytes(const mamba3_rmsnorm_bwd_args *b) {
     if (!b->dweight) return 0;
     // rows longer than the registers leave their 1 / rms instead
-    return (size_t)(b->dim > 8192 ? b->rows * 4 : bwd_parts(b->rows, b->dim) * b->dim * 4);
+    return (size_t)(b->dim > 8192 ? b->rows * 4 : bwd_blocks(b->rows, b->dim) * b->dim * 4);
 }
 
 mamba3_status launch_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *b, hipStream_t st) {
@@ -418,14 +493,14 @@ mamba3_status launch_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *b, hipStream_t s
     const bool vec = b->dim % 8 == 0 && wide(p.x, p.dim, rs) && wide(p.dy, p.dy_row, es) && wide(p.dres, p.dim, rs) &&
                      wide(p.w, p.dim, 4) && wide(p.res_out, p.dim, rs) && wide(p.dx, p.dim, es);
     if (p.rows > 0) {
-        if (b->dtype == MAMBA3_F32) norm_go<float, float>(p, vec, true, st);
-        else if (b->residual_dtype == MAMBA3_F32) norm_go<bf16, float>(p, vec, true, st);
-        else norm_go<bf16, bf16>(p, vec, true, st);
+        if (b->dtype == MAMBA3_F32) norm_bwd_go<float, float>(p, vec, st);
+        else if (b->residual_dtype == MAMBA3_F32) norm_bwd_go<bf16, float>(p, vec, st);
+        else norm_bwd_go<bf16, bf16>(p, vec, st);
     }
     if (b->dweight) {
         if (b->dim <= 8192) {
-            hipLaunchKernelGGL(k_norm_reduce, dim3((b->dim + 63) / 64), dim3(256), 0, st, p.part,
-                               bwd_parts(b->rows, b->dim), b->dim, b->dweight);
+            hipLaunchKernelGGL(k_norm_reduce, dim3((b->dim + 15) / 16), dim3(256), 0, st, p.part,
+                               (int)bwd_blocks(b->rows, b->dim), b->dim, b->dweight);
         } else if (b->dtype == MAMBA3_F32) {
             dw_go<float, float>(p, st);
         } else if (b->residual_dtype == MAMBA3_F32) {
