@@ -208,9 +208,103 @@ __device__ __forceinline__ void conv_state_grad(const ConvParams &p, int64_t i) 
     ((T *)p.dconv_in)[i] = from_f<T>(g);
 }
 
-// The backward walks the same tokens plus W - 1 behind them: with e_t = dy_t act'(p_t),
+// The backward walks kTokBwd tokens plus the W - 1 behind them: with e_t = dy_t act'(p_t),
 // dx_tau = sum_j w[j] e_{tau + W - 1 - j}, so dx of a token is complete W - 1 tokens later and waits
-// in registers until then. dweight's and dbias' sums over a workgroup's tokens go to `part`.
+// in registers until then. dweight's and dbias' sums over a workgroup's tokens go to `part`. Four
+// channels a thread (8 bytes of bf16) leave three waves a SIMD. Tokens are taken in fours whose loads are in flight while
+// the four before are worked on; INSIDE: the walk and its W - 1 neighbours on both sides lie in one
+// sequence, which leaves no branch in it.
+constexpr int kTokBwd = 32;
+
+template <typename T, int W, int V>
+struct ConvWalk {
+    typedef typename RawVec<T, V>::type raw;
+    float w[W][V], bias[V], win[W][V], pend[W][V];   // pend[j]: dx of token t - W + 1 + j so far
+    float dw[W][V], db[V];
+
+    template <bool INSIDE>
+    __device__ __forceinline__ void run(const ConvParams &p, SeqAt q, int t0, int t1, int c) {
+        constexpr int U = 4;
+        const T *x = (const T *)p.x + c, *dy = (const T *)p.dy + c;
+        const int end = t1 + W - 1;
+        raw rx[U], rd[U];
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int64_t k = min(t + u, p.total - 1);
+                rx[u] = *(const raw *)(x + k * p.x_row);
+                rd[u] = *(const raw *)(dy + k * p.dy_row);
+            }
+        };
+        fetch(t0);
+        for (int tb = t0; tb < end; tb += U) {
+            raw cx[U], cd[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                cx[u] = rx[u];
+                cd[u] = rd[u];
+            }
+            if (tb + U < end) fetch(tb + U);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int t = tb + u;
+                if (t >= end) break;
+                float e_t[V];
+#pragma unroll
+                for (int e = 0; e < V; e++) {
+#pragma unroll
+                    for (int j = 0; j + 1 < W; j++) pend[j][e] = pend[j + 1][e];
+                    pend[W - 1][e] = 0.f;
+                }
+                if (INSIDE || t < p.total) {
+                    if (!INSIDE && t >= q.b) {
+                        next_seq(p, t, q);
+#pragma unroll
+                        for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; e++) {
+#pragma unroll
+                        for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
+                        win[W - 1][e] = raw_f<T, V>(cx[u], e);
+                        e_t[e] = raw_f<T, V>(cd[u], e);
+                        if (p.silu) {
+                            float v = bias[e];
+#pragma unroll
+                            for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
+                            e_t[e] *= silu_grad(v);
+                        }
+                    }
+                    const int pos = t - q.a;
+#pragma unroll
+                    for (int j = 0; j < W; j++)
+                        if (INSIDE || pos >= W - 1 - j) {     // tap j's input is a token of this sequence
+#pragma unroll
+                            for (int e = 0; e < V; e++) pend[j][e] += w[j][e] * e_t[e];
+                        }
+                    if (t < t1) {
+#pragma unroll
+                        for (int e = 0; e < V; e++) {
+                            db[e] += e_t[e];
+#pragma unroll
+                            for (int j = 0; j < W; j++) dw[j][e] += e_t[e] * win[j][e];
+                        }
+                        const int k = t - q.b + (W - 1);      // the token's row of conv_out, if it has one
+                        if (!INSIDE && p.dconv_out && k >= 0) {
+                            float o[V];
+                            load_vec<T, V>(o, (const T *)p.dconv_out + ((int64_t)q.s * (W - 1) + k) * p.dim + c);
+#pragma unroll
+                            for (int e = 0; e < V; e++) pend[W - 1][e] += o[e];
+                        }
+                    }
+                }
+                const int tau = t - (W - 1);
+                if (tau >= t0) store_vec<T, V>((T *)p.dx + (int64_t)tau * p.dim + c, pend[0]);
+            }
+        }
+    }
+};
+
 template <typename T, int W, int V>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
     if ((int)blockIdx.x >= p.main_blocks) {
@@ -221,97 +315,42 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
     }
     __shared__ float red[4][64 * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = (int)(blockIdx.x % p.chan_blocks) * 64 * V + lane * V;
+    const int c0 = (int)(blockIdx.x % p.chan_blocks) * 64 * V, c = c0 + lane * V;
     const int blk = blockIdx.x / p.chan_blocks;
-    const int64_t first = ((int64_t)blk * 4 + wave) * kTok;
-    float dw[W][V], db[V];
+    const int64_t first = ((int64_t)blk * 4 + wave) * kTokBwd;
+    ConvWalk<T, W, V> k;
 #pragma unroll
     for (int e = 0; e < V; e++) {
-        db[e] = 0.f;
+        k.db[e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < W; j++) dw[j][e] = 0.f;
+        for (int j = 0; j < W; j++) k.dw[j][e] = 0.f;
     }
     if (first < p.total && c < p.dim) {
         const int t0 = __builtin_amdgcn_readfirstlane((int)first);
-        const int t1 = min(t0 + kTok, p.total);
+        const int t1 = min(t0 + kTokBwd, p.total);
         SeqAt q = seq_of(p, t0);
         next_seq(p, t0, q);
-        float w[W][V], bias[V], win[W][V], pend[W][V];   // pend[j]: dx of token t - W + 1 + j so far
 #pragma unroll
         for (int e = 0; e < V; e++) {
-            bias[e] = p.bias ? p.bias[c + e] : 0.f;
+            k.bias[e] = p.bias ? p.bias[c + e] : 0.f;
 #pragma unroll
             for (int j = 0; j < W; j++) {
-                w[j][e] = p.w[(int64_t)(c + e) * W + j];
-                pend[j][e] = 0.f;
+                k.w[j][e] = p.w[(int64_t)(c + e) * W + j];
+                k.pend[j][e] = 0.f;
             }
         }
 #pragma unroll
-        for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t0 - W + j, c, win[j]);
-        for (int t = t0; t < t1 + W - 1; t++) {
-            float e_t[V], xin[V];
-#pragma unroll
-            for (int e = 0; e < V; e++) {
-#pragma unroll
-                for (int j = 0; j + 1 < W; j++) pend[j][e] = pend[j + 1][e];
-                pend[W - 1][e] = 0.f;
-                e_t[e] = 0.f;
-            }
-            if (t < p.total) {
-                if (t >= q.b) {
-                    next_seq(p, t, q);
-#pragma unroll
-                    for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
-                }
-                load_vec<T, V>(xin, (const T *)p.x + (int64_t)t * p.x_row + c);
-                load_vec<T, V>(e_t, (const T *)p.dy + (int64_t)t * p.dy_row + c);
-#pragma unroll
-                for (int e = 0; e < V; e++) {
-#pragma unroll
-                    for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
-                    win[W - 1][e] = xin[e];
-                    if (p.silu) {
-                        float v = bias[e];
-#pragma unroll
-                        for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
-                        e_t[e] *= silu_grad(v);
-                    }
-                }
-                const int pos = t - q.a;
-#pragma unroll
-                for (int j = 0; j < W; j++)
-                    if (pos >= W - 1 - j) {           // tap j's input is a token of this sequence
-#pragma unroll
-                        for (int e = 0; e < V; e++) pend[j][e] += w[j][e] * e_t[e];
-                    }
-                if (t < t1) {
-#pragma unroll
-                    for (int e = 0; e < V; e++) {
-                        db[e] += e_t[e];
-#pragma unroll
-                        for (int j = 0; j < W; j++) dw[j][e] += e_t[e] * win[j][e];
-                    }
-                    const int k = t - q.b + (W - 1);  // the token's row of conv_out, if it has one
-                    if (p.dconv_out && k >= 0) {
-                        float o[V];
-                        load_vec<T, V>(o, (const T *)p.dconv_out + ((int64_t)q.s * (W - 1) + k) * p.dim + c);
-#pragma unroll
-                        for (int e = 0; e < V; e++) pend[W - 1][e] += o[e];
-                    }
-                }
-            }
-            const int tau = t - (W - 1);
-            if (tau >= t0) store_vec<T, V>((T *)p.dx + (int64_t)tau * p.dim + c, pend[0]);
-        }
+        for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t0 - W + j, c, k.win[j]);
+        if (t0 - (W - 1) >= q.a && t1 + W - 1 <= q.b && t1 + W - 1 <= p.total) k.template run<true>(p, q, t0, t1, c);
+        else k.template run<false>(p, q, t0, t1, c);
     }
     // the four waves' sums, in order
 #pragma unroll
     for (int j = 0; j <= W; j++) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < V; e++) red[wave][lane * V + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        for (int e = 0; e < V; e++) red[wave][lane * V + e] = j < W ? k.dw[j < W ? j : 0][e] : k.db[e];
         __syncthreads();
-        const int c0 = (int)(blockIdx.x % p.chan_blocks) * 64 * V;
         for (int i = threadIdx.x; i < 64 * V; i += 256)
             if (c0 + i < p.dim)
                 p.part[((int64_t)blk * (W + 1) + j) * p.dim + c0 + i] =
@@ -319,14 +358,24 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
     }
 }
 
-// dweight [D, W] and dbias [D] from the partial sums of `blocks` workgroups.
+// dweight [D, W] and dbias [D] from the partial sums of `blocks` workgroups: 16 columns of [W + 1][D] a
+// workgroup, 16 threads over the rows of each.
 __global__ __launch_bounds__(256) void k_conv_reduce(const float *part, int blocks, int dim, int W, float *dweight,
                                                      float *dbias) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= dim * (W + 1)) return;
-    const int j = i / dim, c = i % dim;
+    __shared__ float red[16][17];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, n = dim * (W + 1), i = blockIdx.x * 16 + x;
     float s = 0.f;
-    for (int b = 0; b < blocks; b++) s += part[((int64_t)b * (W + 1) + j) * dim + c];
+    if (i < n) {
+#pragma unroll 8
+        for (int b = y; b < blocks; b += 16) s += part[(int64_t)b * n + i];
+    }
+    red[y][x] = s;
+    __syncthreads();
+    if (y || i >= n) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k++) s += red[k][x];
+    const int j = i / dim, c = i % dim;
     if (j < W) dweight[(int64_t)c * W + j] = s;
     else if (dbias) dbias[c] = s;
 }
@@ -392,7 +441,7 @@ ConvParams conv_params(const mamba3_conv_args *a) {
     return p;
 }
 
-int64_t token_blocks(int64_t total) { return (total + 4 * kTok - 1) / (4 * kTok); }
+int64_t token_blocks(int64_t total, int tok) { return (total + 4 * tok - 1) / (4 * tok); }
 
 #define M3_CONV_WIDTHS(W, CALL)     \
     switch (W) {                    \
@@ -405,16 +454,16 @@ int64_t token_blocks(int64_t total) { return (total + 4 * kTok - 1) / (4 * kTok)
         default: CALL(8); break;    \
     }
 
-template <typename T, int V>
-void conv_go(ConvParams p, int width, bool back, hipStream_t st) {
+template <typename T, int V, bool BACK>
+void conv_go(ConvParams p, int width, hipStream_t st) {
     p.chan_blocks = (p.dim + 64 * V - 1) / (64 * V);
-    p.main_blocks = (int32_t)(token_blocks(p.total) * p.chan_blocks);
-    const bool state = back ? p.dconv_in != nullptr : p.conv_out != nullptr;
+    p.main_blocks = (int32_t)(token_blocks(p.total, BACK ? kTokBwd : kTok) * p.chan_blocks);
+    const bool state = BACK ? p.dconv_in != nullptr : p.conv_out != nullptr;
     const int64_t extra = state ? ((int64_t)p.nseq * (width - 1) * p.dim + 255) / 256 : 0;
     const dim3 grid((uint32_t)(p.main_blocks + extra));
     if (grid.x == 0) return;
-#define M3_GO(W)                                                                                  \
-    if (back) hipLaunchKernelGGL((k_conv_bwd<T, W, V>), grid, dim3(256), 0, st, p);               \
+#define M3_GO(W)                                                                                        \
+    if constexpr (BACK) hipLaunchKernelGGL((k_conv_bwd<T, W, V>), grid, dim3(256), 0, st, p);           \
     else hipLaunchKernelGGL((k_conv<T, W, V>), grid, dim3(256), 0, st, p)
     M3_CONV_WIDTHS(width, M3_GO)
 #undef M3_GO
@@ -434,18 +483,18 @@ void conv_step_go(const ConvStepParams &p, int width, hipStream_t st) {
 mamba3_status launch_conv(const mamba3_conv_args *a, hipStream_t st) {
     const ConvParams p = conv_params(a);
     if (a->dtype == MAMBA3_F32) {
-        if (wide(4, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<float, 4>(p, a->width, false, st);
-        else conv_go<float, 1>(p, a->width, false, st);
+        if (wide(4, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<float, 4, false>(p, a->width, st);
+        else conv_go<float, 1, false>(p, a->width, st);
     } else {
-        if (wide(2, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<bf16, 8>(p, a->width, false, st);
-        else conv_go<bf16, 1>(p, a->width, false, st);
+        if (wide(2, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<bf16, 8, false>(p, a->width, st);
+        else conv_go<bf16, 1, false>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 
 size_t conv_bwd_workspace_bytes(const mamba3_conv_bwd_args *b) {
     const int64_t total = (int64_t)b->fwd.batch * b->fwd.seqlen;
-    return (size_t)(token_blocks(total) * (b->fwd.width + 1) * b->fwd.dim * 4);
+    return (size_t)(token_blocks(total, kTokBwd) * (b->fwd.width + 1) * b->fwd.dim * 4);
 }
 
 mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st) {
@@ -457,15 +506,15 @@ mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st) {
     const int64_t es = a->dtype == MAMBA3_BF16 ? 2 : 4;
     const bool wd = wide(es, p.dim, {p.x, p.conv_in, p.dy, p.dconv_out, p.dx}, {p.x_row, p.dy_row});
     if (a->dtype == MAMBA3_F32) {
-        if (wd) conv_go<float, 4>(p, a->width, true, st);
-        else conv_go<float, 1>(p, a->width, true, st);
+        if (wd) conv_go<float, 4, true>(p, a->width, st);
+        else conv_go<float, 1, true>(p, a->width, st);
     } else {
-        if (wd) conv_go<bf16, 8>(p, a->width, true, st);
-        else conv_go<bf16, 1>(p, a->width, true, st);
+        if (wd) conv_go<bf16, 4, true>(p, a->width, st);
+        else conv_go<bf16, 1, true>(p, a->width, st);
     }
     const int64_t n = (int64_t)p.dim * (a->width + 1);
-    hipLaunchKernelGGL(k_conv_reduce, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, st, p.part,
-                       (int)token_blocks(p.total), p.dim, a->width, b->dweight, b->dbias);
+    hipLaunchKernelGGL(k_conv_reduce, dim3((uint32_t)((n + 15) / 16)), dim3(256), 0, st, p.part,
+                       (int)token_blocks(p.total, kTokBwd), p.dim, a->width, b->dweight, b->dbias);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 

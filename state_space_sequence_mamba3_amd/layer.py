@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 from . import MAMBA3_BF16, MAMBA3_F32, MAMBA3_OK, Mamba3Error, lib
 
@@ -121,16 +122,49 @@ def _bad(what):
     raise ValueError(f"mamba3: {what}")
 
 
-def _dense(t, shape, dtype, dev, name):
-    """Device address of a contiguous tensor of this shape and type, None for None."""
-    if t is None:
-        return None
+class _Op:
+    """One entry point, called with its struct packed by its values: a single token's call takes a few
+    microseconds on the GPU, and filling a ctypes structure field by field takes as long."""
+    _CODES = {_i32: "i", _i64: "q", _f32: "f", _vp: "P", _size: "N"}
+
+    def __init__(self, op):
+        args, tail, ws = _OPS[op]
+        fields = [f for _, k in args._fields_ for f in ([c for _, c in k._fields_] if hasattr(k, "_fields_") else [k])]
+        inner = [k for _, k in args._fields_ if hasattr(k, "_fields_")]
+        # native alignment as in C; an inner struct ends at a multiple of 8 bytes
+        n = len(inner[0]._fields_) if inner else 0
+        codes = [self._CODES[f] for f in fields]
+        self.pack = struct.Struct("@" + "".join(codes[:n]) + ("0P" if n else "") + "".join(codes[n:]) + "0P").pack
+        self.name = f"mamba3_{op}" + (f"_{tail}" if tail else "")
+        l = lib()
+        self.run = l[self.name]          # (a function object of its own beside the declared one)
+        self.run.argtypes, self.run.restype = [ctypes.c_char_p, _vp], ctypes.c_int
+        if ws:
+            self.size = l[f"mamba3_{op}_workspace_size"]
+            self.size.argtypes, self.size.restype = [ctypes.c_char_p], _size
+        assert len(self.pack(*[0] * len(fields))) == ctypes.sizeof(args)
+
+
+@functools.lru_cache(None)
+def _op(op):
+    return _Op(op)
+
+
+def _refuse(t, shape, dtype, dev, name):
     if t.shape != shape:
         _bad(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         _bad(f"{name} must be on {dev}, got {t.device}")
+
+
+def _dense(t, shape, dtype, dev, name):
+    """Device address of a contiguous tensor of this shape and type, 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _refuse(t, shape, dtype, dev, name)
     if not t.is_contiguous():
         _bad(f"{name} must be contiguous; call .contiguous()")
     return t.data_ptr()
@@ -140,13 +174,9 @@ def _rows(t, shape, lead, dtype, dev, name):
     """(device address, elements from token to token or 0) of a token array whose first `lead`
     dimensions count tokens."""
     if t is None:
-        return None, 0
-    if t.shape != shape:
-        _bad(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        _bad(f"{name} must be on {dev}, got {t.device}")
+        return 0, 0
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _refuse(t, shape, dtype, dev, name)
     if t.is_contiguous():
         return t.data_ptr(), 0
     st = t.stride()
@@ -174,61 +204,58 @@ def _token(x, dims, name="x"):
         _bad(f"{name} must have {dims} dimensions, got {tuple(x.shape)}")
     if not x.is_cuda:
         _bad("tensors must be in device memory")
-    code = _dtypes().get(x.dtype)
+    ty = x.dtype
+    code = _dtypes().get(ty)
     if code is None:
-        raise TypeError(f"token inputs must be float32 or bfloat16, got {x.dtype}")
-    return code, x.dtype, x.device
+        raise TypeError(f"token inputs must be float32 or bfloat16, got {ty}")
+    return code, ty, x.device
 
 
 def _packed(x, cu):
     """(cu_seqlens address, nseq, sequences) of a whole-sequence call."""
     import torch
     if cu is None:
-        return None, 0, x.shape[0]
+        return 0, 0, x.shape[0]
     if cu.dim() != 1 or cu.numel() < 2 or x.shape[0] != 1:
         _bad("packed batches have x [1, tokens, ...] and cu_seqlens [nseq + 1]")
     nseq = cu.numel() - 1
     return _dense(cu, cu.shape, torch.int32, x.device, "cu_seqlens"), nseq, nseq
 
 
-def _call(name, a, dev, stream, made=()):
+def _call(op, args, dev, stream, made=()):
     """Runs an entry point on `stream` (None: the device's current one); `made`: tensors allocated here."""
     import torch
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, int):
-        raw = stream
-        for t in made:
-            if t is not None:
-                t.record_stream(torch.cuda.ExternalStream(raw, device=dev))
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
         if stream.device != dev:
             _bad(f"the stream is on {stream.device}, the tensors are on {dev}")
         raw = stream.cuda_stream
-        for t in made:
+        for t in made:      # their memory is not given out again before the stream is done with it
             if t is not None:
                 t.record_stream(stream)
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = f(ctypes.byref(a), raw)
+    if dev.index == torch._C._cuda_getDevice():
+        st = op.run(args, raw)
     else:
         with torch.cuda.device(dev):
-            st = f(ctypes.byref(a), raw)
+            st = op.run(args, raw)
     if st != MAMBA3_OK:
-        raise Mamba3Error(st, name)
+        raise Mamba3Error(st, op.name)
 
 
-def _workspace(name, a, given, dev):
-    """Sets a's workspace: the one given (a contiguous uint8 tensor) or a new one."""
+def _workspace(op, args, given, dev):
+    """The workspace given (a contiguous uint8 tensor) or a new one, as (tensor, address, bytes); `args`
+    are the call's without one."""
     import torch
     if given is None:
-        need = getattr(lib(), name)(ctypes.byref(a))
+        need = op.size(op.pack(*args, 0, 0))
         if need == 0:
-            return None
+            return None, 0, 0
         given = torch.empty((need,), dtype=torch.uint8, device=dev)
-    a.workspace = _dense(given, (given.numel(),), torch.uint8, dev, "workspace")
-    a.workspace_bytes = given.numel()
-    return given
+        return given, given.data_ptr(), need
+    return given, _dense(given, (given.numel(),), torch.uint8, dev, "workspace"), given.numel()
 
 
 # ----------------------------------------------------------------------------- convolution
@@ -241,10 +268,8 @@ def _conv_args(x, weight, bias, silu, conv_in, cu_seqlens):
     W = weight.shape[1]
     cu, nseq, S = _packed(x, cu_seqlens)
     xp, xr = _rows(x, x.shape, 2, ty, dev, "x")
-    a = ConvArgs(b, L, D, W, code, 1 if silu else 0, cu, nseq, xr, xp,
-                 _dense(weight, (D, W), torch.float32, dev, "weight"),
-                 _dense(bias, (D,), torch.float32, dev, "bias"),
-                 _dense(conv_in, (S, W - 1, D), ty, dev, "conv_in"), None, None)
+    a = (b, L, D, W, code, 1 if silu else 0, cu, nseq, xr, xp, _dense(weight, (D, W), torch.float32, dev, "weight"),
+         _dense(bias, (D,), torch.float32, dev, "bias"), _dense(conv_in, (S, W - 1, D), ty, dev, "conv_in"))
     return a, ty, dev, S, W
 
 
@@ -263,9 +288,9 @@ def mamba3_conv_fwd(x, weight, bias=None, *, silu=True, conv_in=None, cu_seqlens
     if conv_out is None and want_state:
         conv_out = torch.empty((S, max(W - 1, 0), x.shape[2]), dtype=ty, device=dev)
         made.append(conv_out)
-    a.y = _dense(y, x.shape, ty, dev, "y")
-    a.conv_out = _dense(conv_out, (S, W - 1, x.shape[2]), ty, dev, "conv_out")
-    _call("mamba3_conv_fwd", a, dev, stream, made)
+    op = _op("conv")
+    _call(op, op.pack(*a, _dense(y, x.shape, ty, dev, "y"),
+                      _dense(conv_out, (S, W - 1, x.shape[2]), ty, dev, "conv_out")), dev, stream, made)
     return y, conv_out
 
 
@@ -283,10 +308,11 @@ def mamba3_conv_bwd(x, weight, bias=None, *, dy, dconv_out=None, silu=True, conv
         g["dconv_in"] = torch.empty_like(conv_in)
     yp, yr = _rows(dy, x.shape, 2, ty, dev, "dy")
     p = {k: v.data_ptr() for k, v in g.items()}
-    q = ConvBwdArgs(a, yr, yp, _dense(dconv_out, (S, W - 1, D), ty, dev, "dconv_out"), p["dx"], p["dweight"],
-                    p.get("dbias"), p.get("dconv_in"), None, 0)
-    ws = _workspace("mamba3_conv_bwd_workspace_size", q, workspace, dev)
-    _call("mamba3_conv_bwd", q, dev, stream, [*g.values(), ws])
+    q = (*a, 0, 0, yr, yp, _dense(dconv_out, (S, W - 1, D), ty, dev, "dconv_out"), p["dx"], p["dweight"],
+         p.get("dbias", 0), p.get("dconv_in", 0))
+    op = _op("conv_bwd")
+    ws, wp, wn = _workspace(op, q, workspace, dev)
+    _call(op, op.pack(*q, wp, wn), dev, stream, [*g.values(), ws])
     return g
 
 
@@ -294,7 +320,7 @@ def _slots(slots, batch, state, dev):
     """(address, pool size, states) of a step's slot table."""
     import torch
     if slots is None:
-        return None, 0, batch
+        return 0, 0, batch
     return _dense(slots, (batch,), torch.int32, dev, "slots"), state.shape[0], state.shape[0]
 
 
@@ -314,10 +340,11 @@ def mamba3_conv_step(x, weight, bias=None, *, conv, silu=True, slots=None, y=Non
         made.append(y)
     sp, ns, states = _slots(slots, b, conv, dev)
     xp, xr = _rows(x, x.shape, 1, ty, dev, "x")
-    a = ConvStepArgs(b, D, W, code, 1 if silu else 0, xr, xp, _dense(weight, (D, W), torch.float32, dev, "weight"),
-                     _dense(bias, (D,), torch.float32, dev, "bias"),
-                     _dense(conv, (states, W - 1, D), ty, dev, "conv"), _dense(y, (b, D), ty, dev, "y"), sp, ns)
-    _call("mamba3_conv_step", a, dev, stream, made)
+    op = _op("conv_step")
+    a = op.pack(b, D, W, code, 1 if silu else 0, xr, xp, _dense(weight, (D, W), torch.float32, dev, "weight"),
+                _dense(bias, (D,), torch.float32, dev, "bias"), _dense(conv, (states, W - 1, D), ty, dev, "conv"),
+                _dense(y, (b, D), ty, dev, "y"), sp, ns)
+    _call(op, a, dev, stream, made)
     return y
 
 
@@ -336,10 +363,9 @@ def _sel_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h_in, cu_seqlens):
     bp, br = _rows(B, (b, L, G, N), 2, ty, dev, "B")
     cp, cr = _rows(C, (b, L, G, N), 2, ty, dev, "C")
     f = torch.float32
-    a = SelectiveScanArgs(b, L, dim, N, G, code, 1 if dt_softplus else 0, cu, nseq, xr, dr, br, cr, zr, xp, dp, bp, cp,
-                          zp, _dense(A, (dim, N), f, dev, "A"), _dense(D, (dim,), f, dev, "D"),
-                          _dense(dt_bias, (dim,), f, dev, "dt_bias"), _dense(h_in, (S, dim, N), f, dev, "h_in"),
-                          None, None, None, 0)
+    a = (b, L, dim, N, G, code, 1 if dt_softplus else 0, cu, nseq, xr, dr, br, cr, zr, xp, dp, bp, cp, zp,
+         _dense(A, (dim, N), f, dev, "A"), _dense(D, (dim,), f, dev, "D"), _dense(dt_bias, (dim,), f, dev, "dt_bias"),
+         _dense(h_in, (S, dim, N), f, dev, "h_in"))
     return a, ty, dev, S, N
 
 
@@ -358,10 +384,11 @@ def mamba3_selective_scan_fwd(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, d
     if h_out is None and want_state:
         h_out = torch.empty((S, x.shape[2], N), dtype=torch.float32, device=dev)
         made.append(h_out)
-    a.y = _dense(y, x.shape, ty, dev, "y")
-    a.h_out = _dense(h_out, (S, x.shape[2], N), torch.float32, dev, "h_out")
-    made.append(_workspace("mamba3_selective_scan_workspace_size", a, workspace, dev))
-    _call("mamba3_selective_scan_fwd", a, dev, stream, made)
+    a += (_dense(y, x.shape, ty, dev, "y"), _dense(h_out, (S, x.shape[2], N), torch.float32, dev, "h_out"))
+    op = _op("selective_scan")
+    ws, wp, wn = _workspace(op, a, workspace, dev)
+    made.append(ws)
+    _call(op, op.pack(*a, wp, wn), dev, stream, made)
     return y, h_out
 
 
@@ -386,11 +413,11 @@ def mamba3_selective_scan_bwd(x, dt, A, B, C, D=None, *, dy, dh_out=None, z=None
         g["dh_in"] = torch.empty((S, dim, N), dtype=torch.float32, device=dev)
     yp, yr = _rows(dy, x.shape, 2, ty, dev, "dy")
     p = {k: v.data_ptr() for k, v in g.items()}
-    q = SelectiveScanBwdArgs(a, yr, yp, _dense(dh_out, (S, dim, N), torch.float32, dev, "dh_out"),
-                             *[p.get(k) for k in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dh_in")],
-                             None, 0)
-    ws = _workspace("mamba3_selective_scan_bwd_workspace_size", q, workspace, dev)
-    _call("mamba3_selective_scan_bwd", q, dev, stream, [*g.values(), ws])
+    q = (*a, 0, 0, 0, 0, yr, yp, _dense(dh_out, (S, dim, N), torch.float32, dev, "dh_out"),
+         *[p.get(k, 0) for k in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dh_in")])
+    op = _op("selective_scan_bwd")
+    ws, wp, wn = _workspace(op, q, workspace, dev)
+    _call(op, op.pack(*q, wp, wn), dev, stream, [*g.values(), ws])
     return g
 
 
@@ -416,11 +443,12 @@ def mamba3_selective_step(x, dt, A, B, C, D=None, *, h, z=None, dt_bias=None, dt
     zp, zr = _rows(z, x.shape, 1, ty, dev, "z")
     bp, br = _rows(B, (b, G, N), 1, ty, dev, "B")
     cp, cr = _rows(C, (b, G, N), 1, ty, dev, "C")
-    a = SelectiveStepArgs(b, dim, N, G, code, 1 if dt_softplus else 0, xr, dr, br, cr, zr, xp, dp, bp, cp, zp,
-                          _dense(A, (dim, N), f, dev, "A"), _dense(D, (dim,), f, dev, "D"),
-                          _dense(dt_bias, (dim,), f, dev, "dt_bias"), _dense(h, (states, dim, N), f, dev, "h"),
-                          _dense(y, (b, dim), ty, dev, "y"), sp, ns)
-    _call("mamba3_selective_step", a, dev, stream, made)
+    op = _op("selective_step")
+    a = op.pack(b, dim, N, G, code, 1 if dt_softplus else 0, xr, dr, br, cr, zr, xp, dp, bp, cp, zp,
+                _dense(A, (dim, N), f, dev, "A"), _dense(D, (dim,), f, dev, "D"),
+                _dense(dt_bias, (dim,), f, dev, "dt_bias"), _dense(h, (states, dim, N), f, dev, "h"),
+                _dense(y, (b, dim), ty, dev, "y"), sp, ns)
+    _call(op, a, dev, stream, made)
     return y
 
 
@@ -453,7 +481,7 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
             y = torch.empty(x.shape, dtype=ty, device=dev)
             made.append(y)
         out["y"] = y
-    qp = sp = None
+    qp = sp = 0
     qcode = 0
     if quant is not None:
         if quant not in _qtypes():
@@ -465,11 +493,11 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
         made += [out["q"], out["scale"]]
         qp, sp = out["q"].data_ptr(), out["scale"].data_ptr()
     xp, xr = _rows(flat, (rows, dim), 1, ty, dev, "x")
-    a = RmsnormArgs(rows, dim, code, _dtypes()[rt], qcode, qblock, eps, xr, xp,
-                    _dense(residual, x.shape, rt, dev, "residual"),
-                    _dense(weight, (dim,), torch.float32, dev, "weight"),
-                    _dense(residual_out, x.shape, rt, dev, "residual_out"), _dense(y, x.shape, ty, dev, "y"), qp, sp)
-    _call("mamba3_rmsnorm_fwd", a, dev, stream, made)
+    op = _op("rmsnorm")
+    a = op.pack(rows, dim, code, _dtypes()[rt], qcode, qblock, eps, xr, xp,
+                _dense(residual, x.shape, rt, dev, "residual"), _dense(weight, (dim,), torch.float32, dev, "weight"),
+                _dense(residual_out, x.shape, rt, dev, "residual_out"), _dense(y, x.shape, ty, dev, "y"), qp, sp)
+    _call(op, a, dev, stream, made)
     return out
 
 
@@ -499,10 +527,12 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
         g["dweight"] = torch.empty_like(weight)
         made.append(g["dweight"])
     yp, yr = _rows(flat, (rows, dim), 1, ty, dev, "dy")
-    a = RmsnormBwdArgs(rows, dim, code, _dtypes()[rt], eps, yr, _dense(s, s.shape, rt, dev, "s"), yp,
-                       _dense(dresidual_out, s.shape, rt, dev, "dresidual_out"),
-                       _dense(weight, (dim,), torch.float32, dev, "weight"), dx.data_ptr() if dx is not None else None,
-                       g["dresidual"].data_ptr(), g["dweight"].data_ptr() if weight is not None else None, None, 0)
-    made.append(_workspace("mamba3_rmsnorm_bwd_workspace_size", a, workspace, dev))
-    _call("mamba3_rmsnorm_bwd", a, dev, stream, made)
+    op = _op("rmsnorm_bwd")
+    a = (rows, dim, code, _dtypes()[rt], eps, yr, _dense(s, s.shape, rt, dev, "s"), yp,
+         _dense(dresidual_out, s.shape, rt, dev, "dresidual_out"), _dense(weight, (dim,), torch.float32, dev, "weight"),
+         dx.data_ptr() if dx is not None else 0, g["dresidual"].data_ptr(),
+         g["dweight"].data_ptr() if weight is not None else 0)
+    ws, wp, wn = _workspace(op, a, workspace, dev)
+    made.append(ws)
+    _call(op, op.pack(*a, wp, wn), dev, stream, made)
     return g
