@@ -418,7 +418,7 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  * Token rows. Token arrays are [batch, seqlen, n] with n innermost. Those with
  * a `_row` field may be views of wider rows (the halves of one projection's
  * output): `_row` is the number of elements from one token to the next, n at
- * least, or 0 for dense rows. Tokens of a padded batch lie at one distance
+ * least and 2^25 at most, or 0 for dense rows. Tokens of a padded batch lie at one distance
  * across sequences too. Any element alignment is accepted; rows and pointers
  * that are multiples of 16 bytes are read fastest. Arrays without a `_row`
  * field are dense.

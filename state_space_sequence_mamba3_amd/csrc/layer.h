@@ -11,33 +11,37 @@ template <> struct QuadOf<float> { typedef f32x4 type; };
 template <> struct QuadOf<bf16> { typedef bf16x4 type; };
 template <typename T> using quad = typename QuadOf<T>::type;
 
-// Elements c0 .. c0 + 3 of a row of n elements. VEC: n and c0 are multiples of 4 and the row is
-// aligned to a quad. Places behind the row's end repeat its last element (or quad), so that every
-// lane loads from inside the row; their results are never stored.
+// Elements c0 .. c0 + 3 of row t behind `base` (rows of n elements, `row` apart). VEC: n, c0 and row
+// are multiples of 4 and base is aligned to a quad. Places behind a row's end repeat its last element
+// (or quad), so that every lane loads from inside the row; their results are never stored. `base` is
+// the same for all lanes and the offset has 32 bits, so that the load takes the address from scalar
+// registers and an offset that does not change from tile to tile.
 template <typename T, bool VEC>
-__device__ __forceinline__ quad<T> load_quad(const T *row, int c0, int n) {
+__device__ __forceinline__ quad<T> load_quad(const T *base, int t, int64_t row, int c0, int n) {
     quad<T> v;
     if constexpr (VEC) {
-        v = *(const quad<T> *)(row + min(c0, n - 4));
+        v = *(const quad<T> *)((const char *)base + (uint32_t)(t * (uint32_t)row + min(c0, n - 4)) * (uint32_t)sizeof(T));
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = row[min(c0 + e, n - 1)];
+        for (int e = 0; e < 4; e++)
+            v[e] = *(const T *)((const char *)base + (uint32_t)(t * (uint32_t)row + min(c0 + e, n - 1)) * (uint32_t)sizeof(T));
     }
     return v;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_quad(T *row, int c0, int n, f32x4 v) {
+__device__ __forceinline__ void store_quad(T *base, int t, int64_t row, int c0, int n, f32x4 v) {
     if constexpr (VEC) {
         if (c0 < n) {
             quad<T> o;
 #pragma unroll
             for (int e = 0; e < 4; e++) o[e] = from_f<T>(v[e]);
-            *(quad<T> *)(row + c0) = o;
+            *(quad<T> *)((char *)base + (uint32_t)(t * (uint32_t)row + c0) * (uint32_t)sizeof(T)) = o;
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 4; e++)
-            if (c0 + e < n) row[c0 + e] = from_f<T>(v[e]);
+            if (c0 + e < n)
+                *(T *)((char *)base + (uint32_t)(t * (uint32_t)row + c0 + e) * (uint32_t)sizeof(T)) = from_f<T>(v[e]);
     }
 }
 

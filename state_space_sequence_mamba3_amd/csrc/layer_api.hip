@@ -68,7 +68,8 @@ mamba3_status check_workspace(const void *ws, size_t bytes, size_t need, const A
 bool dtype_ok(int32_t t) { return t == MAMBA3_F32 || t == MAMBA3_BF16; }
 int64_t esize(int32_t t) { return t == MAMBA3_BF16 ? 2 : 4; }
 bool flag(int32_t f) { return f == 0 || f == 1; }
-bool row_ok(int64_t row, int64_t n) { return row == 0 || (row >= n && row <= INT32_MAX); }
+// (rows of at most 2^25 elements: a tile's 16 rows are addressed by 32 bits of bytes)
+bool row_ok(int64_t row, int64_t n) { return n <= (1 << 25) && (row == 0 || (row >= n && row <= (1 << 25))); }
 
 // batch, seqlen, cu_seqlens and nseq of a whole-sequence call; S the sequences, T the tokens
 mamba3_status check_batch(int32_t batch, int32_t seqlen, const int32_t *cu, int32_t nseq, int64_t *S, int64_t *T) {

@@ -46,7 +46,7 @@ struct SelRow {
     bool first, last;
 };
 
-__device__ __forceinline__ SelRow sel_row(const SelParams &p, int r) {
+__device__ __forceinline__ SelRow sel_row_of(const SelParams &p, int r) {
     SelRow o;
     o.first = o.last = true;
     if (p.table) {
@@ -67,6 +67,15 @@ __device__ __forceinline__ SelRow sel_row(const SelParams &p, int r) {
         o.first = k == 0;
         o.last = k == p.nseg - 1;
     }
+    return o;
+}
+
+// The same, in scalar registers
+__device__ __forceinline__ SelRow sel_row(const SelParams &p, int r) {
+    SelRow o = sel_row_of(p, r);
+    o.t0 = __builtin_amdgcn_readfirstlane(o.t0);
+    o.t1 = __builtin_amdgcn_readfirstlane(o.t1);
+    o.seq = __builtin_amdgcn_readfirstlane(o.seq);
     return o;
 }
 

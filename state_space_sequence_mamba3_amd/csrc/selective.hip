@@ -8,6 +8,8 @@
 // an exponential (two issue slots), two products and two fused adds for every token, channel and
 // state, on the vector unit. Where N is 16 that is 96 slots for 8 bytes of bf16, so the vector
 // unit and not the memory bounds the scan.
+#include <type_traits>
+
 #include "selective.h"
 
 namespace m3 {
@@ -95,25 +97,36 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     T *y = (T *)p.y + g * p.dpg;
 
     quad<T> rx[XE], rd[XE], rz[XE], ry[XE], rB[BE], rC[BE];
-    auto fetch = [&](int t0) {
+    // the tile from t0 on; TAIL: it may end behind the row's last token, whose inputs are repeated then
+    auto fetch = [&](int t0, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const T *x0 = x + (int64_t)t0 * p.x_row, *d0 = dt + (int64_t)t0 * p.dt_row, *z0 = z + (int64_t)t0 * p.z_row,
+                *y0 = dy + (int64_t)t0 * p.dy_row, *B0 = B + (int64_t)t0 * p.B_row, *C0 = C + (int64_t)t0 * p.C_row;
 #pragma unroll
         for (int i = 0; i < XE; i++) {
-            const int64_t t = min(t0 + xt[i], row.t1 - 1);
-            rx[i] = load_quad<T, VEC>(x + t * p.x_row, xc[i], p.dpg);
-            rd[i] = load_quad<T, VEC>(dt + t * p.dt_row, xc[i], p.dpg);
-            if (z) rz[i] = load_quad<T, VEC>(z + t * p.z_row, xc[i], p.dpg);
-            if (MODE == STORE_PART) ry[i] = load_quad<T, VEC>(dy + t * p.dy_row, xc[i], p.dpg);
+            const int t = TAIL ? min(xt[i], row.t1 - 1 - t0) : xt[i];
+            rx[i] = load_quad<T, VEC>(x0, t, p.x_row, xc[i], p.dpg);
+            rd[i] = load_quad<T, VEC>(d0, t, p.dt_row, xc[i], p.dpg);
+            if (z) rz[i] = load_quad<T, VEC>(z0, t, p.z_row, xc[i], p.dpg);
+            if (MODE == STORE_PART) ry[i] = load_quad<T, VEC>(y0, t, p.dy_row, xc[i], p.dpg);
         }
 #pragma unroll
         for (int i = 0; i < BE; i++) {
-            const int64_t t = min(t0 + bt[i], row.t1 - 1);
-            rB[i] = load_quad<T, VEC>(B + t * p.B_row, bn[i], p.N);
-            if (NEEDC) rC[i] = load_quad<T, VEC>(C + t * p.C_row, bn[i], p.N);
+            const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
+            rB[i] = load_quad<T, VEC>(B0, t, p.B_row, bn[i], p.N);
+            if (NEEDC) rC[i] = load_quad<T, VEC>(C0, t, p.C_row, bn[i], p.N);
         }
     };
+    const std::integral_constant<bool, false> whole_tile;
+    const std::integral_constant<bool, true> last_tile;
+    auto fetch_next = [&](int t0) {
+        if (t0 + TT <= row.t1) fetch(t0, whole_tile);
+        else if (t0 < row.t1) fetch(t0, last_tile);
+    };
     const int64_t stored = stored_base(row.t0, r, kSelStored);
-    if (row.t0 < row.t1) fetch(row.t0);
-    for (int t0 = row.t0; t0 < row.t1; t0 += TT) {
+    auto tile = [&](int t0, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const int left = TAIL ? row.t1 - t0 : TT;           // the tile's tokens
         f32x4 xv[XE], zv[XE];
 #pragma unroll
         for (int i = 0; i < XE; i++) {
@@ -125,7 +138,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                 float s = to_f(rd[i][e]) + biasv[i][e];
                 if (p.softplus) s = softplus_hw(s);
                 // a step of 0 behind the sequence's end keeps the state
-                const bool in = t0 + xt[i] < row.t1;
+                const bool in = !TAIL || xt[i] < left;
                 u[e >> 1][2 * (e & 1)] = in ? s : 0.f;
                 u[e >> 1][2 * (e & 1) + 1] = in ? s * xv[i][e] : 0.f;
             }
@@ -139,7 +152,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                     for (int e = 0; e < 4; e++) {
                         v[e] = to_f(ry[i][e]);
                         if (z) v[e] *= zv[i][e] * sigmoid_hw(zv[i][e]);
-                        v[e] = t0 + xt[i] < row.t1 ? v[e] : 0.f;
+                        v[e] = !TAIL || xt[i] < left ? v[e] : 0.f;
                     }
                     *(f32x4 *)&S.y[xt[i]][xc[i] - c0] = v;
                 }
@@ -151,24 +164,31 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                 f32x4 b, c;
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
+                    b[e] = to_f(rB[i][e]);
+                    c[e] = NEEDC ? to_f(rC[i][e]) : 0.f;
+                }
+                if (TAIL || p.N != NP) {
                     // places behind the last state or token hold zero, whatever lies there
-                    const bool in = bn[i] + e < p.N && t0 + bt[i] < row.t1;
-                    b[e] = in ? to_f(rB[i][e]) : 0.f;
-                    c[e] = in && NEEDC ? to_f(rC[i][e]) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const bool in = bn[i] + e < p.N && (!TAIL || bt[i] < left);
+                        b[e] = in ? b[e] : 0.f;
+                        c[e] = in ? c[e] : 0.f;
+                    }
                 }
                 *(f32x4 *)&S.B[bt[i]][bn[i]] = b;
                 if (NEEDC) *(f32x4 *)&S.C[bt[i]][bn[i]] = c;
             }
         }
         wave_lds_fence();
-        if (t0 + TT < row.t1) fetch(t0 + TT);
+        fetch_next(t0 + TT);
 #pragma unroll
         for (int tg = 0; tg < TT; tg += LPC) {
             float part[LPC];
 #pragma unroll
             for (int j = 0; j < LPC; j++) {
                 const int t = tg + j;
-                if (CKPT && t % kSelStored == 0 && t0 + t < row.t1) {
+                if (CKPT && t % kSelStored == 0 && t < left) {
                     const int64_t k = stored + (t0 - row.t0 + t) / kSelStored;
                     float *to = p.ckpt + stored_at(k, per, gt, wave, lane, NPL);
 #pragma unroll
@@ -196,22 +216,26 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
             if (MODE == FULL) S.y[tg + sub][ch] = transpose_sum<LPC>(part, lane);
         }
         wave_lds_fence();
-        if (MODE != FULL) continue;
+        if (MODE != FULL) return;
+        T *y0 = y + (int64_t)t0 * p.dim;
 #pragma unroll
         for (int i = 0; i < XE; i++) {
-            const int t = t0 + xt[i];
-            if ((XQ % 64 == 0 || lane + 64 * i < XQ) && t < row.t1) {
+            if ((XQ % 64 == 0 || lane + 64 * i < XQ) && (!TAIL || xt[i] < left)) {
                 f32x4 v = *(const f32x4 *)&S.y[xt[i]][xc[i] - c0];
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     v[e] += Dv[i][e] * xv[i][e];
                     if (z) v[e] *= zv[i][e] * sigmoid_hw(zv[i][e]);
                 }
-                store_quad<T, VEC>(y + (int64_t)t * p.dim, xc[i], p.dpg, v);
+                store_quad<T, VEC>(y0, xt[i], p.dim, xc[i], p.dpg, v);
             }
         }
         wave_lds_fence();
-    }
+    };
+    fetch_next(row.t0);
+    int t0 = row.t0;
+    for (; t0 + TT <= row.t1; t0 += TT) tile(t0, whole_tile);
+    if (t0 < row.t1) tile(t0, last_tile);
     if (!real) return;
     if (MODE == FULL && p.h_out && row.last)
         store_states<NPL, VEC>(h, p.h_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
@@ -346,7 +370,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     float Bv[NPL], Cv[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; i += 4) {
-        const quad<T> bq = load_quad<T, VEC>(B, n0 + i, p.N), cq = load_quad<T, VEC>(C, n0 + i, p.N);
+        const quad<T> bq = load_quad<T, VEC>(B, 0, 0, n0 + i, p.N), cq = load_quad<T, VEC>(C, 0, 0, n0 + i, p.N);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             Bv[i + e] = n0 + i + e < p.N ? to_f(bq[e]) : 0.f;

@@ -9,6 +9,8 @@
 // this pass walks those pieces backwards. A piece's states and decays are computed again and stay in
 // registers while its tokens are taken in reverse. The vector unit
 // bounds it: about 20 issue slots for every token, channel and state.
+#include <type_traits>
+
 #include "selective.h"
 
 namespace m3 {
@@ -102,7 +104,9 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     load_states<NPL, VEC>(A, p.A + (int64_t)d * p.N, n0, p.N);
 #pragma unroll
     for (int i = 0; i < NPL; i++) G[i] = dA[i] = 0.f;
-    if (p.seg_g) load_states<NPL, VEC>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
+    // lanes behind the group's last channel repeat it with no gradient: they add nothing to dB and dC
+    if (!real) {
+    } else if (p.seg_g) load_states<NPL, VEC>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
     else if (q.dh_out) load_states<NPL, VEC>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
 
     float H[NPL];                                               // the state that enters the segment
@@ -140,21 +144,29 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     float h0n[NSUB][NPL], s0n[NSUB];
 #pragma unroll
     for (int b = 0; b < NSUB; b++) s0n[b] = 0.f;
+    // the tile from t0 on (tokens behind the row's last repeat it)
     auto fetch = [&](int t0) {
+        const T *x0 = x + (int64_t)t0 * p.x_row, *d0 = dt + (int64_t)t0 * p.dt_row, *z0 = z + (int64_t)t0 * p.z_row,
+                *y0 = dy + (int64_t)t0 * p.dy_row, *B0 = B + (int64_t)t0 * p.B_row, *C0 = C + (int64_t)t0 * p.C_row;
+        auto load = [&](auto tail) {
+            constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
-        for (int i = 0; i < XE; i++) {
-            const int64_t t = min(t0 + xt[i], row.t1 - 1);
-            rx[i] = load_quad<T, VEC>(x + t * p.x_row, xc[i], p.dpg);
-            rd[i] = load_quad<T, VEC>(dt + t * p.dt_row, xc[i], p.dpg);
-            if (z) rz[i] = load_quad<T, VEC>(z + t * p.z_row, xc[i], p.dpg);
-            ry[i] = load_quad<T, VEC>(dy + t * p.dy_row, xc[i], p.dpg);
-        }
+            for (int i = 0; i < XE; i++) {
+                const int t = TAIL ? min(xt[i], row.t1 - 1 - t0) : xt[i];
+                rx[i] = load_quad<T, VEC>(x0, t, p.x_row, xc[i], p.dpg);
+                rd[i] = load_quad<T, VEC>(d0, t, p.dt_row, xc[i], p.dpg);
+                if (z) rz[i] = load_quad<T, VEC>(z0, t, p.z_row, xc[i], p.dpg);
+                ry[i] = load_quad<T, VEC>(y0, t, p.dy_row, xc[i], p.dpg);
+            }
 #pragma unroll
-        for (int i = 0; i < BE; i++) {
-            const int64_t t = min(t0 + bt[i], row.t1 - 1);
-            rB[i] = load_quad<T, VEC>(B + t * p.B_row, bn[i], p.N);
-            rC[i] = load_quad<T, VEC>(C + t * p.C_row, bn[i], p.N);
-        }
+            for (int i = 0; i < BE; i++) {
+                const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
+                rB[i] = load_quad<T, VEC>(B0, t, p.B_row, bn[i], p.N);
+                rC[i] = load_quad<T, VEC>(C0, t, p.C_row, bn[i], p.N);
+            }
+        };
+        if (t0 + TT <= row.t1) load(std::integral_constant<bool, false>());
+        else load(std::integral_constant<bool, true>());
 #pragma unroll
         for (int b = 0; b < NSUB; b++) {
             if (t0 + b * SUB >= row.t1) continue;
@@ -179,7 +191,7 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
         for (int b = 0; b < NSUB; b++)
 #pragma unroll
             for (int i = 0; i < NPL; i++)       // a segment's states were stored as from zero
-                h0s[b][i] = p.seg_h ? h0n[b][i] + __builtin_amdgcn_exp2f(s0n[b] * (A[i] * kLog2e)) * H[i] : h0n[b][i];
+                h0s[b][i] = !real ? 0.f : p.seg_h ? h0n[b][i] + __builtin_amdgcn_exp2f(s0n[b] * (A[i] * kLog2e)) * H[i] : h0n[b][i];
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const bool in = t0 + xt[i] < row.t1;
@@ -188,7 +200,7 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                 xv[i][e] = to_f(rx[i][e]);
                 zv[i][e] = z ? to_f(rz[i][e]) : 0.f;
                 // behind the sequence's end: a step of 0 and no gradient hand everything on unchanged
-                const float o = in ? to_f(ry[i][e]) : 0.f;
+                const float o = in && xc[i] + e < p.dpg ? to_f(ry[i][e]) : 0.f;
                 ov[i][e] = o;
                 const float raw = to_f(rd[i][e]) + biasv[i][e];
                 const float s = p.softplus ? softplus_hw(raw) : raw;
@@ -277,7 +289,6 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                 S.ds[b0 + tg + sub % GS][ch] = w;
             }
             // dB and dC: the sum over the wave's channels
-            const bool live = real;
 #pragma unroll
             for (int tb = 0; tb < SUB; tb += TV) {
                 float vals[V];
@@ -285,8 +296,8 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                 for (int t = 0; t < TV; t++)
 #pragma unroll
                     for (int i = 0; i < NPL; i++) {
-                        vals[t * VT + i] = live ? as[tb + t][i] : 0.f;
-                        vals[t * VT + NPL + i] = live ? hs[tb + t][i] : 0.f;
+                        vals[t * VT + i] = as[tb + t][i];
+                        vals[t * VT + NPL + i] = hs[tb + t][i];
                     }
                 channel_sum<V, 5, LOW>(vals, lane);
 #pragma unroll
@@ -323,10 +334,10 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                     dDv[i][e] += rv[i][e] * xv[i][e];
                     dbv[i][e] += od[e];
                 }
-                const int64_t at = (int64_t)t * p.dim + g * p.dpg;
-                store_quad<T, VEC>((T *)q.dx + at, xc[i], p.dpg, ox);
-                store_quad<T, VEC>((T *)q.ddt + at, xc[i], p.dpg, od);
-                if (q.dz) store_quad<T, VEC>((T *)q.dz + at, xc[i], p.dpg, oz);
+                const int64_t at = (int64_t)t0 * p.dim + g * p.dpg;
+                store_quad<T, VEC>((T *)q.dx + at, xt[i], p.dim, xc[i], p.dpg, ox);
+                store_quad<T, VEC>((T *)q.ddt + at, xt[i], p.dim, xc[i], p.dpg, od);
+                if (q.dz) store_quad<T, VEC>((T *)q.dz + at, xt[i], p.dim, xc[i], p.dpg, oz);
             }
         }
         wave_lds_fence();

@@ -198,6 +198,14 @@ def _rows(t, shape, lead, dtype, dev, name):
     return t.data_ptr(), row
 
 
+def _new(x, dtype):
+    """A new contiguous tensor of x's shape and device (empty_like costs half of empty)."""
+    import torch
+    if x.is_contiguous():
+        return torch.empty_like(x) if x.dtype is dtype else torch.empty_like(x, dtype=dtype)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
+
+
 def _token(x, dims, name="x"):
     """(token dtype code, torch dtype, device) of the leading token array."""
     if x.dim() != dims:
@@ -283,7 +291,7 @@ def mamba3_conv_fwd(x, weight, bias=None, *, silu=True, conv_in=None, cu_seqlens
     a, ty, dev, S, W = _conv_args(x, weight, bias, silu, conv_in, cu_seqlens)
     made = []
     if y is None:
-        y = torch.empty(x.shape, dtype=ty, device=dev)
+        y = _new(x, ty)
         made.append(y)
     if conv_out is None and want_state:
         conv_out = torch.empty((S, max(W - 1, 0), x.shape[2]), dtype=ty, device=dev)
@@ -301,7 +309,7 @@ def mamba3_conv_bwd(x, weight, bias=None, *, dy, dconv_out=None, silu=True, conv
     import torch
     a, ty, dev, S, W = _conv_args(x, weight, bias, silu, conv_in, cu_seqlens)
     D = x.shape[2]
-    g = dict(dx=torch.empty(x.shape, dtype=ty, device=dev), dweight=torch.empty_like(weight))
+    g = dict(dx=_new(x, ty), dweight=torch.empty_like(weight))
     if bias is not None:
         g["dbias"] = torch.empty_like(bias)
     if conv_in is not None:
@@ -336,7 +344,7 @@ def mamba3_conv_step(x, weight, bias=None, *, conv, silu=True, slots=None, y=Non
     W = weight.shape[1]
     made = []
     if y is None:
-        y = torch.empty((b, D), dtype=ty, device=dev)
+        y = _new(x, ty)
         made.append(y)
     sp, ns, states = _slots(slots, b, conv, dev)
     xp, xr = _rows(x, x.shape, 1, ty, dev, "x")
@@ -379,7 +387,7 @@ def mamba3_selective_scan_fwd(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, d
     a, ty, dev, S, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h_in, cu_seqlens)
     made = []
     if y is None:
-        y = torch.empty(x.shape, dtype=ty, device=dev)
+        y = _new(x, ty)
         made.append(y)
     if h_out is None and want_state:
         h_out = torch.empty((S, x.shape[2], N), dtype=torch.float32, device=dev)
@@ -400,13 +408,13 @@ def mamba3_selective_scan_bwd(x, dt, A, B, C, D=None, *, dy, dh_out=None, z=None
     import torch
     a, ty, dev, S, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h_in, cu_seqlens)
     dim = x.shape[2]
-    g = dict(dx=torch.empty(x.shape, dtype=ty, device=dev), ddt=torch.empty(x.shape, dtype=ty, device=dev),
-             dB=torch.empty(B.shape, dtype=ty, device=dev), dC=torch.empty(B.shape, dtype=ty, device=dev),
+    g = dict(dx=_new(x, ty), ddt=_new(x, ty),
+             dB=_new(B, ty), dC=_new(B, ty),
              dA=torch.empty_like(A))
     if D is not None:
         g["dD"] = torch.empty_like(D)
     if z is not None:
-        g["dz"] = torch.empty(x.shape, dtype=ty, device=dev)
+        g["dz"] = _new(x, ty)
     if dt_bias is not None:
         g["ddt_bias"] = torch.empty_like(dt_bias)
     if h_in is not None if want_dh_in is None else want_dh_in:
@@ -434,7 +442,7 @@ def mamba3_selective_step(x, dt, A, B, C, D=None, *, h, z=None, dt_bias=None, dt
     G, N = B.shape[1], B.shape[2]
     made = []
     if y is None:
-        y = torch.empty((b, dim), dtype=ty, device=dev)
+        y = _new(x, ty)
         made.append(y)
     f = torch.float32
     sp, ns, states = _slots(slots, b, h, dev)
@@ -472,13 +480,13 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
         _bad("nothing to compute: want_y is false and quant is None")
     out, made = {}, []
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rt, device=dev)
+        residual_out = _new(x, rt)
         made.append(residual_out)
     if residual_out is not None:
         out["residual"] = residual_out
     if want_y or y is not None:
         if y is None:
-            y = torch.empty(x.shape, dtype=ty, device=dev)
+            y = _new(x, ty)
             made.append(y)
         out["y"] = y
     qp = sp = 0
@@ -488,7 +496,7 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
             _bad(f"quant must be one of {sorted(_qtypes())}, got {quant!r}")
         qcode, qt = _qtypes()[quant]
         blocks = 1 if qblock <= 0 or qblock >= dim else -(-dim // qblock)
-        out["q"] = torch.empty(x.shape, dtype=qt, device=dev)
+        out["q"] = _new(x, qt)
         out["scale"] = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=dev)
         made += [out["q"], out["scale"]]
         qp, sp = out["q"].data_ptr(), out["scale"].data_ptr()
@@ -514,14 +522,14 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
     rows, rt = flat.shape[0], s.dtype
     if rt not in _dtypes():
         raise TypeError(f"s must be float32 or bfloat16, got {rt}")
-    g = dict(dresidual=torch.empty(s.shape, dtype=rt, device=dev))
+    g = dict(dresidual=_new(s, rt))
     made = [g["dresidual"]]
     dx = None
     if want_dx:
         if rt == ty:
             g["dx"] = g["dresidual"]
         else:
-            dx = g["dx"] = torch.empty(s.shape, dtype=ty, device=dev)
+            dx = g["dx"] = _new(s, ty)
             made.append(dx)
     if weight is not None:
         g["dweight"] = torch.empty_like(weight)
