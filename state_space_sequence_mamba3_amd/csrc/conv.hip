@@ -392,22 +392,28 @@ struct ConvStepParams {
 template <typename T, int W, int V>
 __global__ __launch_bounds__(256) void k_conv_step(ConvStepParams p, int chan_blocks) {
     const int b = blockIdx.x / chan_blocks, c = ((int)(blockIdx.x % chan_blocks) * 256 + threadIdx.x) * V;
+    if (c >= p.dim) return;
+    // what does not wait for the slot first: a step is a few memory latencies long
+    float w[V * W], bias[V], h[W][V], o[V];
+    const float *wp = p.w + (int64_t)c * W;
+#pragma unroll
+    for (int i = 0; i < V * W; i++) w[i] = wp[i];
+#pragma unroll
+    for (int e = 0; e < V; e++) bias[e] = p.bias ? p.bias[c + e] : 0.f;
+    load_vec<T, V>(h[W - 1], (const T *)p.x + b * p.x_row + c);
     int64_t slot = b;
     if (p.slots) {
         slot = p.slots[b];
         if (slot < 0 || slot >= p.nslots) return;
     }
-    if (c >= p.dim) return;
     T *st = (T *)p.conv + slot * (W - 1) * p.dim + c;
-    float h[W][V], o[V];
 #pragma unroll
     for (int j = 0; j + 1 < W; j++) load_vec<T, V>(h[j], st + (int64_t)j * p.dim);
-    load_vec<T, V>(h[W - 1], (const T *)p.x + b * p.x_row + c);
 #pragma unroll
     for (int e = 0; e < V; e++) {
-        float v = p.bias ? p.bias[c + e] : 0.f;
+        float v = bias[e];
 #pragma unroll
-        for (int j = 0; j < W; j++) v += p.w[(int64_t)(c + e) * W + j] * h[j][e];
+        for (int j = 0; j < W; j++) v += w[e * W + j] * h[j][e];
         o[e] = p.silu ? v * sigmoid_hw(v) : v;
     }
 #pragma unroll

@@ -353,19 +353,14 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     constexpr int CB = 256 / LPC;                       // channels of a workgroup
     const int b = blockIdx.x / tiles, d = (blockIdx.x % tiles) * CB + threadIdx.x / LPC;
     const int sub = threadIdx.x % LPC, n0 = sub * NPL;
-    int64_t slot = b;
-    if (p.slots) {
-        slot = p.slots[b];
-        if (slot < 0 || slot >= p.nslots) return;       // inactive row (uniform across the workgroup)
-    }
     if (d >= p.dim) return;                             // whole channels: a channel's lanes stay together
-    float *hs = p.h + (slot * p.dim + d) * p.N;
+    // what does not wait for the slot first: a step is a few memory latencies long
     float h[NPL], A2[NPL];
-    load_states<NPL, VEC>(h, hs, n0, p.N);
     load_states<NPL, VEC>(A2, p.A + (int64_t)d * p.N, n0, p.N);
     const int g = d / p.dpg;
     const T *B = (const T *)p.B + b * p.B_row + g * p.N, *C = (const T *)p.C + b * p.C_row + g * p.N;
-    const float x = to_f(((const T *)p.x)[b * p.x_row + d]);
+    const float x = to_f(((const T *)p.x)[b * p.x_row + d]), D = p.D ? p.D[d] : 0.f;
+    const float z = p.z ? to_f(((const T *)p.z)[b * p.z_row + d]) : 0.f;
     float s = to_f(((const T *)p.dt)[b * p.dt_row + d]) + (p.bias ? p.bias[d] : 0.f);
     float Bv[NPL], Cv[NPL];
 #pragma unroll
@@ -377,6 +372,13 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
             Cv[i + e] = n0 + i + e < p.N ? to_f(cq[e]) : 0.f;
         }
     }
+    int64_t slot = b;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.nslots) return;       // inactive row (uniform across the workgroup)
+    }
+    float *hs = p.h + (slot * p.dim + d) * p.N;
+    load_states<NPL, VEC>(h, hs, n0, p.N);
     if (p.softplus) s = softplus_hw(s);
     const float u = s * x;
     float acc = 0.f;
@@ -389,11 +391,8 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
 #pragma unroll
     for (int o = 1; o < LPC; o <<= 1) acc += __shfl_xor(acc, o, 64);
     if (sub == 0) {
-        float v = acc + (p.D ? p.D[d] * x : 0.f);
-        if (p.z) {
-            const float z = to_f(((const T *)p.z)[b * p.z_row + d]);
-            v *= z * sigmoid_hw(z);
-        }
+        float v = acc + D * x;
+        if (p.z) v *= z * sigmoid_hw(z);
         ((T *)p.y)[(int64_t)b * p.dim + d] = from_f<T>(v);
     }
 }

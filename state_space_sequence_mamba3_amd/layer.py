@@ -155,19 +155,18 @@ def _refuse(t, shape, dtype, dev, name):
         _bad(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        _bad(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        _bad(f"{name} must be on device {dev}, got {t.device}")
+    _bad(f"{name} must be contiguous; call .contiguous()")
 
 
 def _dense(t, shape, dtype, dev, name):
-    """Device address of a contiguous tensor of this shape and type, 0 for None."""
+    """Address of a contiguous tensor of this shape and type on device number `dev`, 0 for None."""
     if t is None:
         return 0
-    if t.shape != shape or t.dtype is not dtype or t.device != dev:
-        _refuse(t, shape, dtype, dev, name)
-    if not t.is_contiguous():
-        _bad(f"{name} must be contiguous; call .contiguous()")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, shape, dtype, dev, name)
 
 
 def _rows(t, shape, lead, dtype, dev, name):
@@ -175,7 +174,7 @@ def _rows(t, shape, lead, dtype, dev, name):
     dimensions count tokens."""
     if t is None:
         return 0, 0
-    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, shape, dtype, dev, name)
     if t.is_contiguous():
         return t.data_ptr(), 0
@@ -207,7 +206,7 @@ def _new(x, dtype):
 
 
 def _token(x, dims, name="x"):
-    """(token dtype code, torch dtype, device) of the leading token array."""
+    """(token dtype code, torch dtype, device number) of the leading token array."""
     if x.dim() != dims:
         _bad(f"{name} must have {dims} dimensions, got {tuple(x.shape)}")
     if not x.is_cuda:
@@ -216,7 +215,7 @@ def _token(x, dims, name="x"):
     code = _dtypes().get(ty)
     if code is None:
         raise TypeError(f"token inputs must be float32 or bfloat16, got {ty}")
-    return code, ty, x.device
+    return code, ty, x.get_device()
 
 
 def _packed(x, cu):
@@ -227,24 +226,24 @@ def _packed(x, cu):
     if cu.dim() != 1 or cu.numel() < 2 or x.shape[0] != 1:
         _bad("packed batches have x [1, tokens, ...] and cu_seqlens [nseq + 1]")
     nseq = cu.numel() - 1
-    return _dense(cu, cu.shape, torch.int32, x.device, "cu_seqlens"), nseq, nseq
+    return _dense(cu, cu.shape, torch.int32, x.get_device(), "cu_seqlens"), nseq, nseq
 
 
 def _call(op, args, dev, stream, made=()):
     """Runs an entry point on `stream` (None: the device's current one); `made`: tensors allocated here."""
     import torch
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream.device != dev:
-            _bad(f"the stream is on {stream.device}, the tensors are on {dev}")
+        if stream.device.index != dev:
+            _bad(f"the stream is on {stream.device}, the tensors are on device {dev}")
         raw = stream.cuda_stream
         for t in made:      # their memory is not given out again before the stream is done with it
             if t is not None:
                 t.record_stream(stream)
-    if dev.index == torch._C._cuda_getDevice():
+    if dev == torch._C._cuda_getDevice():
         st = op.run(args, raw)
     else:
         with torch.cuda.device(dev):
@@ -294,7 +293,7 @@ def mamba3_conv_fwd(x, weight, bias=None, *, silu=True, conv_in=None, cu_seqlens
         y = _new(x, ty)
         made.append(y)
     if conv_out is None and want_state:
-        conv_out = torch.empty((S, max(W - 1, 0), x.shape[2]), dtype=ty, device=dev)
+        conv_out = torch.empty((S, max(W - 1, 0), x.shape[2]), dtype=ty, device=x.device)
         made.append(conv_out)
     op = _op("conv")
     _call(op, op.pack(*a, _dense(y, x.shape, ty, dev, "y"),
@@ -390,7 +389,7 @@ def mamba3_selective_scan_fwd(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, d
         y = _new(x, ty)
         made.append(y)
     if h_out is None and want_state:
-        h_out = torch.empty((S, x.shape[2], N), dtype=torch.float32, device=dev)
+        h_out = torch.empty((S, x.shape[2], N), dtype=torch.float32, device=x.device)
         made.append(h_out)
     a += (_dense(y, x.shape, ty, dev, "y"), _dense(h_out, (S, x.shape[2], N), torch.float32, dev, "h_out"))
     op = _op("selective_scan")
@@ -418,7 +417,7 @@ def mamba3_selective_scan_bwd(x, dt, A, B, C, D=None, *, dy, dh_out=None, z=None
     if dt_bias is not None:
         g["ddt_bias"] = torch.empty_like(dt_bias)
     if h_in is not None if want_dh_in is None else want_dh_in:
-        g["dh_in"] = torch.empty((S, dim, N), dtype=torch.float32, device=dev)
+        g["dh_in"] = torch.empty((S, dim, N), dtype=torch.float32, device=x.device)
     yp, yr = _rows(dy, x.shape, 2, ty, dev, "dy")
     p = {k: v.data_ptr() for k, v in g.items()}
     q = (*a, 0, 0, 0, 0, yr, yp, _dense(dh_out, (S, dim, N), torch.float32, dev, "dh_out"),
@@ -497,7 +496,7 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
         qcode, qt = _qtypes()[quant]
         blocks = 1 if qblock <= 0 or qblock >= dim else -(-dim // qblock)
         out["q"] = _new(x, qt)
-        out["scale"] = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=dev)
+        out["scale"] = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=x.device)
         made += [out["q"], out["scale"]]
         qp, sp = out["q"].data_ptr(), out["scale"].data_ptr()
     xp, xr = _rows(flat, (rows, dim), 1, ty, dev, "x")

@@ -221,7 +221,7 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 def test_token_rows():
     """Which views count as token rows, and their distance."""
     from state_space_sequence_mamba3_amd.layer import _rows
-    cpu = torch.device("cpu")
+    cpu = -1
 
     def row(t, lead):
         return _rows(t, t.shape, lead, t.dtype, cpu, "t")[1]
