@@ -11,37 +11,50 @@ template <> struct QuadOf<float> { typedef f32x4 type; };
 template <> struct QuadOf<bf16> { typedef bf16x4 type; };
 template <typename T> using quad = typename QuadOf<T>::type;
 
-// Elements c0 .. c0 + 3 of row t behind `base` (rows of n elements, `row` apart). VEC: n, c0 and row
-// are multiples of 4 and base is aligned to a quad. Places behind a row's end repeat its last element
-// (or quad), so that every lane loads from inside the row; their results are never stored. `base` is
-// the same for all lanes and the offset has 32 bits, so that the load takes the address from scalar
-// registers and an offset that does not change from tile to tile.
-template <typename T, bool VEC>
+// How a kernel reads rows of token arrays in fours. ALIGNED: rows of a multiple of 4 elements, every
+// quad aligned to its size. ANY: rows of 4 elements or more, any length and alignment (global memory
+// takes a load of 8 or 16 bytes at any element); the quad that crosses a row's end is loaded from
+// its last 4 elements and shifted. ONE: rows of any length, element by element.
+enum Access { ONE, ANY, ALIGNED };
+
+template <typename T> struct LooseQuad { typedef T type __attribute__((ext_vector_type(4), aligned(sizeof(T)))); };
+
+// Elements c0 .. c0 + 3 of row t behind `base` (rows of n elements, `row` apart). Places behind a row's
+// end get other elements of the row or zero; their results are never stored. `base` is the same for
+// all lanes and the offset has 32 bits, so that the load takes the address from scalar registers and
+// an offset that does not change from tile to tile.
+template <typename T, Access ACC>
 __device__ __forceinline__ quad<T> load_quad(const T *base, int t, int64_t row, int c0, int n) {
     quad<T> v;
-    if constexpr (VEC) {
-        v = *(const quad<T> *)((const char *)base + (uint32_t)(t * (uint32_t)row + min(c0, n - 4)) * (uint32_t)sizeof(T));
+    const uint32_t r = t * (uint32_t)row;
+    if constexpr (ACC == ALIGNED) {
+        v = *(const quad<T> *)((const char *)base + (r + min(c0, n - 4)) * (uint32_t)sizeof(T));
+    } else if constexpr (ACC == ANY) {
+        typedef typename LooseQuad<T>::type loose;
+        const int at = min(c0, n - 4), over = c0 - at;
+        v = *(const loose *)((const char *)base + (r + at) * (uint32_t)sizeof(T));
+        if (over & 1) v = quad<T>{v[1], v[2], v[3], from_f<T>(0.f)};
+        if (over & 2) v = quad<T>{v[2], v[3], from_f<T>(0.f), from_f<T>(0.f)};
     } else {
 #pragma unroll
         for (int e = 0; e < 4; e++)
-            v[e] = *(const T *)((const char *)base + (uint32_t)(t * (uint32_t)row + min(c0 + e, n - 1)) * (uint32_t)sizeof(T));
+            v[e] = *(const T *)((const char *)base + (r + min(c0 + e, n - 1)) * (uint32_t)sizeof(T));
     }
     return v;
 }
-template <typename T, bool VEC>
+template <typename T, Access ACC>
 __device__ __forceinline__ void store_quad(T *base, int t, int64_t row, int c0, int n, f32x4 v) {
-    if constexpr (VEC) {
-        if (c0 < n) {
-            quad<T> o;
+    T *to = (T *)((char *)base + (uint32_t)(t * (uint32_t)row + c0) * (uint32_t)sizeof(T));
+    if (ACC == ALIGNED ? c0 < n : ACC == ANY && c0 + 4 <= n) {
+        quad<T> o;
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[e] = from_f<T>(v[e]);
-            *(quad<T> *)((char *)base + (uint32_t)(t * (uint32_t)row + c0) * (uint32_t)sizeof(T)) = o;
-        }
-    } else {
+        for (int e = 0; e < 4; e++) o[e] = from_f<T>(v[e]);
+        if (ACC == ALIGNED) *(quad<T> *)to = o;
+        else *(typename LooseQuad<T>::type *)to = o;
+    } else if (ACC != ALIGNED) {
 #pragma unroll
         for (int e = 0; e < 4; e++)
-            if (c0 + e < n)
-                *(T *)((char *)base + (uint32_t)(t * (uint32_t)row + c0 + e) * (uint32_t)sizeof(T)) = from_f<T>(v[e]);
+            if (c0 + e < n) to[e] = from_f<T>(v[e]);
     }
 }
 

@@ -120,7 +120,9 @@ __device__ __forceinline__ void store_states(const float (&h)[NPL], float *row, 
     }
 }
 
-// The lane arrangement of N states: as few lanes a channel as leave 4 or 8 states a lane.
+// The lane arrangement of N states: as few lanes a channel as leave 4 or 8 states a lane. The backward
+// keeps the states and decays of 8 tokens, and with 8 states a lane that takes more than 256
+// registers, one wave a SIMD at half its rate: it takes 4 a lane up to 64 states.
 #define M3_SEL_DISPATCH(N, CALL)              \
     do {                                      \
         if ((N) <= 4) CALL(4, 1);             \
@@ -130,25 +132,35 @@ __device__ __forceinline__ void store_states(const float (&h)[NPL], float *row, 
         else if ((N) <= 64) CALL(8, 8);       \
         else CALL(8, 16);                     \
     } while (0)
+#define M3_SELBWD_DISPATCH(N, CALL)           \
+    do {                                      \
+        if ((N) <= 4) CALL(4, 1);             \
+        else if ((N) <= 8) CALL(4, 2);        \
+        else if ((N) <= 16) CALL(4, 4);       \
+        else if ((N) <= 32) CALL(4, 8);       \
+        else if ((N) <= 64) CALL(4, 16);      \
+        else CALL(8, 16);                     \
+    } while (0)
 
 // Lanes a channel and states a lane of the arrangement above.
-inline void sel_shape(int N, int &npl, int &lpc) {
+inline void sel_shape(int N, bool back, int &npl, int &lpc) {
 #define M3_GO(NPL, LPC) npl = NPL, lpc = LPC
-    M3_SEL_DISPATCH(N, M3_GO);
+    if (back) M3_SELBWD_DISPATCH(N, M3_GO);
+    else M3_SEL_DISPATCH(N, M3_GO);
 #undef M3_GO
 }
 
 SelParams sel_params(const mamba3_selective_scan_args *a);
-bool sel_vec(const SelParams &p, int64_t es);
+Access sel_access(const SelParams &p, int64_t es);
 // Rows of a call (p.rows, nseg, seg_tokens): whole sequences, or segments where those leave the GPU
 // empty. True if segments; they need seg_bytes of workspace for the parts that `sel_segments` lays out.
-bool sel_plan(SelParams &p);
+bool sel_plan(SelParams &p, bool back);
 size_t sel_segment_bytes(const SelParams &p);
 void sel_segments(SelParams &p, char *ws);
 // Enqueue: a packed batch's segment table; the scan that writes p.ckpt (and segments' ends) and no
 // outputs; the chain over the segments of a sequence, forward and (p.seg_g) backward.
 void launch_sel_table(const SelParams &p, hipStream_t st);
-void launch_sel_stored(const SelParams &p, int32_t dtype, bool vec, hipStream_t st);
+void launch_sel_stored(const SelParams &p, int32_t dtype, Access acc, hipStream_t st);
 void launch_sel_chain(const SelParams &p, const float *dh_out, hipStream_t st);
 
 }  // namespace m3

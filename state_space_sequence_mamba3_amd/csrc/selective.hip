@@ -34,7 +34,7 @@ struct SelLds {
 // gradient that flows on to the one before it, sum_t (prod_{s <= t} a_s) C_t r_t.
 enum SelMode { FULL, PART, STORE, STORE_PART };
 
-template <typename T, int NPL, int LPC, bool VEC, int MODE>
+template <typename T, int NPL, int LPC, Access ACC, int MODE>
 __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     constexpr int CW = 64 / LPC, NP = NPL * LPC, TT = kSelTile;
     constexpr int XQ = TT * CW / 4, XE = (XQ + 63) / 64;      // quads of a channel tile, and of a lane
@@ -55,13 +55,13 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     const int d = g * p.dpg + min(c0 + ch, p.dpg - 1);        // the lane's channel in the recurrence
 
     float A2[NPL], h[NPL];
-    load_states<NPL, VEC>(A2, p.A + (int64_t)d * p.N, n0, p.N);
+    load_states<NPL, ACC == ALIGNED>(A2, p.A + (int64_t)d * p.N, n0, p.N);
 #pragma unroll
     for (int i = 0; i < NPL; i++) A2[i] *= kLog2e;
 #pragma unroll
     for (int i = 0; i < NPL; i++) h[i] = 0.f;
-    if (MODE == FULL && p.seg_h) load_states<NPL, VEC>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
-    else if (!ENDS && p.h_in) load_states<NPL, VEC>(h, p.h_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    if (MODE == FULL && p.seg_h) load_states<NPL, ACC == ALIGNED>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+    else if (!ENDS && p.h_in) load_states<NPL, ACC == ALIGNED>(h, p.h_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
     float sum = 0.f, prod[NPL], share[NPL];             // of the steps; of the decays; see STORE_PART
 #pragma unroll
     for (int i = 0; i < NPL; i++) {
@@ -105,16 +105,16 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const int t = TAIL ? min(xt[i], row.t1 - 1 - t0) : xt[i];
-            rx[i] = load_quad<T, VEC>(x0, t, p.x_row, xc[i], p.dpg);
-            rd[i] = load_quad<T, VEC>(d0, t, p.dt_row, xc[i], p.dpg);
-            if (z) rz[i] = load_quad<T, VEC>(z0, t, p.z_row, xc[i], p.dpg);
-            if (MODE == STORE_PART) ry[i] = load_quad<T, VEC>(y0, t, p.dy_row, xc[i], p.dpg);
+            rx[i] = load_quad<T, ACC>(x0, t, p.x_row, xc[i], p.dpg);
+            rd[i] = load_quad<T, ACC>(d0, t, p.dt_row, xc[i], p.dpg);
+            if (z) rz[i] = load_quad<T, ACC>(z0, t, p.z_row, xc[i], p.dpg);
+            if (MODE == STORE_PART) ry[i] = load_quad<T, ACC>(y0, t, p.dy_row, xc[i], p.dpg);
         }
 #pragma unroll
         for (int i = 0; i < BE; i++) {
             const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
-            rB[i] = load_quad<T, VEC>(B0, t, p.B_row, bn[i], p.N);
-            if (NEEDC) rC[i] = load_quad<T, VEC>(C0, t, p.C_row, bn[i], p.N);
+            rB[i] = load_quad<T, ACC>(B0, t, p.B_row, bn[i], p.N);
+            if (NEEDC) rC[i] = load_quad<T, ACC>(C0, t, p.C_row, bn[i], p.N);
         }
     };
     const std::integral_constant<bool, false> whole_tile;
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
                     v[e] += Dv[i][e] * xv[i][e];
                     if (z) v[e] *= zv[i][e] * sigmoid_hw(zv[i][e]);
                 }
-                store_quad<T, VEC>(y0, xt[i], p.dim, xc[i], p.dpg, v);
+                store_quad<T, ACC>(y0, xt[i], p.dim, xc[i], p.dpg, v);
             }
         }
         wave_lds_fence();
@@ -238,12 +238,12 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     if (t0 < row.t1) tile(t0, last_tile);
     if (!real) return;
     if (MODE == FULL && p.h_out && row.last)
-        store_states<NPL, VEC>(h, p.h_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+        store_states<NPL, ACC == ALIGNED>(h, p.h_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
     if (ENDS) {
-        store_states<NPL, VEC>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+        store_states<NPL, ACC == ALIGNED>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
         if (sub == 0) p.seg_s[(int64_t)r * p.dim + d] = sum;
     }
-    if (MODE == STORE_PART) store_states<NPL, VEC>(share, p.seg_g + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
+    if (MODE == STORE_PART) store_states<NPL, ACC == ALIGNED>(share, p.seg_g + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
 }
 
 // The segments of a packed batch in the order of their tokens, one at least a sequence; entries behind
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     float Bv[NPL], Cv[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; i += 4) {
-        const quad<T> bq = load_quad<T, VEC>(B, 0, 0, n0 + i, p.N), cq = load_quad<T, VEC>(C, 0, 0, n0 + i, p.N);
+        const quad<T> bq = load_quad<T, VEC ? ALIGNED : ONE>(B, 0, 0, n0 + i, p.N), cq = load_quad<T, VEC ? ALIGNED : ONE>(C, 0, 0, n0 + i, p.N);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             Bv[i + e] = n0 + i + e < p.N ? to_f(bq[e]) : 0.f;
@@ -425,52 +425,57 @@ SelParams sel_params(const mamba3_selective_scan_args *a) {
     return p;
 }
 
-// Whether every row can be read in quads: channels of a group and states in fours, rows and
-// pointers aligned to a quad. Otherwise every element is loaded by itself.
-bool sel_vec(const SelParams &p, int64_t es) {
-    return p.dpg % 4 == 0 && p.N % 4 == 0 && quads(p.x, p.x_row, es) && quads(p.dt, p.dt_row, es) &&
+// How the rows can be read: a group's channels and the states are the rows' lengths.
+Access sel_access(const SelParams &p, int64_t es) {
+    const bool al = p.dpg % 4 == 0 && p.N % 4 == 0 && quads(p.x, p.x_row, es) && quads(p.dt, p.dt_row, es) &&
            quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es) && quads(p.z, p.z_row, es) && quads(p.y, p.dim, es);
+    return al ? ALIGNED : p.dpg >= 4 && p.N >= 4 ? ANY : ONE;
 }
 
 template <typename T, int MODE>
-static void scan_go(const SelParams &p, bool vec, hipStream_t st) {
+static void scan_go(const SelParams &p, Access acc, hipStream_t st) {
 #define M3_GO(NPL, LPC)                                                                                          \
     do {                                                                                                         \
         const dim3 grid((uint32_t)p.rows * p.tiles * p.G);                                                       \
-        if (vec) hipLaunchKernelGGL((k_selscan<T, NPL, LPC, true, MODE>), grid, dim3(64 * kSelWaves), 0, st, p); \
-        else hipLaunchKernelGGL((k_selscan<T, NPL, LPC, false, MODE>), grid, dim3(64 * kSelWaves), 0, st, p);    \
+        const dim3 block(64 * kSelWaves);                                                                        \
+        if (acc == ALIGNED) hipLaunchKernelGGL((k_selscan<T, NPL, LPC, ALIGNED, MODE>), grid, block, 0, st, p);  \
+        else if (acc == ANY) hipLaunchKernelGGL((k_selscan<T, NPL, LPC, ANY, MODE>), grid, block, 0, st, p);     \
+        else hipLaunchKernelGGL((k_selscan<T, NPL, LPC, ONE, MODE>), grid, block, 0, st, p);                     \
     } while (0)
-    M3_SEL_DISPATCH(p.N, M3_GO);
+    if constexpr (MODE >= STORE) M3_SELBWD_DISPATCH(p.N, M3_GO);
+    else M3_SEL_DISPATCH(p.N, M3_GO);
 #undef M3_GO
 }
 
 // A wave's instructions issue every second slot at best when it is alone on its SIMD, so fewer than
-// 1024 waves (one a SIMD) run at less than half the vector unit's rate. Segments cost a first pass of
-// about three quarters of the scan and the chain, and pay below that. They are as long as leave 4096
-// waves, 64 tokens at least. Packed sequences are of unknown lengths, and the longest one decides
-// when nothing else is left to run: they are cut below 4096 waves.
-bool sel_plan(SelParams &p) {
+// 256 workgroups (one a CU, one wave a SIMD) run at less than half the vector unit's rate. Segments cost
+// a first pass of about two thirds of the scan and the chain, and pay below that. They are as long as
+// leave 1024 workgroups of the forward (four a CU; 512 of the backward, whose registers allow two),
+// 64 tokens at least: no workgroup waits for a place. Packed sequences are of unknown lengths, and the
+// longest one decides when nothing else is left to run: they are cut below 1024 workgroups too.
+bool sel_plan(SelParams &p, bool back) {
     int npl, lpc;
-    sel_shape(p.N, npl, lpc);
+    sel_shape(p.N, back, npl, lpc);
     const int cw = kSelWaves * (64 / lpc);
     p.tiles = (p.dpg + cw - 1) / cw;
     p.rows = p.nseq;
     p.nseg = 1;
     p.seg_tokens = p.seqlen;
-    const int64_t waves = (int64_t)p.tiles * p.G * kSelWaves;
-    if (p.nseq * waves >= (p.cu ? 4096 : 1024)) return false;
-    const int64_t want = (4096 + waves - 1) / waves;                  // segments of the batch
-    int64_t len = ((int64_t)p.total + want - 1) / want;
-    len = std::max<int64_t>((len + 15) / 16 * 16, 64);
+    const int64_t per = (int64_t)p.tiles * p.G;
+    if (p.nseq * per >= (p.cu ? 1024 : 256)) return false;
+    const int64_t most = (back ? 512 : 1024) / per;                   // rows in all
+    const int64_t cut = p.cu ? most - p.nseq : most / p.nseq;         // of which the tokens make this many
+    if (cut < 2) return false;
+    const int64_t tokens = p.cu ? p.total : p.seqlen;
+    const int64_t len = std::max<int64_t>(((tokens + cut - 1) / cut + 15) / 16 * 16, 64);
+    if (len >= tokens) return false;
+    p.seg_tokens = (int32_t)len;
     if (p.cu) {
-        if (len >= p.total) return false;
-        p.rows = (int32_t)(p.nseq + (p.total + len - 1) / len);
+        p.rows = (int32_t)(p.nseq + (tokens + len - 1) / len);
     } else {
-        if (len >= p.seqlen) return false;
-        p.nseg = (int32_t)((p.seqlen + len - 1) / len);
+        p.nseg = (int32_t)((tokens + len - 1) / len);
         p.rows = p.nseq * p.nseg;
     }
-    p.seg_tokens = (int32_t)len;
     return true;
 }
 
@@ -504,32 +509,33 @@ void launch_sel_chain(const SelParams &p, const float *dh_out, hipStream_t st) {
 
 mamba3_status launch_selective_scan(const mamba3_selective_scan_args *a, hipStream_t st) {
     SelParams p = sel_params(a);
-    const bool segments = sel_plan(p), f32 = a->dtype == MAMBA3_F32, vec = sel_vec(p, f32 ? 4 : 2);
+    const bool segments = sel_plan(p, false), f32 = a->dtype == MAMBA3_F32;
+    const Access acc = sel_access(p, f32 ? 4 : 2);
     if (segments) {
         sel_segments(p, (char *)a->workspace);
         launch_sel_table(p, st);
-        if (f32) scan_go<float, PART>(p, vec, st);
-        else scan_go<bf16, PART>(p, vec, st);
+        if (f32) scan_go<float, PART>(p, acc, st);
+        else scan_go<bf16, PART>(p, acc, st);
         launch_sel_chain(p, nullptr, st);
     }
-    if (f32) scan_go<float, FULL>(p, vec, st);
-    else scan_go<bf16, FULL>(p, vec, st);
+    if (f32) scan_go<float, FULL>(p, acc, st);
+    else scan_go<bf16, FULL>(p, acc, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 
 size_t selective_workspace_bytes(const mamba3_selective_scan_args *a) {
     SelParams p = sel_params(a);
-    return sel_plan(p) ? sel_segment_bytes(p) : 0;
+    return sel_plan(p, false) ? sel_segment_bytes(p) : 0;
 }
 
-void launch_sel_stored(const SelParams &p, int32_t dtype, bool vec, hipStream_t st) {
+void launch_sel_stored(const SelParams &p, int32_t dtype, Access acc, hipStream_t st) {
     const bool f32 = dtype == MAMBA3_F32;
     if (p.seg_h) {
-        if (f32) scan_go<float, STORE_PART>(p, vec, st);
-        else scan_go<bf16, STORE_PART>(p, vec, st);
+        if (f32) scan_go<float, STORE_PART>(p, acc, st);
+        else scan_go<bf16, STORE_PART>(p, acc, st);
     } else {
-        if (f32) scan_go<float, STORE>(p, vec, st);
-        else scan_go<bf16, STORE>(p, vec, st);
+        if (f32) scan_go<float, STORE>(p, acc, st);
+        else scan_go<bf16, STORE>(p, acc, st);
     }
 }
 

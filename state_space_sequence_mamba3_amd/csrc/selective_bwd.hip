@@ -77,7 +77,7 @@ template <int LPC> constexpr int kLow = LPC == 1 ? 0 : LPC == 2 ? 1 : LPC == 4 ?
 
 // The workgroups and their channels are k_selscan's; its four waves keep step, because dB and dC are
 // summed over them before they leave the workgroup.
-template <typename T, int NPL, int LPC, bool VEC>
+template <typename T, int NPL, int LPC, Access ACC>
 __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void k_selbwd(SelBwdParams q) {
     constexpr int CW = 64 / LPC, NP = NPL * LPC, SUB = kSelStored, TT = 64 / NPL, NSUB = TT / SUB;
     constexpr int XQ = TT * CW / 4, XE = (XQ + 63) / 64;
@@ -101,18 +101,18 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     const int d = g * p.dpg + min(c0 + ch, p.dpg - 1);
 
     float A[NPL], G[NPL], dA[NPL];
-    load_states<NPL, VEC>(A, p.A + (int64_t)d * p.N, n0, p.N);
+    load_states<NPL, ACC == ALIGNED>(A, p.A + (int64_t)d * p.N, n0, p.N);
 #pragma unroll
     for (int i = 0; i < NPL; i++) G[i] = dA[i] = 0.f;
     // lanes behind the group's last channel repeat it with no gradient: they add nothing to dB and dC
     if (!real) {
-    } else if (p.seg_g) load_states<NPL, VEC>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
-    else if (q.dh_out) load_states<NPL, VEC>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+    } else if (p.seg_g) load_states<NPL, ACC == ALIGNED>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
+    else if (q.dh_out) load_states<NPL, ACC == ALIGNED>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
 
     float H[NPL];                                               // the state that enters the segment
 #pragma unroll
     for (int i = 0; i < NPL; i++) H[i] = 0.f;
-    if (p.seg_h) load_states<NPL, VEC>(H, p.seg_h + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
+    if (p.seg_h) load_states<NPL, ACC == ALIGNED>(H, p.seg_h + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
 
     int xt[XE], xc[XE], bt[BE], bn[BE];
     f32x4 biasv[XE], Dv[XE], dDv[XE], dbv[XE];
@@ -153,16 +153,16 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
 #pragma unroll
             for (int i = 0; i < XE; i++) {
                 const int t = TAIL ? min(xt[i], row.t1 - 1 - t0) : xt[i];
-                rx[i] = load_quad<T, VEC>(x0, t, p.x_row, xc[i], p.dpg);
-                rd[i] = load_quad<T, VEC>(d0, t, p.dt_row, xc[i], p.dpg);
-                if (z) rz[i] = load_quad<T, VEC>(z0, t, p.z_row, xc[i], p.dpg);
-                ry[i] = load_quad<T, VEC>(y0, t, p.dy_row, xc[i], p.dpg);
+                rx[i] = load_quad<T, ACC>(x0, t, p.x_row, xc[i], p.dpg);
+                rd[i] = load_quad<T, ACC>(d0, t, p.dt_row, xc[i], p.dpg);
+                if (z) rz[i] = load_quad<T, ACC>(z0, t, p.z_row, xc[i], p.dpg);
+                ry[i] = load_quad<T, ACC>(y0, t, p.dy_row, xc[i], p.dpg);
             }
 #pragma unroll
             for (int i = 0; i < BE; i++) {
                 const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
-                rB[i] = load_quad<T, VEC>(B0, t, p.B_row, bn[i], p.N);
-                rC[i] = load_quad<T, VEC>(C0, t, p.C_row, bn[i], p.N);
+                rB[i] = load_quad<T, ACC>(B0, t, p.B_row, bn[i], p.N);
+                rC[i] = load_quad<T, ACC>(C0, t, p.C_row, bn[i], p.N);
             }
         };
         if (t0 + TT <= row.t1) load(std::integral_constant<bool, false>());
@@ -335,16 +335,16 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                     dbv[i][e] += od[e];
                 }
                 const int64_t at = (int64_t)t0 * p.dim + g * p.dpg;
-                store_quad<T, VEC>((T *)q.dx + at, xt[i], p.dim, xc[i], p.dpg, ox);
-                store_quad<T, VEC>((T *)q.ddt + at, xt[i], p.dim, xc[i], p.dpg, od);
-                if (q.dz) store_quad<T, VEC>((T *)q.dz + at, xt[i], p.dim, xc[i], p.dpg, oz);
+                store_quad<T, ACC>((T *)q.dx + at, xt[i], p.dim, xc[i], p.dpg, ox);
+                store_quad<T, ACC>((T *)q.ddt + at, xt[i], p.dim, xc[i], p.dpg, od);
+                if (q.dz) store_quad<T, ACC>((T *)q.dz + at, xt[i], p.dim, xc[i], p.dpg, oz);
             }
         }
         wave_lds_fence();
     }
     if (real) {
-        store_states<NPL, VEC>(dA, q.part_a + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
-        if (q.dh_in && row.first) store_states<NPL, VEC>(G, q.dh_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
+        store_states<NPL, ACC == ALIGNED>(dA, q.part_a + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
+        if (q.dh_in && row.first) store_states<NPL, ACC == ALIGNED>(G, q.dh_in + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
     }
     // dD and ddt_bias: the sum over the lanes that hold the same channels (token lanes), in LDS
     __syncthreads();
@@ -407,7 +407,7 @@ struct SelWs {
 SelWs sel_ws(const SelParams &p, bool segments) {
     SelWs w{};
     int npl, lpc;
-    sel_shape(p.N, npl, lpc);
+    sel_shape(p.N, true, npl, lpc);
     const int64_t per = (int64_t)p.tiles * p.G, stored = p.total / kSelStored + p.rows;
     auto al = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
     size_t o = 0;
@@ -423,15 +423,17 @@ SelWs sel_ws(const SelParams &p, bool segments) {
 }
 
 template <typename T>
-void bwd_go(SelBwdParams &q, bool vec, hipStream_t st) {
+void bwd_go(SelBwdParams &q, Access acc, hipStream_t st) {
     SelParams &p = q.f;
 #define M3_GO(NPL, LPC)                                                                                             \
     do {                                                                                                            \
         const dim3 grid((uint32_t)p.rows * p.tiles * p.G);                                                          \
-        if (vec) hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, true>), grid, dim3(64 * kSelWaves), 0, st, q);           \
-        else hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, false>), grid, dim3(64 * kSelWaves), 0, st, q);              \
+        const dim3 block(64 * kSelWaves);                                                                           \
+        if (acc == ALIGNED) hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, ALIGNED>), grid, block, 0, st, q);            \
+        else if (acc == ANY) hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, ANY>), grid, block, 0, st, q);               \
+        else hipLaunchKernelGGL((k_selbwd<T, NPL, LPC, ONE>), grid, block, 0, st, q);                               \
     } while (0)
-    if (p.rows > 0) M3_SEL_DISPATCH(p.N, M3_GO);
+    if (p.rows > 0) M3_SELBWD_DISPATCH(p.N, M3_GO);
 #undef M3_GO
     const int64_t bc = ((int64_t)p.total * p.G * 2 * p.N + 255) / 256, a = ((int64_t)p.dim * (p.N + 2) + 255) / 256;
     hipLaunchKernelGGL((k_selbwd_reduce<T>), dim3((uint32_t)(bc + a)), dim3(256), 0, st, q, (int)bc);
@@ -441,7 +443,7 @@ void bwd_go(SelBwdParams &q, bool vec, hipStream_t st) {
 
 size_t selective_bwd_workspace_bytes(const mamba3_selective_scan_bwd_args *b) {
     SelParams p = sel_params(&b->fwd);
-    const bool segments = sel_plan(p);
+    const bool segments = sel_plan(p, true);
     return sel_ws(p, segments).total;
 }
 
@@ -451,7 +453,7 @@ mamba3_status launch_selective_scan_bwd(const mamba3_selective_scan_bwd_args *b,
     SelParams &p = q.f;
     p.y = nullptr;
     p.h_out = nullptr;
-    const bool segments = sel_plan(p);
+    const bool segments = sel_plan(p, true);
     const SelWs w = sel_ws(p, segments);
     char *ws = (char *)b->workspace;
     if (segments) {
@@ -470,14 +472,15 @@ mamba3_status launch_selective_scan_bwd(const mamba3_selective_scan_bwd_args *b,
     q.dA = b->dA; q.dD = b->dD; q.dbias = b->ddt_bias; q.dh_in = b->dh_in;
     const int64_t es = b->fwd.dtype == MAMBA3_BF16 ? 2 : 4;
     auto quads = [&](const void *a, int64_t row) { return ((uintptr_t)a % (4 * es)) == 0 && row % 4 == 0; };
-    const bool vec = sel_vec(p, es) && quads(p.dy, p.dy_row) && quads(q.dx, 0) && quads(q.ddt, 0) && quads(q.dz, 0);
+    Access acc = sel_access(p, es);
+    if (acc == ALIGNED && !(quads(p.dy, p.dy_row) && quads(q.dx, 0) && quads(q.ddt, 0) && quads(q.dz, 0))) acc = ANY;
     if (p.rows > 0) {
         launch_sel_table(p, st);
-        launch_sel_stored(p, b->fwd.dtype, vec, st);
+        launch_sel_stored(p, b->fwd.dtype, acc, st);
         if (segments) launch_sel_chain(p, b->dh_out, st);
     }
-    if (b->fwd.dtype == MAMBA3_F32) bwd_go<float>(q, vec, st);
-    else bwd_go<bf16>(q, vec, st);
+    if (b->fwd.dtype == MAMBA3_F32) bwd_go<float>(q, acc, st);
+    else bwd_go<bf16>(q, acc, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
 
