@@ -17,6 +17,14 @@ template <typename T> using quad = typename QuadOf<T>::type;
 // its last 4 elements and shifted. ONE: rows of any length, element by element.
 enum Access { ONE, ANY, ALIGNED };
 
+// A token number that is the same for all lanes, in a scalar register and unknown to the compiler, which
+// would otherwise carry each lane's 64-bit addresses from tile to tile and add to every one of them.
+__device__ __forceinline__ int64_t scalar_token(int t) {
+    t = __builtin_amdgcn_readfirstlane(t);
+    asm("" : "+s"(t));
+    return t;
+}
+
 template <typename T> struct LooseQuad { typedef T type __attribute__((ext_vector_type(4), aligned(sizeof(T)))); };
 
 // Elements c0 .. c0 + 3 of row t behind `base` (rows of n elements, `row` apart). Places behind a row's
@@ -59,15 +67,13 @@ __device__ __forceinline__ void store_quad(T *base, int t, int64_t row, int c0, 
 }
 
 // e^v, log(1 + e^v) and 1 / (1 + e^-v) on the hardware's exp2, log2 and reciprocal (about one unit
-// in the last place each). log1p by its series where e^v < 1/16: 1 + e^v would round the small
-// term's low bits away, and the step sizes of a layer lie there.
+// in the last place each). log1p adds what 1 + e^v rounded away, over 1 + e^v (log(u + c) = log u +
+// c / u for a c far below u): the step sizes of a layer lie where that is most of the value.
 __device__ __forceinline__ float exp_hw(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
 __device__ __forceinline__ float softplus_hw(float v) {
-    const float w = exp_hw(v);
-    const float series =
-        w * (1.f + w * (-0.5f + w * (0.33333333f + w * (-0.25f + w * (0.2f + w * (-0.16666667f + w * 0.14285715f))))));
-    const float big = __builtin_amdgcn_logf(1.f + w) * 0.69314718056f;
-    return v > 20.f ? v : w < 0.0625f ? series : big;
+    const float w = exp_hw(v), u = 1.f + w, c = w - (u - 1.f);
+    const float l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, c * __builtin_amdgcn_rcpf(u));
+    return v > 20.f ? v : l;
 }
 __device__ __forceinline__ float sigmoid_hw(float v) { return __builtin_amdgcn_rcpf(1.f + exp_hw(-v)); }
 

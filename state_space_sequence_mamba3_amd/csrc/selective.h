@@ -76,6 +76,8 @@ __device__ __forceinline__ SelRow sel_row(const SelParams &p, int r) {
     o.t0 = __builtin_amdgcn_readfirstlane(o.t0);
     o.t1 = __builtin_amdgcn_readfirstlane(o.t1);
     o.seq = __builtin_amdgcn_readfirstlane(o.seq);
+    o.first = __builtin_amdgcn_readfirstlane(o.first);
+    o.last = __builtin_amdgcn_readfirstlane(o.last);
     return o;
 }
 

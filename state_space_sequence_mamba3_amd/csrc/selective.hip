@@ -40,7 +40,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     constexpr int XQ = TT * CW / 4, XE = (XQ + 63) / 64;      // quads of a channel tile, and of a lane
     constexpr int BQ = TT * NP / 4, BE = (BQ + 63) / 64;
     __shared__ SelLds<NP, CW> lds[kSelWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     SelLds<NP, CW> &S = lds[wave];
     const int per = p.tiles * p.G;
     const int r = blockIdx.x / per, gt = blockIdx.x % per, g = gt / p.tiles;
@@ -100,8 +100,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
     // the tile from t0 on; TAIL: it may end behind the row's last token, whose inputs are repeated then
     auto fetch = [&](int t0, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
-        const T *x0 = x + (int64_t)t0 * p.x_row, *d0 = dt + (int64_t)t0 * p.dt_row, *z0 = z + (int64_t)t0 * p.z_row,
-                *y0 = dy + (int64_t)t0 * p.dy_row, *B0 = B + (int64_t)t0 * p.B_row, *C0 = C + (int64_t)t0 * p.C_row;
+        const int64_t at = scalar_token(t0);
+        const T *x0 = x + at * p.x_row, *d0 = dt + at * p.dt_row, *z0 = z + at * p.z_row, *y0 = dy + at * p.dy_row,
+                *B0 = B + at * p.B_row, *C0 = C + at * p.C_row;
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const int t = TAIL ? min(xt[i], row.t1 - 1 - t0) : xt[i];
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
         }
         wave_lds_fence();
         if (MODE != FULL) return;
-        T *y0 = y + (int64_t)t0 * p.dim;
+        T *y0 = y + scalar_token(t0) * p.dim;
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             if ((XQ % 64 == 0 || lane + 64 * i < XQ) && (!TAIL || xt[i] < left)) {

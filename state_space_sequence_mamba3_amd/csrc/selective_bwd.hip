@@ -89,7 +89,7 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     constexpr int V = VT * TV;
     __shared__ SelBwdLds<NP, CW, TT> lds[kSelWaves];
     const SelParams &p = q.f;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     SelBwdLds<NP, CW, TT> &S = lds[wave];
     const int per = p.tiles * p.G;
     const int rw = blockIdx.x / per, gt = blockIdx.x % per, g = gt / p.tiles;
@@ -146,8 +146,9 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     for (int b = 0; b < NSUB; b++) s0n[b] = 0.f;
     // the tile from t0 on (tokens behind the row's last repeat it)
     auto fetch = [&](int t0) {
-        const T *x0 = x + (int64_t)t0 * p.x_row, *d0 = dt + (int64_t)t0 * p.dt_row, *z0 = z + (int64_t)t0 * p.z_row,
-                *y0 = dy + (int64_t)t0 * p.dy_row, *B0 = B + (int64_t)t0 * p.B_row, *C0 = C + (int64_t)t0 * p.C_row;
+        const int64_t at = scalar_token(t0);
+        const T *x0 = x + at * p.x_row, *d0 = dt + at * p.dt_row, *z0 = z + at * p.z_row, *y0 = dy + at * p.dy_row,
+                *B0 = B + at * p.B_row, *C0 = C + at * p.C_row;
         auto load = [&](auto tail) {
             constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
                     dDv[i][e] += rv[i][e] * xv[i][e];
                     dbv[i][e] += od[e];
                 }
-                const int64_t at = (int64_t)t0 * p.dim + g * p.dpg;
+                const int64_t at = scalar_token(t0) * p.dim + g * p.dpg;
                 store_quad<T, ACC>((T *)q.dx + at, xt[i], p.dim, xc[i], p.dpg, ox);
                 store_quad<T, ACC>((T *)q.ddt + at, xt[i], p.dim, xc[i], p.dpg, od);
                 if (q.dz) store_quad<T, ACC>((T *)q.dz + at, xt[i], p.dim, xc[i], p.dpg, oz);
