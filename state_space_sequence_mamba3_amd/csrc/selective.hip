@@ -183,38 +183,58 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
         }
         wave_lds_fence();
         fetch_next(t0 + TT);
+        // The operands of PF tokens come from LDS while the PF before are worked on.
+        constexpr int PF = 2;
+        struct Ops {
+            float s, u, r;
+            f32x4 b[NPL / 4], c[NPL / 4];
+        } op[2][PF];
+        auto operands = [&](int t, Ops &o) {
+            o.s = S.u[t][ch][0];
+            o.u = S.u[t][ch][1];
+            if (MODE == STORE_PART) o.r = S.y[t][ch];
 #pragma unroll
-        for (int tg = 0; tg < TT; tg += LPC) {
-            float part[LPC];
-#pragma unroll
-            for (int j = 0; j < LPC; j++) {
-                const int t = tg + j;
-                if (CKPT && t % kSelStored == 0 && t < left) {
-                    const int64_t k = stored + (t0 - row.t0 + t) / kSelStored;
-                    float *to = p.ckpt + stored_at(k, per, gt, wave, lane, NPL);
-#pragma unroll
-                    for (int i = 0; i < NPL; i += 4)
-                        *(f32x4 *)(to + i * 64) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
-                    if (MODE == STORE_PART && sub == 0)
-                        p.ckpt_s[((k * per + gt) * kSelWaves + wave) * CW + ch] = sum;
-                }
-                const float s = S.u[t][ch][0], u = S.u[t][ch][1];
-                const float rr = MODE == STORE_PART ? S.y[t][ch] : 0.f;
-                if (ENDS) sum += s;
-                float acc = 0.f;
-#pragma unroll
-                for (int i = 0; i < NPL; i++) {
-                    const float a = __builtin_amdgcn_exp2f(s * A2[i]);
-                    h[i] = a * h[i] + u * S.B[t][n0 + i];
-                    if (MODE == FULL) acc += h[i] * S.C[t][n0 + i];
-                    if (MODE == STORE_PART) {
-                        prod[i] *= a;
-                        share[i] += prod[i] * (rr * S.C[t][n0 + i]);
-                    }
-                }
-                part[j] = acc;
+            for (int i = 0; i < NPL / 4; i++) {
+                o.b[i] = *(const f32x4 *)&S.B[t][n0 + 4 * i];
+                if (NEEDC) o.c[i] = *(const f32x4 *)&S.C[t][n0 + 4 * i];
             }
-            if (MODE == FULL) S.y[tg + sub][ch] = transpose_sum<LPC>(part, lane);
+        };
+#pragma unroll
+        for (int k = 0; k < PF; k++) operands(k, op[0][k]);
+        float part[LPC];
+#pragma unroll
+        for (int t = 0; t < TT; t++) {
+            if (t % PF == 0) {
+                if (t + PF < TT) {
+#pragma unroll
+                    for (int k = 0; k < PF; k++) operands(t + PF + k, op[(t / PF + 1) & 1][k]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const Ops &o = op[t / PF & 1][t % PF];
+            if (CKPT && t % kSelStored == 0 && t < left) {
+                const int64_t k = stored + (t0 - row.t0 + t) / kSelStored;
+                float *to = p.ckpt + stored_at(k, per, gt, wave, lane, NPL);
+#pragma unroll
+                for (int i = 0; i < NPL; i += 4)
+                    *(f32x4 *)(to + i * 64) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+                if (MODE == STORE_PART && sub == 0)
+                    p.ckpt_s[((k * per + gt) * kSelWaves + wave) * CW + ch] = sum;
+            }
+            if (ENDS) sum += o.s;
+            float acc = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; i++) {
+                const float a = __builtin_amdgcn_exp2f(o.s * A2[i]);
+                h[i] = a * h[i] + o.u * o.b[i / 4][i % 4];
+                if (MODE == FULL) acc += h[i] * o.c[i / 4][i % 4];
+                if (MODE == STORE_PART) {
+                    prod[i] *= a;
+                    share[i] += prod[i] * (o.r * o.c[i / 4][i % 4]);
+                }
+            }
+            part[t % LPC] = acc;
+            if (MODE == FULL && t % LPC == LPC - 1) S.y[t - (LPC - 1) + sub][ch] = transpose_sum<LPC>(part, lane);
         }
         wave_lds_fence();
         if (MODE != FULL) return;
