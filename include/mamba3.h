@@ -423,8 +423,10 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  * that are multiples of 16 bytes are read fastest. Arrays without a `_row`
  * field are dense.
  * cu_seqlens, nseq and packed batches are as for mamba3_scan_fwd (entries
- * clamped to [0, seqlen]; batch 1); S = batch (padded) or nseq (packed);
- * batch * seqlen <= INT32_MAX.
+ * clamped to [0, seqlen]; batch 1), and may leave tokens out before the first
+ * and behind the last sequence, cu_seqlens[0] > 0 or cu_seqlens[nseq] < seqlen:
+ * their inputs take no part and their output rows are left as they were. S =
+ * batch (padded) or nseq (packed); batch * seqlen <= 2^30.
  */
 
 /* Short causal convolution over every channel by itself, width W = 2..8:
@@ -592,7 +594,7 @@ mamba3_status mamba3_selective_step(const mamba3_selective_step_args *args, void
  *              the block / largest value, 2^-126 at least (so a block of zeros
  *              has zeros for q). Both round from fp32 to the nearest, ties to
  *              even.
- * At least one of y and q is given. eps is finite and >= 0. Outputs overlap
+ * rows < 2^24. At least one of y and q is given. eps is finite and >= 0. Outputs overlap
  * neither each other nor any input, residual_out = residual aside. */
 typedef enum { MAMBA3_E4M3 = 0, MAMBA3_INT8 = 1 } mamba3_qtype;
 

@@ -24,16 +24,28 @@ struct ConvParams {
 
 constexpr int kTok = 16;                // tokens of a thread
 
-// The sequence that holds token t, and its tokens [a, b).
+// The sequence that holds token t, and its tokens [a, b). Tokens before the first sequence count as one
+// of their own with number -1; those behind the last have no end.
 struct SeqAt {
     int s, a, b;
 };
+// The tokens [first, second) that belong to sequences.
+__device__ __forceinline__ int2 live_tokens(const ConvParams &p) {
+    if (!p.cu) return make_int2(0, p.total);
+    return make_int2(min(max(p.cu[0], 0), p.total), min(max(p.cu[p.nseq], 0), p.total));
+}
 __device__ __forceinline__ SeqAt seq_of(const ConvParams &p, int t) {
     SeqAt q;
     if (!p.cu) {
         q.s = t / p.seqlen;
         q.a = q.s * p.seqlen;
         q.b = q.a + p.seqlen;
+        return q;
+    }
+    if (t < p.cu[0]) {
+        q.s = -1;
+        q.a = t;
+        q.b = min(p.cu[0], p.total);
         return q;
     }
     int lo = 0, hi = p.nseq - 1;        // the last sequence that starts at or before t
@@ -60,7 +72,7 @@ __device__ __forceinline__ SeqAt bounds_of(const ConvParams &p, int s) {
 // The sequence after token t reached the end of q (the next one that is not empty).
 __device__ __forceinline__ void next_seq(const ConvParams &p, int t, SeqAt &q) {
     while (t >= q.b) {
-        if (q.s + 1 >= p.nseq) {        // no token lies there in a valid table
+        if (q.s + 1 >= p.nseq) {        // behind the last sequence
             q.a = t;
             q.b = INT32_MAX;
             return;
@@ -108,7 +120,7 @@ __device__ __forceinline__ void hist_vec(const ConvParams &p, const SeqAt &q, in
     const int j = W - 1 + tau - q.a;
     if (tau >= q.a) {
         load_vec<T, V>(o, (const T *)p.x + (int64_t)tau * p.x_row + c);
-    } else if (p.conv_in && j >= 0) {
+    } else if (p.conv_in && j >= 0 && q.s >= 0) {
         load_vec<T, V>(o, (const T *)p.conv_in + ((int64_t)q.s * (W - 1) + j) * p.dim + c);
     } else {
 #pragma unroll
@@ -146,6 +158,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvParams p) {
 #pragma unroll
     for (int i = 0; i < kTok; i++)
         raw[i] = *(const typename RawVec<T, V>::type *)(x + (int64_t)min(t0 + i, p.total - 1) * p.x_row);
+    const int2 live = live_tokens(p);
     SeqAt q = seq_of(p, t0);
     next_seq(p, t0, q);
     float w[W][V], bias[V], win[W][V];   // win[j]: input t - W + 1 + j
@@ -177,7 +190,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvParams p) {
             for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
             o[e] = p.silu ? v * sigmoid_hw(v) : v;
         }
-        store_vec<T, V>((T *)p.y + (int64_t)t * p.dim + c, o);
+        if (t >= live.x && t < live.y) store_vec<T, V>((T *)p.y + (int64_t)t * p.dim + c, o);
     }
 }
 
@@ -227,6 +240,7 @@ struct ConvWalk {
         constexpr int U = 4;
         const T *x = (const T *)p.x + c, *dy = (const T *)p.dy + c;
         const int end = t1 + W - 1;
+        const int2 live = live_tokens(p);
         raw rx[U], rd[U];
         auto fetch = [&](int t) {
 #pragma unroll
@@ -267,7 +281,7 @@ struct ConvWalk {
 #pragma unroll
                         for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
                         win[W - 1][e] = raw_f<T, V>(cx[u], e);
-                        e_t[e] = raw_f<T, V>(cd[u], e);
+                        e_t[e] = INSIDE || (t >= live.x && t < live.y) ? raw_f<T, V>(cd[u], e) : 0.f;
                         if (p.silu) {
                             float v = bias[e];
 #pragma unroll
@@ -282,7 +296,7 @@ struct ConvWalk {
 #pragma unroll
                             for (int e = 0; e < V; e++) pend[j][e] += w[j][e] * e_t[e];
                         }
-                    if (t < t1) {
+                    if (t < t1 && (INSIDE || (t >= live.x && t < live.y))) {
 #pragma unroll
                         for (int e = 0; e < V; e++) {
                             db[e] += e_t[e];
@@ -290,7 +304,7 @@ struct ConvWalk {
                             for (int j = 0; j < W; j++) dw[j][e] += e_t[e] * win[j][e];
                         }
                         const int k = t - q.b + (W - 1);      // the token's row of conv_out, if it has one
-                        if (!INSIDE && p.dconv_out && k >= 0) {
+                        if (!INSIDE && p.dconv_out && k >= 0 && q.s >= 0) {
                             float o[V];
                             load_vec<T, V>(o, (const T *)p.dconv_out + ((int64_t)q.s * (W - 1) + k) * p.dim + c);
 #pragma unroll
@@ -299,7 +313,7 @@ struct ConvWalk {
                     }
                 }
                 const int tau = t - (W - 1);
-                if (tau >= t0) store_vec<T, V>((T *)p.dx + (int64_t)tau * p.dim + c, pend[0]);
+                if (tau >= t0 && (INSIDE || (tau >= live.x && tau < live.y))) store_vec<T, V>((T *)p.dx + (int64_t)tau * p.dim + c, pend[0]);
             }
         }
     }

@@ -78,7 +78,7 @@ mamba3_status check_batch(int32_t batch, int32_t seqlen, const int32_t *cu, int3
     if ((uintptr_t)cu & 3u) return MAMBA3_EALIGN;
     *S = cu ? nseq : batch;
     *T = (int64_t)batch * seqlen;
-    return *T <= INT32_MAX ? MAMBA3_OK : MAMBA3_EINVAL;
+    return *T <= (1 << 30) ? MAMBA3_OK : MAMBA3_EINVAL;   // (token numbers, and some past the end, in 32 bits)
 }
 
 // ---- convolution ----

@@ -374,10 +374,11 @@ __global__ __launch_bounds__(256) void k_selbwd_reduce(SelBwdParams q, int bc_bl
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [G][total][2][N]
         if (i >= n) return;
         const int64_t each = (int64_t)p.total * 2 * p.N, g = i / each, o = i % each;
+        const int64_t t = o / (2 * p.N), which = o / p.N % 2, m = o % p.N;
+        if (p.cu && (t < p.cu[0] || t >= p.cu[p.nseq])) return;       // a token of no sequence
         float s = 0.f;
 #pragma unroll 8
         for (int k = 0; k < p.tiles; k++) s += q.part_bc[(g * p.tiles + k) * each + o];
-        const int64_t t = o / (2 * p.N), which = o / p.N % 2, m = o % p.N;
         ((T *)(which ? q.dC : q.dB))[(t * p.G + g) * p.N + m] = from_f<T>(s);
         return;
     }
