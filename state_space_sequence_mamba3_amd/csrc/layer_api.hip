@@ -286,7 +286,8 @@ mamba3_status mamba3_rmsnorm_validate(const mamba3_rmsnorm_args *a) {
     if (!a) return MAMBA3_EINVAL;
     const mamba3_status st = norm_shape(a->rows, a->dim, a->dtype, a->residual_dtype, a->eps, a->x_row);
     if (st != MAMBA3_OK) return st;
-    if ((a->q == nullptr) != (a->qscale == nullptr) || (!a->q && !a->y)) return MAMBA3_EINVAL;
+    // (empty arrays may have no address)
+    if (a->rows > 0 && ((a->q == nullptr) != (a->qscale == nullptr) || (!a->q && !a->y))) return MAMBA3_EINVAL;
     int64_t blocks = 0;
     if (a->q) {
         if ((a->qtype != MAMBA3_E4M3 && a->qtype != MAMBA3_INT8) || a->qblock < 0) return MAMBA3_EINVAL;
@@ -319,7 +320,7 @@ mamba3_status mamba3_rmsnorm_bwd_validate(const mamba3_rmsnorm_bwd_args *b) {
     if (!b) return MAMBA3_EINVAL;
     mamba3_status st = norm_shape(b->rows, b->dim, b->dtype, b->residual_dtype, b->eps, b->dy_row);
     if (st != MAMBA3_OK) return st;
-    if (!b->dx && !b->dresidual) return MAMBA3_EINVAL;
+    if (b->rows > 0 && !b->dx && !b->dresidual) return MAMBA3_EINVAL;
     const int64_t es = esize(b->dtype), rs = esize(b->residual_dtype), M = b->rows * b->dim;
     const Arr in[] = {dense_of(b->s, M, rs, true), rows_of(b->dy, b->rows, b->dy_row, b->dim, es, true),
                       dense_of(b->dresidual_out, M, rs, false), dense_of(b->weight, b->dim, 4, false)};

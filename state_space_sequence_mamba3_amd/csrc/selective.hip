@@ -483,7 +483,7 @@ bool sel_plan(SelParams &p, bool back) {
     p.nseg = 1;
     p.seg_tokens = p.seqlen;
     const int64_t per = (int64_t)p.tiles * p.G;
-    if (p.nseq * per >= (p.cu ? 1024 : 256)) return false;
+    if (p.nseq == 0 || p.nseq * per >= (p.cu ? 1024 : 256)) return false;
     const int64_t most = (back ? 512 : 1024) / per;                   // rows in all
     const int64_t cut = p.cu ? most - p.nseq : most / p.nseq;         // of which the tokens make this many
     if (cut < 2) return false;

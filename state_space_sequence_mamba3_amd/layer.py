@@ -229,20 +229,21 @@ def _packed(x, cu):
     return _dense(cu, cu.shape, torch.int32, x.get_device(), "cu_seqlens"), nseq, nseq
 
 
-def _call(op, args, dev, stream, made=()):
-    """Runs an entry point on `stream` (None: the device's current one); `made`: tensors allocated here."""
+def _on(stream, x):
+    """The context of a call on `stream` (a torch stream or its address): its device's and stream's
+    allocations too, so that an output's memory is never one that another stream still uses."""
     import torch
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream.device.index != dev:
-            _bad(f"the stream is on {stream.device}, the tensors are on device {dev}")
-        raw = stream.cuda_stream
-        for t in made:      # their memory is not given out again before the stream is done with it
-            if t is not None:
-                t.record_stream(stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=x.device)
+    if stream.device != x.device:
+        _bad(f"the stream is on {stream.device}, the tensors are on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _call(op, args, dev):
+    """Runs an entry point on the device's current stream."""
+    import torch
+    raw = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch._C._cuda_getDevice():
         st = op.run(args, raw)
     else:
@@ -287,17 +288,18 @@ def mamba3_conv_fwd(x, weight, bias=None, *, silu=True, conv_in=None, cu_seqlens
     start (zeros if None). Returns (y, conv_out): conv_out [S, W-1, D] holds each sequence's last
     W - 1 inputs (None with want_state=False), what conv_in or mamba3_conv_step takes up."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_conv_fwd(x, weight, bias, silu=silu, conv_in=conv_in, cu_seqlens=cu_seqlens, y=y,
+                                   conv_out=conv_out, want_state=want_state)
     a, ty, dev, S, W = _conv_args(x, weight, bias, silu, conv_in, cu_seqlens)
-    made = []
     if y is None:
         y = _new(x, ty)
-        made.append(y)
     if conv_out is None and want_state:
         conv_out = torch.empty((S, max(W - 1, 0), x.shape[2]), dtype=ty, device=x.device)
-        made.append(conv_out)
     op = _op("conv")
-    _call(op, op.pack(*a, _dense(y, x.shape, ty, dev, "y"),
-                      _dense(conv_out, (S, W - 1, x.shape[2]), ty, dev, "conv_out")), dev, stream, made)
+    a = op.pack(*a, _dense(y, x.shape, ty, dev, "y"), _dense(conv_out, (S, W - 1, x.shape[2]), ty, dev, "conv_out"))
+    _call(op, a, dev)
     return y, conv_out
 
 
@@ -306,6 +308,10 @@ def mamba3_conv_bwd(x, weight, bias=None, *, dy, dconv_out=None, silu=True, conv
     """Gradients of mamba3_conv_fwd from dy and dconv_out [S, W-1, D] (None: zero): a dict of dx,
     dweight, dbias (with a bias) and dconv_in (with conv_in)."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_conv_bwd(x, weight, bias, dy=dy, dconv_out=dconv_out, silu=silu, conv_in=conv_in,
+                                   cu_seqlens=cu_seqlens, workspace=workspace)
     a, ty, dev, S, W = _conv_args(x, weight, bias, silu, conv_in, cu_seqlens)
     D = x.shape[2]
     g = dict(dx=_new(x, ty), dweight=torch.empty_like(weight))
@@ -319,7 +325,7 @@ def mamba3_conv_bwd(x, weight, bias=None, *, dy, dconv_out=None, silu=True, conv
          p.get("dbias", 0), p.get("dconv_in", 0))
     op = _op("conv_bwd")
     ws, wp, wn = _workspace(op, q, workspace, dev)
-    _call(op, op.pack(*q, wp, wn), dev, stream, [*g.values(), ws])
+    _call(op, op.pack(*q, wp, wn), dev)
     return g
 
 
@@ -336,22 +342,23 @@ def mamba3_conv_step(x, weight, bias=None, *, conv, silu=True, slots=None, y=Non
     place. With slots (int32 [batch] on the device) conv is a pool [nslots, W-1, D]; rows with a slot
     outside the pool are skipped (their y rows stay as they were). Returns y."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_conv_step(x, weight, bias, conv=conv, silu=silu, slots=slots, y=y)
     code, ty, dev = _token(x, 2)
     b, D = x.shape
     if weight.dim() != 2:
         _bad(f"weight must be [dim, width], got {tuple(weight.shape)}")
     W = weight.shape[1]
-    made = []
     if y is None:
         y = _new(x, ty)
-        made.append(y)
     sp, ns, states = _slots(slots, b, conv, dev)
     xp, xr = _rows(x, x.shape, 1, ty, dev, "x")
     op = _op("conv_step")
     a = op.pack(b, D, W, code, 1 if silu else 0, xr, xp, _dense(weight, (D, W), torch.float32, dev, "weight"),
                 _dense(bias, (D,), torch.float32, dev, "bias"), _dense(conv, (states, W - 1, D), ty, dev, "conv"),
                 _dense(y, (b, D), ty, dev, "y"), sp, ns)
-    _call(op, a, dev, stream, made)
+    _call(op, a, dev)
     return y
 
 
@@ -383,19 +390,20 @@ def mamba3_selective_scan_fwd(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, d
     [batch, seqlen, G, N] (N <= 128); A [dim, N], D, dt_bias [dim], h_in [S, dim, N] fp32. Returns (y,
     h_out [S, dim, N] or None with want_state=False)."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_selective_scan_fwd(x, dt, A, B, C, D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus,
+                                             h_in=h_in, cu_seqlens=cu_seqlens, y=y, h_out=h_out, want_state=want_state,
+                                             workspace=workspace)
     a, ty, dev, S, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h_in, cu_seqlens)
-    made = []
     if y is None:
         y = _new(x, ty)
-        made.append(y)
     if h_out is None and want_state:
         h_out = torch.empty((S, x.shape[2], N), dtype=torch.float32, device=x.device)
-        made.append(h_out)
     a += (_dense(y, x.shape, ty, dev, "y"), _dense(h_out, (S, x.shape[2], N), torch.float32, dev, "h_out"))
     op = _op("selective_scan")
     ws, wp, wn = _workspace(op, a, workspace, dev)
-    made.append(ws)
-    _call(op, op.pack(*a, wp, wn), dev, stream, made)
+    _call(op, op.pack(*a, wp, wn), dev)
     return y, h_out
 
 
@@ -405,6 +413,11 @@ def mamba3_selective_scan_bwd(x, dt, A, B, C, D=None, *, dy, dh_out=None, z=None
     ddt, dB, dC, dA, and dD, dz, ddt_bias, dh_in where the input exists (dh_in always with
     want_dh_in=True)."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_selective_scan_bwd(x, dt, A, B, C, D, dy=dy, dh_out=dh_out, z=z, dt_bias=dt_bias,
+                                             dt_softplus=dt_softplus, h_in=h_in, cu_seqlens=cu_seqlens,
+                                             want_dh_in=want_dh_in, workspace=workspace)
     a, ty, dev, S, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h_in, cu_seqlens)
     dim = x.shape[2]
     g = dict(dx=_new(x, ty), ddt=_new(x, ty),
@@ -424,7 +437,7 @@ def mamba3_selective_scan_bwd(x, dt, A, B, C, D=None, *, dy, dh_out=None, z=None
          *[p.get(k, 0) for k in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dh_in")])
     op = _op("selective_scan_bwd")
     ws, wp, wn = _workspace(op, q, workspace, dev)
-    _call(op, op.pack(*q, wp, wn), dev, stream, [*g.values(), ws])
+    _call(op, op.pack(*q, wp, wn), dev)
     return g
 
 
@@ -434,15 +447,17 @@ def mamba3_selective_step(x, dt, A, B, C, D=None, *, h, z=None, dt_bias=None, dt
     (fp32) is updated in place. With slots (int32 [batch] on the device) h is a pool [nslots, dim,
     N]; rows with a slot outside the pool are skipped (their y rows stay as they were). Returns y."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_selective_step(x, dt, A, B, C, D, h=h, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus,
+                                         slots=slots, y=y)
     code, ty, dev = _token(x, 2)
     b, dim = x.shape
     if B.dim() != 3 or A.dim() != 2:
         _bad(f"A must be [dim, dstate] and B [batch, groups, dstate], got {tuple(A.shape)}, {tuple(B.shape)}")
     G, N = B.shape[1], B.shape[2]
-    made = []
     if y is None:
         y = _new(x, ty)
-        made.append(y)
     f = torch.float32
     sp, ns, states = _slots(slots, b, h, dev)
     xp, xr = _rows(x, x.shape, 1, ty, dev, "x")
@@ -455,7 +470,7 @@ def mamba3_selective_step(x, dt, A, B, C, D=None, *, h, z=None, dt_bias=None, dt
                 _dense(A, (dim, N), f, dev, "A"), _dense(D, (dim,), f, dev, "D"),
                 _dense(dt_bias, (dim,), f, dev, "dt_bias"), _dense(h, (states, dim, N), f, dev, "h"),
                 _dense(y, (b, dim), ty, dev, "y"), sp, ns)
-    _call(op, a, dev, stream, made)
+    _call(op, a, dev)
     return y
 
 
@@ -468,6 +483,10 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
     and with quant "e4m3" or "int8" q [..., dim] and scale [..., blocks] (fp32, the norm is q * scale
     up to rounding): one scale for each qblock (32, 64, 128, 256) channels, or a row with qblock 0."""
     import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_rmsnorm_fwd(x, weight, residual=residual, eps=eps, y=y, residual_out=residual_out,
+                                      want_y=want_y, quant=quant, qblock=qblock)
     dim = x.shape[-1] if x.dim() else 0
     flat = x if x.dim() == 2 else x.reshape(-1, dim) if dim else x
     code, ty, dev = _token(flat, 2)
@@ -477,16 +496,14 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
         raise TypeError(f"residual must be float32 or bfloat16, got {rt}")
     if not want_y and quant is None:
         _bad("nothing to compute: want_y is false and quant is None")
-    out, made = {}, []
+    out = {}
     if residual is not None and residual_out is None:
         residual_out = _new(x, rt)
-        made.append(residual_out)
     if residual_out is not None:
         out["residual"] = residual_out
     if want_y or y is not None:
         if y is None:
             y = _new(x, ty)
-            made.append(y)
         out["y"] = y
     qp = sp = 0
     qcode = 0
@@ -497,14 +514,13 @@ def mamba3_rmsnorm_fwd(x, weight=None, *, residual=None, eps=1e-5, y=None, resid
         blocks = 1 if qblock <= 0 or qblock >= dim else -(-dim // qblock)
         out["q"] = _new(x, qt)
         out["scale"] = torch.empty((*x.shape[:-1], blocks), dtype=torch.float32, device=x.device)
-        made += [out["q"], out["scale"]]
         qp, sp = out["q"].data_ptr(), out["scale"].data_ptr()
     xp, xr = _rows(flat, (rows, dim), 1, ty, dev, "x")
     op = _op("rmsnorm")
     a = op.pack(rows, dim, code, _dtypes()[rt], qcode, qblock, eps, xr, xp,
                 _dense(residual, x.shape, rt, dev, "residual"), _dense(weight, (dim,), torch.float32, dev, "weight"),
                 _dense(residual_out, x.shape, rt, dev, "residual_out"), _dense(y, x.shape, ty, dev, "y"), qp, sp)
-    _call(op, a, dev, stream, made)
+    _call(op, a, dev)
     return out
 
 
@@ -513,6 +529,10 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
     and dresidual_out (of the residual output, s's type; None: zero): a dict of dresidual (s's type),
     dx (dy's type: the same tensor where the types are equal) and dweight (with a weight)."""
     import torch
+    if stream is not None:
+        with _on(stream, s):
+            return mamba3_rmsnorm_bwd(s, weight, dy=dy, dresidual_out=dresidual_out, eps=eps, want_dx=want_dx,
+                                      workspace=workspace)
     dim = s.shape[-1] if s.dim() else 0
     if dy.shape != s.shape:
         _bad(f"dy must have shape {tuple(s.shape)}, got {tuple(dy.shape)}")
@@ -522,17 +542,14 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
     if rt not in _dtypes():
         raise TypeError(f"s must be float32 or bfloat16, got {rt}")
     g = dict(dresidual=_new(s, rt))
-    made = [g["dresidual"]]
     dx = None
     if want_dx:
         if rt == ty:
             g["dx"] = g["dresidual"]
         else:
             dx = g["dx"] = _new(s, ty)
-            made.append(dx)
     if weight is not None:
         g["dweight"] = torch.empty_like(weight)
-        made.append(g["dweight"])
     yp, yr = _rows(flat, (rows, dim), 1, ty, dev, "dy")
     op = _op("rmsnorm_bwd")
     a = (rows, dim, code, _dtypes()[rt], eps, yr, _dense(s, s.shape, rt, dev, "s"), yp,
@@ -540,6 +557,5 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
          dx.data_ptr() if dx is not None else 0, g["dresidual"].data_ptr(),
          g["dweight"].data_ptr() if weight is not None else 0)
     ws, wp, wn = _workspace(op, a, workspace, dev)
-    made.append(ws)
-    _call(op, op.pack(*a, wp, wn), dev, stream, made)
+    _call(op, op.pack(*a, wp, wn), dev)
     return g

@@ -54,6 +54,10 @@ def spans(lead, cu):
     return list(zip(at[:-1], at[1:]))
 
 
+def stack(rows, *shape):
+    return torch.stack(rows) if rows else torch.zeros(0, *shape).double()
+
+
 def conv(x, w, bias, act, conv_in, cu, dy=None, dconv_out=None, mag=False):
     """y and conv_out, and with dy the gradients."""
     f = (lambda t: t.double().abs()) if mag else (lambda t: t.double())
@@ -84,9 +88,9 @@ def conv(x, w, bias, act, conv_in, cu, dy=None, dconv_out=None, mag=False):
             dh[b - a:] += f(dconv_out[i])
         dx[a:b] = dh[W - 1:]
         dins.append(dh[:W - 1])
-    r = dict(y=y.view(x.shape), conv_out=torch.stack(outs))
+    r = dict(y=y.view(x.shape), conv_out=stack(outs, W - 1, D))
     if dy is not None:
-        r.update(dx=dx.view(x.shape), dweight=dw, dbias=db, dconv_in=torch.stack(dins))
+        r.update(dx=dx.view(x.shape), dweight=dw, dbias=db, dconv_in=stack(dins, W - 1, D))
     return r
 
 
@@ -142,12 +146,12 @@ def scan(x, dt, A, B, C, D, z, bias, softplus, h_in, cu, dy=None, dh_out=None, m
             out["dD"] += r * fx[t]
             g = q
         dins.append(g)
-    r = dict(y=y.view(x.shape), h_out=torch.stack(hs))
+    r = dict(y=y.view(x.shape), h_out=stack(hs, dim, N))
     if dy is not None:
         for k in ("dx", "ddt", "dz"):
             out[k] = out[k].view(x.shape)
         out["dB"], out["dC"] = out["dB"].view(B.shape), out["dC"].view(B.shape)
-        r.update(out, dh_in=torch.stack(dins))
+        r.update(out, dh_in=stack(dins, dim, N))
     return r
 
 

@@ -29,11 +29,14 @@ def up(t):
     return t.to(device()) if t is not None else None
 
 
+# 700 sequences of 0 to about 10 tokens
+MANY = [0] + sorted(torch.randint(0, 901, (699,), generator=torch.Generator().manual_seed(7)).tolist()) + [900]
+
 # ----------------------------------------------------------------------------- convolution
 CONV = [  # batch, seqlen, dim, width, cu
     (2, 37, 64, 4, None), (1, 1, 8, 4, None), (3, 2, 40, 4, None), (1, 130, 1, 2, None), (2, 19, 7, 3, None),
     (1, 70, 24, 8, None), (2, 33, 512, 5, None), (1, 100, 72, 4, [0, 0, 1, 3, 3, 40, 41, 100, 100]),
-    (1, 64, 13, 6, [0, 2, 64]), (1, 5, 16, 7, [0, 1, 2, 3, 4, 5]), (1, 0, 8, 4, [0, 0, 0]), (2, 0, 8, 4, None),
+    (0, 9, 16, 4, None), (1, 900, 8, 4, MANY), (1, 64, 13, 6, [0, 2, 64]), (1, 5, 16, 7, [0, 1, 2, 3, 4, 5]), (1, 0, 8, 4, [0, 0, 0]), (2, 0, 8, 4, None),
 ]
 
 
@@ -105,7 +108,7 @@ SCAN = [  # batch, seqlen, dim, N, G, cu
     # long enough to run as segments, and enough sequences not to
     (1, 300, 40, 16, 1, None), (3, 200, 9, 16, 1, None), (2, 129, 36, 24, 2, None), (1, 150, 8, 128, 1, None),
     (1, 400, 20, 16, 1, [0, 0, 64, 65, 65, 300, 399, 400]), (1, 333, 6, 5, 2, [0, 200, 333]),
-    (64, 70, 256, 16, 1, None),
+    (64, 70, 256, 16, 1, None), (0, 9, 8, 16, 1, None), (1, 900, 8, 16, 1, MANY),
 ]
 
 
@@ -229,6 +232,17 @@ def test_selective_steps_continue_a_prompt(case, dtype):
     assert bool((pool[rest] == 5.0).all())
 
 
+@pytest.mark.parametrize("case", [(64, 20, 256, 16, 1, None), (2, 300, 24, 16, 1, None), (1, 300, 24, 16, 1, [0, 100, 300])])
+def test_selective_scan_state_in_place(case):
+    """h_out = h_in, in one pass and in segments."""
+    a, kw, _, _, cu = scan_inputs(case, F32, True, seed=5)
+    a, kw = dev(a), dev(kw)
+    y, h = m3.mamba3_selective_scan_fwd(**a, **kw, cu_seqlens=up(cu))
+    own = kw["h_in"].clone()
+    y2, h2 = m3.mamba3_selective_scan_fwd(**a, **{**kw, "h_in": own}, h_out=own, cu_seqlens=up(cu))
+    assert h2 is own and torch.equal(y, y2) and torch.equal(h, own)
+
+
 def test_selective_scan_views():
     """x and z as the halves of one projection, B and C as slices of another, equal dense inputs."""
     g = gen(9)
@@ -267,7 +281,7 @@ def test_selective_scan_extremes():
 
 # ----------------------------------------------------------------------------- RMS norm
 NORM = [(1, 1), (5, 64), (3, 40), (7, 513), (4, 1000), (2, 2048), (2100, 1024), (2050, 2000), (3, 4100), (2, 8192),
-        (2, 8200), (3, 9001)]
+        (2, 8200), (3, 9001), (4500, 200), (0, 64), (0, 9000)]
 
 
 def norm_inputs(rows, dim, dtype, rt, seed=0):
@@ -297,8 +311,8 @@ def test_rmsnorm(rows, dim, types):
 @pytest.mark.parametrize("quant", ["e4m3", "int8"])
 def test_rmsnorm_quantised(rows, dim, qblock, quant):
     x, res, w, _ = norm_inputs(rows, dim, BF16, BF16)
-    x[0] = 0
-    res[0] = 0                                       # a row of zeros
+    x[:1] = 0
+    res[:1] = 0                                      # a row of zeros
     note(f"rmsnorm {quant} {rows}x{dim} block {qblock}")
     _, v = R.norm(x, res, w, 1e-5)
     got = m3.mamba3_rmsnorm_fwd(up(x), up(w), residual=up(res), eps=1e-5, want_y=False, quant=quant, qblock=qblock)
@@ -321,8 +335,8 @@ def test_rmsnorm_quantised(rows, dim, qblock, quant):
     else:
         half = torch.tensor(0.5).double()
     assert bool(((q - ideal).abs() <= half * (1 + 1e-6) + err * 2).all())
-    assert float(q.abs().max()) <= top
-    assert bool((q[0] == 0).all())
+    assert bool((q.abs() <= top).all())
+    assert bool((q[:1] == 0).all())
 
 
 def test_rmsnorm_in_place_views_and_both_outputs():
@@ -336,6 +350,15 @@ def test_rmsnorm_in_place_views_and_both_outputs():
     assert torch.equal(got["y"], other["y"]) and got["scale"].shape == (6, 3, 2)
     alone = m3.mamba3_rmsnorm_fwd(x, w, residual=keep, want_y=False, quant="e4m3", qblock=32)
     assert torch.equal(alone["q"].view(torch.uint8), got["q"].view(torch.uint8))
+
+
+def test_rmsnorm_first_layer():
+    """A residual stream begun: residual_out without a residual is x in its type."""
+    x, _, w, _ = norm_inputs(6, 72, BF16, None)
+    out = torch.empty(6, 72, device=device())
+    got = m3.mamba3_rmsnorm_fwd(up(x), up(w), residual_out=out)
+    assert got["residual"] is out and torch.equal(out.cpu(), x.float())
+    assert torch.equal(got["y"], m3.mamba3_rmsnorm_fwd(up(x), up(w))["y"])
 
 
 @pytest.mark.parametrize("types", [(F32, F32), (BF16, F32), (BF16, BF16)])

@@ -122,7 +122,9 @@ CASES = [
     (conv_bwd, dict(dconv_in=None, dbias=None, dconv_out=None), OK), (conv_step, {}, OK), (conv_step, dict(batch=0), OK),
     (conv_step, dict(slots=fake(20), nslots=9), OK), (scan, {}, OK), (scan, dict(h_out=fake(9)), OK),
     (scan, dict(z=None, D=None, dt_bias=None, h_in=None, h_out=None), OK), (scan, dict(dstate=128), OK),
-    (scan, dict(dstate=1, x_row=40, B_row=50), OK), (scan_bwd, {}, OK), (scan_bwd, dict(dz=None, dD=None, dh_in=None), OK),
+    (scan, dict(dstate=1, x_row=40, B_row=50), OK), (scan, dict(batch=0), OK), (scan_bwd, dict(fwd_batch=0), OK),
+    (scan, dict(seqlen=0), OK), (scan_bwd, dict(fwd_seqlen=0), OK), (conv_bwd, dict(fwd_batch=0), OK),
+    (norm_bwd, dict(rows=0), OK), (scan, dict(batch=1, seqlen=1 << 20, dim=2), OK), (norm, dict(rows=0, y=None, q=None, qscale=None), OK), (scan_bwd, {}, OK), (scan_bwd, dict(dz=None, dD=None, dh_in=None), OK),
     (step, {}, OK), (step, dict(batch=0), OK), (norm, {}, OK), (norm, dict(q=None, qscale=None), OK),
     (norm, dict(y=None), OK), (norm, dict(residual_out=fake(2)), OK), (norm, dict(rows=0), OK), (norm, dict(qblock=0), OK),
     (norm, dict(qblock=300), OK), (norm, dict(qtype=m3.MAMBA3_INT8, qblock=32), OK), (norm_bwd, {}, OK),
