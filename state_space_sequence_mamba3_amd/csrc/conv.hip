@@ -7,6 +7,8 @@
 // - 1 rows before a thread's first token are read twice (mostly from the caches): 3 of 16 at width 4.
 // Sequence starts inside a thread's tokens reset the registers to conv_in's rows (a branch that is
 // uniform across the wave, which shares its tokens).
+#include <type_traits>
+
 #include "layer.h"
 
 namespace m3 {
@@ -170,28 +172,36 @@ __global__ __launch_bounds__(256) void k_conv(ConvParams p) {
     }
 #pragma unroll
     for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t0 - W + j, c, win[j]);
+    // INSIDE: the thread's tokens lie in one sequence, and nothing is asked of each
+    auto walk = [&](auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
 #pragma unroll
-    for (int i = 0; i < kTok; i++) {
-        const int t = t0 + i;
-        if (t >= p.total) break;
-        if (t >= q.b) {
-            next_seq(p, t, q);
+        for (int i = 0; i < kTok; i++) {
+            const int t = t0 + i;
+            if (!INSIDE) {
+                if (t >= live.y) break;
+                if (t >= q.b) {
+                    next_seq(p, t, q);
 #pragma unroll
-            for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
+                    for (int j = 1; j < W; j++) hist_vec<T, W, V>(p, q, t - W + j, c, win[j]);
+                }
+            }
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+#pragma unroll
+                for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
+                win[W - 1][e] = raw_f<T, V>(raw[i], e);
+                float v = bias[e];
+#pragma unroll
+                for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
+                o[e] = p.silu ? v * sigmoid_hw(v) : v;
+            }
+            if (INSIDE || t >= live.x) store_vec<T, V>((T *)p.y + (int64_t)t * p.dim + c, o);
         }
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; e++) {
-#pragma unroll
-            for (int j = 0; j + 1 < W; j++) win[j][e] = win[j + 1][e];
-            win[W - 1][e] = raw_f<T, V>(raw[i], e);
-            float v = bias[e];
-#pragma unroll
-            for (int j = 0; j < W; j++) v += w[j][e] * win[j][e];
-            o[e] = p.silu ? v * sigmoid_hw(v) : v;
-        }
-        if (t >= live.x && t < live.y) store_vec<T, V>((T *)p.y + (int64_t)t * p.dim + c, o);
-    }
+    };
+    if (q.s >= 0 && t0 + kTok <= min(q.b, live.y)) walk(std::integral_constant<bool, true>());
+    else walk(std::integral_constant<bool, false>());
 }
 
 // SiLU's derivative at v
