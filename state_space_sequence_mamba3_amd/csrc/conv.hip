@@ -558,7 +558,7 @@ mamba3_status launch_conv_step(const mamba3_conv_step_args *a, hipStream_t st) {
         if (wide(4, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<float, 4>(p, a->width, st);
         else conv_step_go<float, 1>(p, a->width, st);
     } else {
-        if (wide(2, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<bf16, 8>(p, a->width, st);
+        if (wide(2, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<bf16, 4>(p, a->width, st);
         else conv_step_go<bf16, 1>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;

@@ -23,6 +23,10 @@ struct NormParams {
     float eps;
 };
 
+// 8 values at any element: global memory takes loads and stores of 8 or 16 bytes there, in one
+// instruction each, which rows of odd lengths (VEC false) use up to their last piece.
+template <typename T> struct Loose8 { typedef T type __attribute__((ext_vector_type(8), aligned(sizeof(T)))); };
+
 // 8 values of a row from column c on; zeros behind the row's end
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(float (&o)[kNV], const T *row, int c, int n) {
@@ -44,6 +48,10 @@ __device__ __forceinline__ void load8(float (&o)[kNV], const T *row, int c, int 
 #pragma unroll
             for (int e = 0; e < 8; e++) o[e] = 0.f;
         }
+    } else if (c + 8 <= n) {
+        const typename Loose8<T>::type v = *(const typename Loose8<T>::type *)(row + c);
+#pragma unroll
+        for (int e = 0; e < 8; e++) o[e] = to_f(v[e]);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; e++) o[e] = c + e < n ? to_f(row[c + e]) : 0.f;
@@ -63,6 +71,11 @@ __device__ __forceinline__ void store8(T *row, int c, int n, const float (&o)[kN
                 *(f32x4 *)(row + c + 4) = f32x4{o[4], o[5], o[6], o[7]};
             }
         }
+    } else if (c + 8 <= n) {
+        typename Loose8<T>::type v;
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = from_f<T>(o[e]);
+        *(typename Loose8<T>::type *)(row + c) = v;
     } else {
 #pragma unroll
         for (int e = 0; e < 8; e++)
@@ -141,6 +154,9 @@ __device__ __forceinline__ void store_q(const NormParams &p, int64_t row, int c,
     uint8_t *q = (uint8_t *)p.q + row * p.dim + c;
     if constexpr (VEC) {
         *(uint2 *)q = make_uint2(w[0], w[1]);
+    } else if (c + 8 <= p.dim) {
+        typedef uint32_t loose __attribute__((ext_vector_type(2), aligned(1)));
+        *(loose *)q = loose{w[0], w[1]};
     } else {
 #pragma unroll
         for (int e = 0; e < kNV; e++)
@@ -239,6 +255,8 @@ __device__ __forceinline__ typename Raw8<T>::type raw8(const T *row, int c, int 
     for (int e = 0; e < 8; e++) v[e] = from_f<T>(0.f);
     if constexpr (VEC) {
         if (c < n) v = *(const typename Raw8<T>::type *)(row + c);
+    } else if (c + 8 <= n) {
+        v = *(const typename Loose8<T>::type *)(row + c);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; e++)
@@ -385,9 +403,11 @@ __global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     float s = 0.f;
-    if (c < p.dim)
+    if (c < p.dim) {
+#pragma unroll 8
         for (int64_t i = wave; i < p.rows; i += 4)
             s += to_f(((const T *)p.dy)[i * p.dy_row + c]) * to_f(((const RT *)p.x)[i * p.dim + c]) * p.part[i];
+    }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && c < p.dim) p.dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);

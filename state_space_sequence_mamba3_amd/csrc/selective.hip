@@ -8,6 +8,7 @@
 // an exponential (two issue slots), two products and two fused adds for every token, channel and
 // state, on the vector unit. Where N is 16 that is 96 slots for 8 bytes of bf16, so the vector
 // unit and not the memory bounds the scan.
+#include <cmath>
 #include <type_traits>
 
 #include "selective.h"
@@ -472,8 +473,9 @@ static void scan_go(const SelParams &p, Access acc, hipStream_t st) {
 // 256 workgroups (one a CU, one wave a SIMD) run at less than half the vector unit's rate. Segments cost
 // a first pass of about two thirds of the scan and the chain, and pay below that. They are as long as
 // leave 1024 workgroups of the forward (four a CU; 512 of the backward, whose registers allow two),
-// 64 tokens at least: no workgroup waits for a place. Packed sequences are of unknown lengths, and the
-// longest one decides when nothing else is left to run: they are cut below 1024 workgroups too.
+// sqrt(2/3 of the sequence) and 64 tokens at least: no workgroup waits for a place. Packed sequences are of unknown lengths, and the
+// longest one decides when nothing else is left to run: they are cut below 1024 workgroups too, into
+// pieces of their mean length at most.
 bool sel_plan(SelParams &p, bool back) {
     int npl, lpc;
     sel_shape(p.N, back, npl, lpc);
@@ -485,10 +487,14 @@ bool sel_plan(SelParams &p, bool back) {
     const int64_t per = (int64_t)p.tiles * p.G;
     if (p.nseq == 0 || p.nseq * per >= (p.cu ? 1024 : 256)) return false;
     const int64_t most = (back ? 512 : 1024) / per;                   // rows in all
-    const int64_t cut = p.cu ? most - p.nseq : most / p.nseq;         // of which the tokens make this many
+    const int64_t cut = p.cu ? std::max<int64_t>(most - p.nseq, p.nseq) : most / p.nseq;   // of these by length
     if (cut < 2) return false;
     const int64_t tokens = p.cu ? p.total : p.seqlen;
-    const int64_t len = std::max<int64_t>(((tokens + cut - 1) / cut + 15) / 16 * 16, 64);
+    // a token of a lone wave takes about 0.2 us in the two passes and a segment 0.15 us in the chain:
+    // segments of sqrt(2/3 tokens) balance the two (one sequence of 65536 tokens and 64 channels in
+    // 1024, 313 segments: 281, 118 us)
+    const int64_t least = std::max<int64_t>((int64_t)std::sqrt(tokens * (2. / 3.)), 64);
+    const int64_t len = (std::max((tokens + cut - 1) / cut, least) + 15) / 16 * 16;
     if (len >= tokens) return false;
     p.seg_tokens = (int32_t)len;
     if (p.cu) {
