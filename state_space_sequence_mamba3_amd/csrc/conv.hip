@@ -7,6 +7,9 @@
 // - 1 rows before a thread's first token are read twice (mostly from the caches): 3 of 16 at width 4.
 // Sequence starts inside a thread's tokens reset the registers to conv_in's rows (a branch that is
 // uniform across the wave, which shares its tokens).
+//
+// 8 x 4096 tokens of 4096 channels, width 4, bf16: 112 us, 4.8 TB/s of what has to move (a large copy runs at
+// 4.94); the backward of 16384 x 4096 packed tokens 105 us, 3.8 TB/s; a step of 128 rows 4.1 us.
 #include <type_traits>
 
 #include "layer.h"
@@ -413,6 +416,8 @@ struct ConvStepParams {
     int32_t batch, nslots, dim, silu;
 };
 
+// One token. Four channels a thread: 16-byte pieces of bf16 (eight channels, 32 weights a thread) took 21.5
+// us at 1024 x 4096 where these take 15.2.
 template <typename T, int W, int V>
 __global__ __launch_bounds__(256) void k_conv_step(ConvStepParams p, int chan_blocks) {
     const int b = blockIdx.x / chan_blocks, c = ((int)(blockIdx.x % chan_blocks) * 256 + threadIdx.x) * V;

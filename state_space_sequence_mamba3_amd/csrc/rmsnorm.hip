@@ -7,6 +7,9 @@
 // sum and its outputs (rows of more than 8192 values are read twice), and everything a row needs
 // is written in the same pass. A lane holds 8 consecutive values, so a wave's load covers 1 KB of
 // bf16, and a scale's block of 32 .. 256 values lies in 4 .. 32 consecutive lanes.
+//
+// 32768 x 2048, bf16 with an fp32 residual: 156 us, 5.16 TB/s (a large copy runs at 4.94); its backward 212 us,
+// 5.07 TB/s; 128 x 2048 to e4m3 in blocks of 128 4.6 us.
 #include "layer.h"
 
 namespace m3 {
@@ -418,7 +421,7 @@ namespace {
 bool wide(const void *q, int64_t row, int64_t es) { return ((uintptr_t)q & 15u) == 0 && row * es % 16 == 0; }
 
 // Rows of up to 2048 values fit one wave's registers; one wave a row needs no barrier, four waves a
-// row spread few rows over more of the GPU.
+// row spread few rows over more of the GPU (below 2048 rows a wave a row leaves SIMDs with one wave).
 bool one_wave(int64_t rows, int dim) { return dim <= 512 || (dim <= 2048 && rows >= 2048); }
 
 // The backward's waves a row, and its workgroups: 16 waves a CU for all (each workgroup leaves a row of

