@@ -420,9 +420,10 @@ namespace {
 
 bool wide(const void *q, int64_t row, int64_t es) { return ((uintptr_t)q & 15u) == 0 && row * es % 16 == 0; }
 
-// Rows of up to 2048 values fit one wave's registers; one wave a row needs no barrier, four waves a
-// row spread few rows over more of the GPU (below 2048 rows a wave a row leaves SIMDs with one wave).
-bool one_wave(int64_t rows, int dim) { return dim <= 512 || (dim <= 2048 && rows >= 2048); }
+// One wave a row needs no barrier, four spread few rows over more of the GPU. In us, one wave and four, bf16
+// with a bf16 residual: 256 x 1024 4.2 and 3.8, 2048 x 1024 5.3 and 5.3, 8192 x 1024 12.4 and 14.0; at 2048
+// values a row, where one wave holds 32 a lane, 256 rows 5.4 and 3.9, 2048 8.3 and 7.0, 32768 107 and 94.
+bool one_wave(int64_t rows, int dim) { return dim <= 512 || (dim <= 1024 && rows >= 2048); }
 
 // The backward's waves a row, and its workgroups: 16 waves a CU for all (each workgroup leaves a row of
 // partial sums).
@@ -444,8 +445,7 @@ template <typename T, typename RT>
 void norm_go(const NormParams &p, bool vec, hipStream_t st) {
     if (one_wave(p.rows, p.dim)) {
         if (p.dim <= 512) norm_launch<T, RT, 1, 1>(p, vec, st);
-        else if (p.dim <= 1024) norm_launch<T, RT, 1, 2>(p, vec, st);
-        else norm_launch<T, RT, 1, 4>(p, vec, st);
+        else norm_launch<T, RT, 1, 2>(p, vec, st);
     } else if (p.dim <= 2048) {
         norm_launch<T, RT, 4, 1>(p, vec, st);
     } else if (p.dim <= 4096) {

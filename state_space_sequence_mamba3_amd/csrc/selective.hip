@@ -477,11 +477,14 @@ static void scan_go(const SelParams &p, Access acc, hipStream_t st) {
 
 // A wave's instructions issue every second slot at best when it is alone on its SIMD, so fewer than
 // 256 workgroups (one a CU, one wave a SIMD) run at less than half the vector unit's rate. Segments cost
-// a first pass of about two thirds of the scan and the chain, and pay below that. They are as long as
-// leave 1024 workgroups of the forward (four a CU; 512 of the backward, whose registers allow two),
-// sqrt(2/3 of the sequence) and 64 tokens at least: no workgroup waits for a place. Packed sequences are of unknown lengths, and the
-// longest one decides when nothing else is left to run: they are cut below 1024 workgroups too, into
-// pieces of their mean length at most.
+// a first pass of about two thirds of the scan and the chain, and pay below that; the backward has its
+// first pass anyway. Sequences of 2048 tokens and 4096 channels (64 workgroups each), whole and in segments:
+// forward 1 204 and 76 us, 3 206 and 182, 4 211 and 234, 8 314 and 437; backward 4 834 and 688, 6 1145 and
+// 1141. Segments are as long as leave 1024 workgroups of the forward (four a CU; 512 of the backward,
+// whose registers allow two), sqrt(2/3 of the sequence) and 64 tokens at least: no workgroup waits for a
+// place. Packed sequences are of unknown lengths, and the longest one decides when nothing else is left to
+// run: they are cut below 1024 workgroups, into pieces of their mean length at most (random lengths, forward: 6
+// sequences 581 and 356 us, 12 745 and 670, 16 792 and 780, 20 888 and 1036).
 bool sel_plan(SelParams &p, bool back) {
     int npl, lpc;
     sel_shape(p.N, back, npl, lpc);
@@ -491,7 +494,7 @@ bool sel_plan(SelParams &p, bool back) {
     p.nseg = 1;
     p.seg_tokens = p.seqlen;
     const int64_t per = (int64_t)p.tiles * p.G;
-    if (p.nseq == 0 || p.nseq * per >= (p.cu ? 1024 : 256)) return false;
+    if (p.nseq == 0 || p.nseq * per >= (p.cu ? 1024 : back ? 384 : 256)) return false;
     const int64_t most = (back ? 512 : 1024) / per;                   // rows in all
     const int64_t cut = p.cu ? std::max<int64_t>(most - p.nseq, p.nseq) : most / p.nseq;   // of these by length
     if (cut < 2) return false;
