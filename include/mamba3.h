@@ -412,16 +412,17 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  * convolution, the selective scan, both for whole sequences, backwards and
  * for one token, and the RMS norm with the residual's addition. They follow
  * the conventions above (device pointers, host validation, no allocation, the
- * given stream, one token dtype, fp32 states, weights and sums). No argument
- * struct above changed with them.
+ * given stream, one token dtype, fp32 states, weights and sums). Every call
+ * writes all of a workspace that it reads; calls that may run at the same time
+ * need workspaces of their own. No argument struct above changed with them.
  *
  * Token rows. Token arrays are [batch, seqlen, n] with n innermost. Those with
  * a `_row` field may be views of wider rows (the halves of one projection's
  * output): `_row` is the number of elements from one token to the next, n at
- * least and 2^25 at most, or 0 for dense rows. Tokens of a padded batch lie at one distance
- * across sequences too. Any element alignment is accepted; rows and pointers
- * that are multiples of 16 bytes are read fastest. Arrays without a `_row`
- * field are dense.
+ * least and 2^25 at most, or 0 for dense rows. Tokens of a padded batch lie at
+ * one distance across sequences too. Any element alignment is accepted; rows
+ * and pointers that are multiples of 16 bytes are read fastest. Arrays without
+ * a `_row` field are dense.
  * cu_seqlens, nseq and packed batches are as for mamba3_scan_fwd (entries
  * clamped to [0, seqlen]; batch 1), and may leave tokens out before the first
  * and behind the last sequence, cu_seqlens[0] > 0 or cu_seqlens[nseq] < seqlen:
