@@ -6,10 +6,14 @@
 // the last W - 1 inputs in registers; its rows are loaded together before they are worked on. The W
 // - 1 rows before a thread's first token are read twice (mostly from the caches): 3 of 16 at width 4.
 // Sequence starts inside a thread's tokens reset the registers to conv_in's rows (a branch that is
-// uniform across the wave, which shares its tokens).
+// uniform across the wave, which shares its tokens). Rows of any length and alignment are read in the
+// same pieces: a row's last thread takes the last V channels, some of them its neighbour's too, which
+// both write alike (16384 tokens of 4095 channels, bf16: 63 us and 119 backward; channel by channel 80
+// and 142; 4096 channels 55 and 112). The step, whose states are in place, cannot read a channel twice and
+// goes channel by channel unless dim is a multiple of 4 (15.8 us for 1024 x 4095, 15.3 for 4096).
 //
 // 8 x 4096 tokens of 4096 channels, width 4, bf16: 112 us, 4.8 TB/s of what has to move (a large copy runs at
-// 4.94); the backward of 16384 x 4096 packed tokens 105 us, 3.8 TB/s; a step of 128 rows 4.1 us.
+// 4.94); the backward of 16384 x 4096 packed tokens 105 us, 3.8 TB/s; a step of 128 rows 4.1 us by itself.
 #include <type_traits>
 
 #include "layer.h"
@@ -87,14 +91,17 @@ __device__ __forceinline__ void next_seq(const ConvParams &p, int t, SeqAt &q) {
     q.a = min(q.a, t);
 }
 
+// V elements of a row as one load: global memory takes one of 8 or 16 bytes at any element.
+template <typename T, int V> struct RawVec { typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T)))); };
+template <typename T> struct RawVec<T, 1> { typedef T type; };
+
 // V elements of a row, as fp32
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(float (&o)[V], const T *row) {
     if constexpr (V == 1) {
         o[0] = to_f(row[0]);
     } else {
-        typedef T vec __attribute__((ext_vector_type(V)));
-        const vec v = *(const vec *)row;
+        const typename RawVec<T, V>::type v = *(const typename RawVec<T, V>::type *)row;
 #pragma unroll
         for (int e = 0; e < V; e++) o[e] = to_f(v[e]);
     }
@@ -104,15 +111,12 @@ __device__ __forceinline__ void store_vec(T *row, const float (&o)[V]) {
     if constexpr (V == 1) {
         row[0] = from_f<T>(o[0]);
     } else {
-        typedef T vec __attribute__((ext_vector_type(V)));
-        vec v;
+        typename RawVec<T, V>::type v;
 #pragma unroll
         for (int e = 0; e < V; e++) v[e] = from_f<T>(o[e]);
-        *(vec *)row = v;
+        *(typename RawVec<T, V>::type *)row = v;
     }
 }
-template <typename T, int V> struct RawVec { typedef T type __attribute__((ext_vector_type(V))); };
-template <typename T> struct RawVec<T, 1> { typedef T type; };
 template <typename T, int V>
 __device__ __forceinline__ float raw_f(const typename RawVec<T, V>::type &v, int e) {
     if constexpr (V == 1) return to_f(v);
@@ -154,9 +158,10 @@ __global__ __launch_bounds__(256) void k_conv(ConvParams p) {
         return;
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = (int)(blockIdx.x % p.chan_blocks) * 64 * V + lane * V;
+    const int from = (int)(blockIdx.x % p.chan_blocks) * 64 * V + lane * V;
     const int64_t first = ((int64_t)(blockIdx.x / p.chan_blocks) * 4 + wave) * kTok;
-    if (first >= p.total || c >= p.dim) return;
+    if (first >= p.total || from >= p.dim) return;
+    const int c = min(from, p.dim - V);  // a row's last thread: its last V channels, some also its neighbour's
     const int t0 = __builtin_amdgcn_readfirstlane((int)first);
     const T *x = (const T *)p.x + c;
     typename RawVec<T, V>::type raw[kTok];
@@ -342,7 +347,8 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
     }
     __shared__ float red[4][64 * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c0 = (int)(blockIdx.x % p.chan_blocks) * 64 * V, c = c0 + lane * V;
+    const int c0 = (int)(blockIdx.x % p.chan_blocks) * 64 * V, from = c0 + lane * V;
+    const int c = min(from, p.dim - V);  // as in the forward; a channel of two threads has equal sums in both
     const int blk = blockIdx.x / p.chan_blocks;
     const int64_t first = ((int64_t)blk * 4 + wave) * kTokBwd;
     ConvWalk<T, W, V> k;
@@ -352,7 +358,7 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
 #pragma unroll
         for (int j = 0; j < W; j++) k.dw[j][e] = 0.f;
     }
-    if (first < p.total && c < p.dim) {
+    if (first < p.total && from < p.dim) {
         const int t0 = __builtin_amdgcn_readfirstlane((int)first);
         const int t1 = min(t0 + kTokBwd, p.total);
         SeqAt q = seq_of(p, t0);
@@ -376,7 +382,8 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
     for (int j = 0; j <= W; j++) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < V; e++) red[wave][lane * V + e] = j < W ? k.dw[j < W ? j : 0][e] : k.db[e];
+        for (int e = 0; e < V; e++)
+            if (from < p.dim && c + e >= c0) red[wave][c - c0 + e] = j < W ? k.dw[j < W ? j : 0][e] : k.db[e];
         __syncthreads();
         for (int i = threadIdx.x; i < 64 * V; i += 256)
             if (c0 + i < p.dim)
@@ -452,17 +459,6 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepParams p, int chan_bl
 
 namespace {
 
-// 16-byte pieces: channels, rows and pointers multiples of them
-bool wide(int64_t es, int32_t dim, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> rows) {
-    const int64_t v = 16 / es;
-    if (dim % v) return false;
-    for (const void *q : ptrs)
-        if ((uintptr_t)q & 15u) return false;
-    for (int64_t r : rows)
-        if (r % v) return false;
-    return true;
-}
-
 ConvParams conv_params(const mamba3_conv_args *a) {
     ConvParams p{};
     p.x = a->x; p.conv_in = a->conv_in; p.w = a->weight; p.bias = a->bias;
@@ -518,10 +514,10 @@ void conv_step_go(const ConvStepParams &p, int width, hipStream_t st) {
 mamba3_status launch_conv(const mamba3_conv_args *a, hipStream_t st) {
     const ConvParams p = conv_params(a);
     if (a->dtype == MAMBA3_F32) {
-        if (wide(4, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<float, 4, false>(p, a->width, st);
+        if (p.dim >= 4) conv_go<float, 4, false>(p, a->width, st);
         else conv_go<float, 1, false>(p, a->width, st);
     } else {
-        if (wide(2, p.dim, {p.x, p.conv_in, p.y}, {p.x_row})) conv_go<bf16, 8, false>(p, a->width, st);
+        if (p.dim >= 8) conv_go<bf16, 8, false>(p, a->width, st);
         else conv_go<bf16, 1, false>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
@@ -538,13 +534,11 @@ mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st) {
     p.dy = b->dy; p.dconv_out = b->dconv_out; p.dx = b->dx; p.dconv_in = b->dconv_in;
     p.dy_row = b->dy_row ? b->dy_row : a->dim;
     p.part = (float *)b->workspace;
-    const int64_t es = a->dtype == MAMBA3_BF16 ? 2 : 4;
-    const bool wd = wide(es, p.dim, {p.x, p.conv_in, p.dy, p.dconv_out, p.dx}, {p.x_row, p.dy_row});
     if (a->dtype == MAMBA3_F32) {
-        if (wd) conv_go<float, 4, true>(p, a->width, st);
+        if (p.dim >= 4) conv_go<float, 4, true>(p, a->width, st);
         else conv_go<float, 1, true>(p, a->width, st);
     } else {
-        if (wd) conv_go<bf16, 4, true>(p, a->width, st);
+        if (p.dim >= 4) conv_go<bf16, 4, true>(p, a->width, st);
         else conv_go<bf16, 1, true>(p, a->width, st);
     }
     const int64_t n = (int64_t)p.dim * (a->width + 1);
@@ -560,10 +554,10 @@ mamba3_status launch_conv_step(const mamba3_conv_step_args *a, hipStream_t st) {
     p.x_row = a->x_row ? a->x_row : a->dim;
     p.batch = a->batch; p.dim = a->dim; p.silu = a->silu;
     if (a->dtype == MAMBA3_F32) {
-        if (wide(4, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<float, 4>(p, a->width, st);
+        if (p.dim % 4 == 0) conv_step_go<float, 4>(p, a->width, st);
         else conv_step_go<float, 1>(p, a->width, st);
     } else {
-        if (wide(2, p.dim, {p.x, p.conv, p.y}, {p.x_row})) conv_step_go<bf16, 4>(p, a->width, st);
+        if (p.dim % 4 == 0) conv_step_go<bf16, 4>(p, a->width, st);
         else conv_step_go<bf16, 1>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;

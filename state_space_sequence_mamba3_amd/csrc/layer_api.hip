@@ -1,5 +1,6 @@
 // C ABI of the layer operators: host-side validation and dispatch. Every check runs before any HIP
 // call, so an error status means nothing was enqueued.
+#include <algorithm>
 #include <cmath>
 
 #include "m3_common.h"
@@ -89,7 +90,7 @@ mamba3_status conv_shape(const mamba3_conv_args *a, int64_t *S, int64_t *T) {
     const mamba3_status st = check_batch(a->batch, a->seqlen, a->cu_seqlens, a->nseq, S, T);
     if (st != MAMBA3_OK) return st;
     // workgroups of 64 tokens and 64 channels at least, and of 256 state values
-    if ((*T / 64 + 1) * ((int64_t)a->dim / 64 + 1) + *S * (a->width - 1) * a->dim / 256 + 1 > kMaxBlocks)
+    if ((*T / 64 + 1) * ((int64_t)a->dim / 64 + 1) + *S * (std::min(a->width, 8) - 1) * a->dim / 256 + 1 > kMaxBlocks)
         return MAMBA3_EINVAL;
     return a->width >= 2 && a->width <= 8 ? MAMBA3_OK : MAMBA3_EUNSUPPORTED;
 }

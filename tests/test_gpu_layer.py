@@ -98,6 +98,33 @@ def test_conv_views_and_steps(dtype):
     assert torch.equal(pool[[5, 0, 2]], view[:, L - W + 1:])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [3, 4, 5, 7, 9, 15, 65, 255, 257, 259, 511, 513, 1025])
+def test_conv_rows_of_any_length(dim, dtype):
+    """Channel counts around the pieces and workgroups that a row is cut into, rows that start at any
+    element: the last pieces of a row share channels."""
+    note(f"conv rows {dim} {dtype}")
+    g = gen(900 + dim)
+    L, W = 70, 4
+    cu = [0, 33, 34, L]
+    wide = rand(g, 1, L, 2 * dim + 1, dtype=dtype)
+    x, dy = wide[:, :, :dim], wide[:, :, dim + 1:]
+    w, bias = rand(g, dim, W, std=0.5), rand(g, dim, std=0.5)
+    cin, dco = rand(g, 3, W - 1, dim, dtype=dtype), rand(g, 3, W - 1, dim, dtype=dtype)
+    ref = R.conv(x, w, bias, True, cin, cu, dy, dco)
+    mag = R.conv(x, w, bias, True, cin, cu, dy, dco, mag=True)
+    cut, on = up(torch.tensor(cu, dtype=torch.int32)), up(wide)
+    xd, dyd = on[:, :, :dim], on[:, :, dim + 1:]
+    # outputs one element behind an aligned address, a guard on both sides
+    y = torch.full((L * dim + 2,), 5.0, dtype=dtype, device=device())
+    m3.mamba3_conv_fwd(xd, up(w), up(bias), conv_in=up(cin), cu_seqlens=cut, y=y[1:-1].view(1, L, dim))
+    R.check(y[1:-1].view(1, L, dim), ref["y"], mag["y"], W + 12, "y")
+    assert float(y[0]) == 5.0 and float(y[-1]) == 5.0
+    gr = m3.mamba3_conv_bwd(xd, up(w), up(bias), dy=dyd, dconv_out=up(dco), conv_in=up(cin), cu_seqlens=cut)
+    for k, count in (("dx", 2 * W + 24), ("dweight", L + W + 24), ("dbias", L + W + 24), ("dconv_in", 2 * W + 24)):
+        R.check(gr[k], ref[k], mag[k], count, k)
+
+
 # ----------------------------------------------------------------------------- selective scan
 SCAN = [  # batch, seqlen, dim, N, G, cu
     (2, 37, 64, 16, 1, None), (1, 1, 8, 16, 1, None), (2, 16, 100, 16, 1, None), (1, 33, 1, 1, 1, None),
