@@ -16,6 +16,9 @@ template <typename T> using quad = typename QuadOf<T>::type;
 // takes a load of 8 or 16 bytes at any element); the quad that crosses a row's end is loaded from
 // its last 4 elements and shifted. ONE: rows of any length, element by element.
 enum Access { ONE, ANY, ALIGNED };
+// How the rows of B and C are read, N elements of a token and group: N may be below 4 where a lane holds
+// all states of a channel.
+constexpr Access states_access(Access acc, int lpc) { return acc == ANY && lpc == 1 ? ONE : acc; }
 
 // A token number that is the same for all lanes, in a scalar register and unknown to the compiler, which
 // would otherwise carry each lane's 64-bit addresses from tile to tile and add to every one of them.

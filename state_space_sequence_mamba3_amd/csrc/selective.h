@@ -93,7 +93,7 @@ __device__ __forceinline__ int64_t stored_at(int64_t k, int per, int gt, int wav
 }
 
 // NPL states of a channel from / to a row of N states, n0 the lane's first. VEC: N is a multiple of 4
-// and the row 16-byte aligned.
+// and the row 16-byte aligned; else a row's last one to three states are taken one by one.
 template <int NPL, bool VEC>
 __device__ __forceinline__ void load_states(float (&h)[NPL], const float *row, int n0, int N) {
     if constexpr (VEC) {
@@ -106,7 +106,18 @@ __device__ __forceinline__ void load_states(float (&h)[NPL], const float *row, i
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NPL; i++) h[i] = n0 + i < N ? row[n0 + i] : 0.f;
+        for (int i = 0; i < NPL; i += 4) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (n0 + i + 4 <= N) {
+                v = *(const LooseQuad<float>::type *)(row + n0 + i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; e++)
+                    if (n0 + i + e < N) v[e] = row[n0 + i + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) h[i + e] = v[e];
+        }
     }
 }
 template <int NPL, bool VEC>
@@ -117,8 +128,15 @@ __device__ __forceinline__ void store_states(const float (&h)[NPL], float *row, 
             if (n0 + i < N) *(f32x4 *)(row + n0 + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
     } else {
 #pragma unroll
-        for (int i = 0; i < NPL; i++)
-            if (n0 + i < N) row[n0 + i] = h[i];
+        for (int i = 0; i < NPL; i += 4) {
+            if (n0 + i + 4 <= N) {
+                *(LooseQuad<float>::type *)(row + n0 + i) = f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; e++)
+                    if (n0 + i + e < N) row[n0 + i + e] = h[i + e];
+            }
+        }
     }
 }
 

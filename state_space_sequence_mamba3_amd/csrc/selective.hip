@@ -10,7 +10,8 @@
 // unit and not the memory bounds the scan: 8 x 4096 tokens of 4096 channels at N = 16 take 0.58 ms
 // (1.86 TB/s of what has to move; the vector unit 87 % busy, two waves a SIMD), one sequence of 32768
 // tokens of 2048 channels in 32 segments 0.44 ms (0.19 first pass, 0.01 chain, 0.24 scan; saturated).
-// The step streams the states: 256 x 4096 channels in 30 us, 4.76 TB/s.
+// The step streams the states: 256 x 4096 channels in 30 us, 4.76 TB/s (27 with states that some cache still
+// holds; then 38 with 15 states, whose rows are taken in unaligned fours and a rest, 45 state by state).
 #include <cmath>
 #include <type_traits>
 
@@ -104,7 +105,9 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
 
     quad<T> rx[XE], rd[XE], rz[XE], ry[XE], rB[BE], rC[BE];
     // the tile from t0 on; TAIL: it may end behind the row's last token, whose inputs are repeated then
-    auto fetch = [&](int t0, auto tail) {
+    // (inlined by force: a call would take the captured registers through scratch memory, which it did with
+    // 3 states: 4 x 2048 tokens of 4096 channels 908 us instead of 166)
+    auto fetch = [&](int t0, auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
         const int64_t at = scalar_token(t0);
         const T *x0 = x + at * p.x_row, *d0 = dt + at * p.dt_row, *z0 = z + at * p.z_row, *y0 = dy + at * p.dy_row,
@@ -120,18 +123,18 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
 #pragma unroll
         for (int i = 0; i < BE; i++) {
             const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
-            rB[i] = load_quad<T, ACC>(B0, t, p.B_row, bn[i], p.N);
-            if (NEEDC) rC[i] = load_quad<T, ACC>(C0, t, p.C_row, bn[i], p.N);
+            rB[i] = load_quad<T, states_access(ACC, LPC)>(B0, t, p.B_row, bn[i], p.N);
+            if (NEEDC) rC[i] = load_quad<T, states_access(ACC, LPC)>(C0, t, p.C_row, bn[i], p.N);
         }
     };
     const std::integral_constant<bool, false> whole_tile;
     const std::integral_constant<bool, true> last_tile;
-    auto fetch_next = [&](int t0) {
+    auto fetch_next = [&](int t0) __attribute__((always_inline)) {
         if (t0 + TT <= row.t1) fetch(t0, whole_tile);
         else if (t0 < row.t1) fetch(t0, last_tile);
     };
     const int64_t stored = stored_base(row.t0, r, kSelStored);
-    auto tile = [&](int t0, auto tail) {
+    auto tile = [&](int t0, auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
         const int left = TAIL ? row.t1 - t0 : TT;           // the tile's tokens
         f32x4 xv[XE], zv[XE];
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
             float s, u, r;
             f32x4 b[NPL / 4], c[NPL / 4];
         } op[2][PF];
-        auto operands = [&](int t, Ops &o) {
+        auto operands = [&](int t, Ops &o) __attribute__((always_inline)) {
             o.s = S.u[t][ch][0];
             o.u = S.u[t][ch][1];
             if (MODE == STORE_PART) o.r = S.y[t][ch];
@@ -376,7 +379,7 @@ struct SelStepParams {
     int32_t nslots, dim, dpg, N, softplus;
 };
 
-template <typename T, int NPL, int LPC, bool VEC>
+template <typename T, int NPL, int LPC, Access ACC>
 __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     constexpr int CB = 256 / LPC;                       // channels of a workgroup
     const int b = blockIdx.x / tiles, d = (blockIdx.x % tiles) * CB + threadIdx.x / LPC;
@@ -384,7 +387,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     if (d >= p.dim) return;                             // whole channels: a channel's lanes stay together
     // what does not wait for the slot first: a step is a few memory latencies long
     float h[NPL], A2[NPL];
-    load_states<NPL, VEC>(A2, p.A + (int64_t)d * p.N, n0, p.N);
+    load_states<NPL, ACC == ALIGNED>(A2, p.A + (int64_t)d * p.N, n0, p.N);
     const int g = d / p.dpg;
     const T *B = (const T *)p.B + b * p.B_row + g * p.N, *C = (const T *)p.C + b * p.C_row + g * p.N;
     const float x = to_f(((const T *)p.x)[b * p.x_row + d]), D = p.D ? p.D[d] : 0.f;
@@ -393,7 +396,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
     float Bv[NPL], Cv[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; i += 4) {
-        const quad<T> bq = load_quad<T, VEC ? ALIGNED : ONE>(B, 0, 0, n0 + i, p.N), cq = load_quad<T, VEC ? ALIGNED : ONE>(C, 0, 0, n0 + i, p.N);
+        const quad<T> bq = load_quad<T, states_access(ACC, LPC)>(B, 0, 0, n0 + i, p.N), cq = load_quad<T, states_access(ACC, LPC)>(C, 0, 0, n0 + i, p.N);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             Bv[i + e] = n0 + i + e < p.N ? to_f(bq[e]) : 0.f;
@@ -406,7 +409,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
         if (slot < 0 || slot >= p.nslots) return;       // inactive row (uniform across the workgroup)
     }
     float *hs = p.h + (slot * p.dim + d) * p.N;
-    load_states<NPL, VEC>(h, hs, n0, p.N);
+    load_states<NPL, ACC == ALIGNED>(h, hs, n0, p.N);
     if (p.softplus) s = softplus_hw(s);
     const float u = s * x;
     float acc = 0.f;
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(256) void k_selstep(SelStepParams p, int tiles) {
         h[i] = exp_hw(s * A2[i]) * h[i] + u * Bv[i];
         acc += h[i] * Cv[i];
     }
-    store_states<NPL, VEC>(h, hs, n0, p.N);
+    store_states<NPL, ACC == ALIGNED>(h, hs, n0, p.N);
 #pragma unroll
     for (int o = 1; o < LPC; o <<= 1) acc += __shfl_xor(acc, o, 64);
     if (sub == 0) {
@@ -457,7 +460,7 @@ SelParams sel_params(const mamba3_selective_scan_args *a) {
 Access sel_access(const SelParams &p, int64_t es) {
     const bool al = p.dpg % 4 == 0 && p.N % 4 == 0 && quads(p.x, p.x_row, es) && quads(p.dt, p.dt_row, es) &&
            quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es) && quads(p.z, p.z_row, es) && quads(p.y, p.dim, es);
-    return al ? ALIGNED : p.dpg >= 4 && p.N >= 4 ? ANY : ONE;
+    return al ? ALIGNED : p.dpg >= 4 ? ANY : ONE;
 }
 
 template <typename T, int MODE>
@@ -578,13 +581,13 @@ void launch_sel_stored(const SelParams &p, int32_t dtype, Access acc, hipStream_
 template <typename T>
 static void step_go(const mamba3_selective_step_args *a, const SelStepParams &p, hipStream_t st) {
     const int64_t es = sizeof(T);
-    const bool vec = p.N % 4 == 0 && quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es);
+    const bool al = p.N % 4 == 0 && quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es);
 #define M3_GO(NPL, LPC)                                                                                        \
     do {                                                                                                       \
         const int tiles = (p.dim + 256 / LPC - 1) / (256 / LPC);                                               \
         const dim3 grid((uint32_t)a->batch * tiles);                                                           \
-        if (vec) hipLaunchKernelGGL((k_selstep<T, NPL, LPC, true>), grid, dim3(256), 0, st, p, tiles);         \
-        else hipLaunchKernelGGL((k_selstep<T, NPL, LPC, false>), grid, dim3(256), 0, st, p, tiles);            \
+        if (al) hipLaunchKernelGGL((k_selstep<T, NPL, LPC, ALIGNED>), grid, dim3(256), 0, st, p, tiles);       \
+        else hipLaunchKernelGGL((k_selstep<T, NPL, LPC, ANY>), grid, dim3(256), 0, st, p, tiles);              \
     } while (0)
     M3_SEL_DISPATCH(p.N, M3_GO);
 #undef M3_GO

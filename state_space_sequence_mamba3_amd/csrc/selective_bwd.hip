@@ -166,8 +166,8 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
 #pragma unroll
             for (int i = 0; i < BE; i++) {
                 const int t = TAIL ? min(bt[i], row.t1 - 1 - t0) : bt[i];
-                rB[i] = load_quad<T, ACC>(B0, t, p.B_row, bn[i], p.N);
-                rC[i] = load_quad<T, ACC>(C0, t, p.C_row, bn[i], p.N);
+                rB[i] = load_quad<T, states_access(ACC, LPC)>(B0, t, p.B_row, bn[i], p.N);
+                rC[i] = load_quad<T, states_access(ACC, LPC)>(C0, t, p.C_row, bn[i], p.N);
             }
         };
         if (t0 + TT <= row.t1) load(std::integral_constant<bool, false>());

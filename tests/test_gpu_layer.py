@@ -136,6 +136,8 @@ SCAN = [  # batch, seqlen, dim, N, G, cu
     (1, 300, 40, 16, 1, None), (3, 200, 9, 16, 1, None), (2, 129, 36, 24, 2, None), (1, 150, 8, 128, 1, None),
     (1, 400, 20, 16, 1, [0, 0, 64, 65, 65, 300, 399, 400]), (1, 333, 6, 5, 2, [0, 200, 333]),
     (64, 70, 256, 16, 1, None), (0, 9, 8, 16, 1, None), (1, 900, 8, 16, 1, MANY),
+    # fewer than four states
+    (2, 90, 40, 1, 1, None), (1, 90, 70, 2, 2, None), (1, 400, 40, 3, 1, [0, 100, 101, 400]), (2, 19, 12, 3, 3, None),
 ]
 
 
@@ -226,7 +228,8 @@ def test_selective_scan_bwd_differences():
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("case", [(2, 29, 64, 16, 1, None), (1, 20, 48, 24, 2, None), (1, 18, 9, 13, 1, None),
-                                  (2, 17, 12, 128, 1, None)])
+                                  (2, 17, 12, 128, 1, None),
+                                  (2, 18, 36, 3, 2, None), (1, 18, 8, 1, 1, None), (1, 18, 40, 18, 1, None)])
 def test_selective_steps_continue_a_prompt(case, dtype):
     """A prompt's state taken up by single tokens through slots; inputs as views of wider rows."""
     note(f"selective steps {case} {dtype}")
