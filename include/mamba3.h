@@ -595,6 +595,9 @@ mamba3_status mamba3_selective_step(const mamba3_selective_step_args *args, void
  *              the block / largest value, 2^-126 at least (so a block of zeros
  *              has zeros for q). Both round from fp32 to the nearest, ties to
  *              even.
+ * A row's sum is held in fp32; a row whose mean square leaves its range is summed
+ * scaled by a power of two, so that every row with a root mean square of 2^-126
+ * to 2^126 has its norm, with eps = 0 too.
  * rows < 2^24. At least one of y and q is given. eps is finite and >= 0. Outputs overlap
  * neither each other nor any input, residual_out = residual aside. */
 typedef enum { MAMBA3_E4M3 = 0, MAMBA3_INT8 = 1 } mamba3_qtype;

@@ -1,7 +1,7 @@
 // RMS norm of rows with the residual's addition, its 8-bit output with scales, and its backward.
 //
 //   s = x + residual,  v = s rsqrt(mean(s^2) + eps) w,  q = round(v / scale)
-//   ds = dresidual_out + r (w dy - sh mean(w dy sh)),  dw = sum over rows of dy sh
+//   ds = dresidual_out + r (w dy - sh mean(w dy sh)),  dw = sum over rows of dy sh   (sh = r s)
 //
 // A few operations a value, so HBM-bound: every row is read once, kept in registers as fp32 between its
 // sum and its outputs (rows of more than 8192 values are read twice), and everything a row needs
@@ -10,6 +10,8 @@
 //
 // 32768 x 2048, bf16 with an fp32 residual: 138 us, 5.84 TB/s (a large copy runs at 4.94); its backward 212 us,
 // 5.07 TB/s; 128 x 2048 to e4m3 in blocks of 128 4.6 us.
+#include <type_traits>
+
 #include "layer.h"
 
 namespace m3 {
@@ -125,6 +127,13 @@ __device__ __forceinline__ float row_max(float v, float *red) {
     return v;
 }
 
+// Squares leave fp32's range long before the values do: a row whose mean square + eps is no number of
+// [2^-80, infinity) is summed again with its values times a power of two, `row_scale` of that mean, which
+// brings every finite row back inside.
+constexpr float kLeastMean = 0x1p-80f;
+__device__ __forceinline__ bool in_range(float mean) { return mean >= kLeastMean && mean < INFINITY; }
+__device__ __forceinline__ float row_scale(float mean) { return mean < kLeastMean ? 0x1p100f : 0x1p-80f; }
+
 constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126: a block of zeros divides by it
 
 // q = round(v / scale). One Newton step makes the quotient by the reciprocal the correctly rounded
@@ -198,7 +207,20 @@ __global__ __launch_bounds__(256) void k_norm(NormParams p) {
 #pragma unroll
         for (int e = 0; e < kNV; e++) ss += s[e] * s[e];
     }
-    const float rms = __builtin_amdgcn_rsqf(row_sum<WPR>(ss, red) / (float)p.dim + p.eps);
+    const float mean = row_sum<WPR>(ss, red) / (float)p.dim + p.eps;
+    float rms = __builtin_amdgcn_rsqf(mean);
+    if (!in_range(mean)) {                           // (the same for all lanes of the row)
+        const float k = row_scale(mean);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < nch; i++) {
+            float(&s)[kNV] = keep[NCH ? i : 0];
+            if constexpr (NCH == 0) sum_of(i * STEP + t * kNV, s);
+#pragma unroll
+            for (int e = 0; e < kNV; e++) ss += s[e] * k * (s[e] * k);
+        }
+        rms = __builtin_amdgcn_rsqf(row_sum<WPR>(ss, red) / (float)p.dim + p.eps * k * k) * k;
+    }
     const bool one = p.q && p.nblocks == 1;          // one scale a row
     const float qmax = p.qtype == MAMBA3_E4M3 ? 448.f : 127.f;
     auto normed = [&](int c, const float (&s)[kNV], float (&v)[kNV]) {
@@ -316,53 +338,90 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_norm_bwd(NormPara
     weigh(0);
 #pragma unroll
     for (int e = 0; e < kNV; e++) dw[e] = 0.f;
-    if (!LONG && first < p.rows) fetch(first, 0);
     int turn = 0;
-    for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
-        float ks[kNV], kd[kNV], kr[kNV];
-        float ss = 0.f, sd = 0.f;
-        auto unpack = [&]() {
+    bool odd = false;                                // a row whose mean is out of range (see in_range)
+    auto walk = [&](auto scaled) __attribute__((always_inline)) {
+        constexpr bool SCALED = decltype(scaled)::value;
+        if (!LONG && first < p.rows) fetch(first, 0);
+        for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
+            float ks[kNV], kd[kNV], kr[kNV];
+            float ss = 0.f, sd = 0.f;
+            auto unpack = [&]() {
 #pragma unroll
-            for (int e = 0; e < kNV; e++) {
-                ks[e] = to_f(rs[e]);
-                kd[e] = to_f(rd[e]);
-                kr[e] = p.dres ? to_f(rr[e]) : 0.f;
-            }
-        };
-        for (int i = 0; i < nch; i++) {
-            if (LONG) {
-                fetch(row, i);
-                weigh(i);
-            }
-            unpack();
-#pragma unroll
-            for (int e = 0; e < kNV; e++) {
-                ss += ks[e] * ks[e];
-                sd += ks[e] * w[e] * kd[e];
-            }
-        }
-        if (!LONG && row + step < p.rows) fetch(row + step, 0);
-        row_sums<WPR>(ss, sd, red[turn]);
-        const float r = __builtin_amdgcn_rsqf(ss / (float)p.dim + p.eps);
-        const float m = sd / (float)p.dim * r * r * r;                      // ds = r w dy - m s
-        if (LONG && t == 0 && p.part) p.part[row] = r;
-        for (int i = 0; i < nch; i++) {
-            const int c = i * STEP + t * kNV;
-            float o[kNV];
-            if (LONG) {
-                fetch(row, i);
-                weigh(i);
+                for (int e = 0; e < kNV; e++) {
+                    ks[e] = to_f(rs[e]);
+                    kd[e] = to_f(rd[e]);
+                    kr[e] = p.dres ? to_f(rr[e]) : 0.f;
+                }
+            };
+            for (int i = 0; i < nch; i++) {
+                if (LONG) {
+                    fetch(row, i);
+                    weigh(i);
+                }
                 unpack();
-            }
 #pragma unroll
-            for (int e = 0; e < kNV; e++) {
-                o[e] = kr[e] + (r * w[e] * kd[e] - m * ks[e]);
-                if (!LONG) dw[e] += kd[e] * ks[e] * r;
+                for (int e = 0; e < kNV; e++) {
+                    ss += ks[e] * ks[e];
+                    sd += ks[e] * w[e] * kd[e];
+                }
             }
-            if (p.res_out) store8<RT, VEC>((RT *)p.res_out + row * p.dim, c, p.dim, o);
-            if (p.dx) store8<T, VEC>((T *)p.dx + row * p.dim, c, p.dim, o);
+            if (!LONG && row + step < p.rows) fetch(row + step, 0);
+            row_sums<WPR>(ss, sd, red[turn]);
+            const float mean = ss / (float)p.dim + p.eps;
+            const bool in = in_range(mean);
+            float root, r;
+            if constexpr (SCALED) {
+                if (in) continue;                    // (the same for all lanes of the row)
+                const float k = row_scale(mean);
+                ss = sd = 0.f;
+                for (int i = 0; i < nch; i++) {
+                    if (LONG) {
+                        fetch(row, i);
+                        weigh(i);
+                        unpack();
+                    }
+#pragma unroll
+                    for (int e = 0; e < kNV; e++) {
+                        ss += ks[e] * k * (ks[e] * k);
+                        sd += ks[e] * k * w[e] * kd[e];
+                    }
+                }
+                row_sums<WPR>(ss, sd, red[turn ^ 1]);    // (its last readers are before the barrier above)
+                if (WPR > 1) __syncthreads();            // the next row writes this half
+                root = __builtin_amdgcn_rsqf(ss / (float)p.dim + p.eps * k * k);
+                r = root * k;
+            } else {
+                odd |= !in;
+                root = in ? __builtin_amdgcn_rsqf(mean) : 0.f;
+                r = root;
+                sd = in ? sd : 0.f;
+            }
+            const float m = sd / (float)p.dim * root;                       // ds = r (w dy - m sh)
+            if (LONG && t == 0 && p.part) p.part[row] = r;
+            for (int i = 0; i < nch; i++) {
+                const int c = i * STEP + t * kNV;
+                float o[kNV];
+                if (LONG) {
+                    fetch(row, i);
+                    weigh(i);
+                    unpack();
+                }
+#pragma unroll
+                for (int e = 0; e < kNV; e++) {
+                    const float sh = ks[e] * r;
+                    o[e] = kr[e] + r * (w[e] * kd[e] - m * sh);
+                    if (!LONG) dw[e] += kd[e] * sh;
+                }
+                if (p.res_out) store8<RT, VEC>((RT *)p.res_out + row * p.dim, c, p.dim, o);
+                if (p.dx) store8<T, VEC>((T *)p.dx + row * p.dim, c, p.dim, o);
+            }
         }
-    }
+    };
+    // Rows out of range pass with r = 0, which leaves dres as it was and adds nothing to dweight, and are
+    // taken in a walk of their own: a branch for them among the others cost 5 % (4096 x 8192 bf16 56 -> 59 us).
+    walk(std::integral_constant<bool, false>());
+    if (odd) walk(std::integral_constant<bool, true>());
     if (LONG || !p.part) return;
     // one row of partial sums a workgroup: with a wave a row, those of its four waves in order
     if constexpr (WPR == 1) {
@@ -409,7 +468,7 @@ __global__ __launch_bounds__(256) void k_norm_dw(NormParams p) {
     if (c < p.dim) {
 #pragma unroll 8
         for (int64_t i = wave; i < p.rows; i += 4)
-            s += to_f(((const T *)p.dy)[i * p.dy_row + c]) * to_f(((const RT *)p.x)[i * p.dim + c]) * p.part[i];
+            s += to_f(((const T *)p.dy)[i * p.dy_row + c]) * (to_f(((const RT *)p.x)[i * p.dim + c]) * p.part[i]);
     }
     red[wave][lane] = s;
     __syncthreads();
