@@ -92,6 +92,14 @@ __device__ __forceinline__ int64_t stored_at(int64_t k, int per, int gt, int wav
     return (((k * per + gt) * kSelWaves + wave) * (npl / 4)) * 256 + lane * 4;
 }
 
+// 2^v h, v the exponent of many steps together. A state may grow (s A > 0) by more than fp32's range while h
+// is zero or tiny: two factors of 2^(v/2), held finite, give h 2^v wherever that is in range, and zero for
+// zero.
+__device__ __forceinline__ float carried(float v, float h) {
+    const float e = fminf(__builtin_amdgcn_exp2f(0.5f * v), 3.40282347e38f);
+    return h * e * e;
+}
+
 // NPL states of a channel from / to a row of N states, n0 the lane's first. VEC: N is a multiple of 4
 // and the row 16-byte aligned; else a row's last one to three states are taken one by one.
 template <int NPL, bool VEC>

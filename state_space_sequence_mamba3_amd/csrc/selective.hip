@@ -274,6 +274,31 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_selscan(SelParams p) {
         store_states<NPL, ACC == ALIGNED>(h, p.seg_h + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
         if (sub == 0) p.seg_s[(int64_t)r * p.dim + d] = sum;
     }
+    if (MODE == STORE_PART) {
+        // decays above one whose product left fp32's range: the share from the last token on, which is in
+        // range wherever the gradient is
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < NPL; i++) over |= !(prod[i] < INFINITY);
+        if (over) {
+#pragma unroll
+            for (int i = 0; i < NPL; i++) share[i] = 0.f;
+            const int c = d - g * p.dpg;
+            for (int64_t t = row.t1 - 1; t >= row.t0; t--) {
+                float s = to_f(dt[t * p.dt_row + c]) + (p.bias ? p.bias[d] : 0.f), r = to_f(dy[t * p.dy_row + c]);
+                if (p.softplus) s = softplus_hw(s);
+                if (z) {
+                    const float zt = to_f(z[t * p.z_row + c]);
+                    r *= zt * sigmoid_hw(zt);
+                }
+#pragma unroll
+                for (int i = 0; i < NPL; i++) {
+                    const float ct = n0 + i < p.N ? to_f(C[t * p.C_row + n0 + i]) : 0.f;
+                    share[i] = __builtin_amdgcn_exp2f(s * A2[i]) * (share[i] + r * ct);
+                }
+            }
+        }
+    }
     if (MODE == STORE_PART) store_states<NPL, ACC == ALIGNED>(share, p.seg_g + ((int64_t)r * p.dim + d) * p.N, n0, p.N);
 }
 
@@ -318,7 +343,7 @@ __global__ __launch_bounds__(kSelTabThreads) void k_seltable(SelParams p, int4 *
 }
 
 // The chain over a sequence's segments, a thread for each channel and state: the state that enters a
-// segment replaces its own end in seg_h, H_{k+1} = exp(A sum_k) H_k + U_k; the gradient that enters it at
+// segment replaces its own end in seg_h, H_{k+1} = exp(A sum_k) H_k + U_k (see `carried`); the gradient that enters it at
 // its end replaces its share in seg_g, G_{k-1} = exp(A sum_k) G_k + V_k from dh_out on. Loads of eight
 // segments are in flight together.
 constexpr int kSelChain = 8;
@@ -345,7 +370,7 @@ __global__ __launch_bounds__(256) void k_selchain(SelParams p, const float *dh_o
             for (int k = 0; k < kSelChain; k++)
                 if (r + k < r1) {
                     p.seg_h[(int64_t)(r + k) * dn + i] = H;
-                    H = __builtin_amdgcn_exp2f(S[k] * A2) * H + U[k];
+                    H = carried(S[k] * A2, H) + U[k];
                 }
         }
     } else {
@@ -362,7 +387,7 @@ __global__ __launch_bounds__(256) void k_selchain(SelParams p, const float *dh_o
             for (int k = 0; k < kSelChain; k++)
                 if (r - k >= r0) {
                     p.seg_g[(int64_t)(r - k) * dn + i] = G;
-                    G = __builtin_amdgcn_exp2f(S[k] * A2) * G + V[k];
+                    G = carried(S[k] * A2, G) + V[k];
                 }
         }
     }

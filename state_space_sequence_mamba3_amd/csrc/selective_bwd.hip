@@ -113,6 +113,12 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
     } else if (p.seg_g) load_states<NPL, ACC == ALIGNED>(G, p.seg_g + ((int64_t)rw * p.dim + d) * p.N, n0, p.N);
     else if (q.dh_out) load_states<NPL, ACC == ALIGNED>(G, q.dh_out + ((int64_t)row.seq * p.dim + d) * p.N, n0, p.N);
 
+    float most = A[0], least = A[0];                            // of the lane's states
+#pragma unroll
+    for (int i = 1; i < NPL; i++) {
+        most = fmaxf(most, A[i]);
+        least = fminf(least, A[i]);
+    }
     float H[NPL];                                               // the state that enters the segment
 #pragma unroll
     for (int i = 0; i < NPL; i++) H[i] = 0.f;
@@ -197,6 +203,18 @@ __global__ __launch_bounds__(64 * kSelWaves, LPC >= 4 && NPL == 4 ? 2 : 1) void 
 #pragma unroll
             for (int i = 0; i < NPL; i++)       // a segment's states were stored as from zero
                 h0s[b][i] = !real ? 0.f : p.seg_h ? h0n[b][i] + __builtin_amdgcn_exp2f(s0n[b] * (A[i] * kLog2e)) * H[i] : h0n[b][i];
+        if (p.seg_h && real) {
+            bool far = false;
+#pragma unroll
+            for (int b = 0; b < NSUB; b++) far |= fmaxf(s0n[b] * most, s0n[b] * least) > 88.f;
+            if (far) {                          // (states that grow: see `carried`)
+#pragma unroll
+                for (int b = 0; b < NSUB; b++)
+#pragma unroll
+                    for (int i = 0; i < NPL; i++)
+                        h0s[b][i] = h0n[b][i] + carried(s0n[b] * (A[i] * kLog2e), H[i]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < XE; i++) {
             const bool in = t0 + xt[i] < row.t1;

@@ -75,3 +75,49 @@ def test_rmsnorm_of_rows_without_a_norm():
     assert bool(torch.isnan(y[2, 5])) and int((y[2] == 0).sum()) == 63
     y = m3.mamba3_rmsnorm_fwd(torch.zeros(2, 64, device=device()), eps=1e-5)["y"]
     assert bool((y == 0).all())
+
+
+# ----------------------------------------------------------------------------- states that grow
+def growing(kind, L, D, N, g):
+    """Inputs of a scan whose states or gradients grow by more than fp32's range over a segment (64 tokens)
+    and yet stay in it: A > 0, or steps below zero."""
+    x, dt = torch.zeros(1, L, D), torch.ones(1, L, D)
+    A = 1 + 0.5 * torch.rand(D, N, generator=g)
+    dy = torch.zeros(1, L, D)
+    h, dh = torch.zeros(1, D, N), torch.zeros(1, D, N)
+    B, C = (0.5 + torch.rand(1, L, 1, N, generator=g) for _ in range(2))
+    if kind == "late inputs":           # zero until 30 tokens before the end; gradients from the first 30 alone
+        x[:, L - 30:] = rand(g, 1, 30, D)
+        dy[:, :30] = rand(g, 1, 30, D)
+    elif kind == "late inputs, steps below zero":
+        x[:, L - 30:] = rand(g, 1, 30, D)
+        dy[:, :30] = rand(g, 1, 30, D)
+        A, dt = -A, -dt
+    elif kind == "from a tiny state":   # e^100 times larger after a segment, and decays from there
+        h = 1e-30 * (1 + torch.rand(1, D, N, generator=g))
+        dt[:, 66:] = -1
+        dy[:, 100:140] = 0.5 + torch.rand(1, 40, D, generator=g)
+    else:                               # the same for the gradient that enters at the end
+        dh = 1e-30 * (1 + torch.rand(1, D, N, generator=g))
+        dt[:, :L - 66] = -1
+        x[:, L - 140:L - 100] = 0.5 + torch.rand(1, 40, D, generator=g)
+    return x, dt, A, B, C, h, dy, dh
+
+
+@pytest.mark.parametrize("L", [60, 400])
+@pytest.mark.parametrize("kind", ["late inputs", "late inputs, steps below zero", "from a tiny state", "from a tiny gradient"])
+def test_growing_states(kind, L):
+    """One sequence, whole (60 tokens) and in segments (400): finite wherever the formula's values are."""
+    if L == 60 and kind.startswith("from"):
+        pytest.skip("needs a segment")
+    note(f"growing {kind} {L}")
+    D, N = 24, 16
+    x, dt, A, B, C, h, dy, dh = growing(kind, L, D, N, gen(L))
+    ref, mag = (R.scan(x, dt, A, B, C, None, None, None, False, h, None, dy, dh, mag=m) for m in (False, True))
+    assert all(bool((v.abs() < 1e38).all()) for v in ref.values())
+    got = dict(zip(("y", "h_out"), m3.mamba3_selective_scan_fwd(up(x), up(dt), up(A), up(B), up(C), h_in=up(h))))
+    got.update(m3.mamba3_selective_scan_bwd(up(x), up(dt), up(A), up(B), up(C), dy=up(dy), dh_out=up(dh), h_in=up(h)))
+    for k, v in got.items():
+        # as in the operator's own tests: a decay is off by 60 roundings of its argument and 10 more a token,
+        # for states and gradients both; sums over channels, states and tokens
+        R.check(v, ref[k], mag[k], 140 * L + 64 + D + N + L, k)
