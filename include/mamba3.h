@@ -428,6 +428,19 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  * and behind the last sequence, cu_seqlens[0] > 0 or cu_seqlens[nseq] < seqlen:
  * their inputs take no part and their output rows are left as they were. S =
  * batch (padded) or nseq (packed); batch * seqlen <= 2^30.
+ *
+ * Sizes. A launch has fewer than 2^24 workgroups; calls that need more are refused
+ * with MAMBA3_EINVAL. With T = batch * seqlen they are
+ *   convolution     ceil(T / 64) ceil(D / 512) + ceil(S (W-1) D / 256), D / 256 with
+ *                   fp32, D / 64 in rows of fewer channels than 16 bytes hold
+ *     backward      ceil(T / 128) ceil(D / 256) + the same, D / 64 below 4 channels
+ *     step          batch ceil(D / 1024), D / 256 unless D is a multiple of 4
+ *   selective scan  R G ceil(D / G / c): c = 256, 128, 64, 64, 32, 16 channels for N
+ *                   up to 4, 8, 16, 32, 64, 128; R = S, or at most 1024 + S segments
+ *     backward      the same with c = 256, 128, 64, 32, 16, 16, and at least
+ *                   ceil(2 T G N / 256) + ceil(D (N + 2) / 256)
+ *     step          batch ceil(D / c)
+ *   RMS norm        its rows
  */
 
 /* Short causal convolution over every channel by itself, width W = 2..8:

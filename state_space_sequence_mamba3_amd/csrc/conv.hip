@@ -14,6 +14,7 @@
 //
 // 8 x 4096 tokens of 4096 channels, width 4, bf16: 112 us, 4.8 TB/s of what has to move (a large copy runs at
 // 4.94); the backward of 16384 x 4096 packed tokens 105 us, 3.8 TB/s; a step of 128 rows 4.1 us by itself.
+#include <algorithm>
 #include <type_traits>
 
 #include "layer.h"
@@ -474,6 +475,19 @@ ConvParams conv_params(const mamba3_conv_args *a) {
 
 int64_t token_blocks(int64_t total, int tok) { return (total + 4 * tok - 1) / (4 * tok); }
 
+// Channels of a thread: 16 bytes forward and 8 backward of bf16, 16 of fp32; single ones in rows of fewer.
+int conv_vec(int dtype, int dim, bool back) {
+    const int v = dtype == MAMBA3_F32 || back ? 4 : 8;
+    return dim >= v ? v : 1;
+}
+int step_vec(int dim) { return dim % 4 == 0 ? 4 : 1; }
+// Workgroups that walk tokens, and those of the states behind them
+int64_t main_blocks(int64_t total, int dim, int v, bool back) {
+    return token_blocks(total, back ? kTokBwd : kTok) * ((dim + 64 * v - 1) / (64 * v));
+}
+int64_t state_blocks(int64_t nseq, int width, int dim) { return (nseq * (width - 1) * dim + 255) / 256; }
+int64_t step_blocks(int dim) { return (dim + 256 * step_vec(dim) - 1) / (256 * step_vec(dim)); }
+
 #define M3_CONV_WIDTHS(W, CALL)     \
     switch (W) {                    \
         case 2: CALL(2); break;     \
@@ -488,9 +502,9 @@ int64_t token_blocks(int64_t total, int tok) { return (total + 4 * tok - 1) / (4
 template <typename T, int V, bool BACK>
 void conv_go(ConvParams p, int width, hipStream_t st) {
     p.chan_blocks = (p.dim + 64 * V - 1) / (64 * V);
-    p.main_blocks = (int32_t)(token_blocks(p.total, BACK ? kTokBwd : kTok) * p.chan_blocks);
+    p.main_blocks = (int32_t)main_blocks(p.total, p.dim, V, BACK);
     const bool state = BACK ? p.dconv_in != nullptr : p.conv_out != nullptr;
-    const int64_t extra = state ? ((int64_t)p.nseq * (width - 1) * p.dim + 255) / 256 : 0;
+    const int64_t extra = state ? state_blocks(p.nseq, width, p.dim) : 0;
     const dim3 grid((uint32_t)(p.main_blocks + extra));
     if (grid.x == 0) return;
 #define M3_GO(W)                                                                                        \
@@ -502,7 +516,7 @@ void conv_go(ConvParams p, int width, hipStream_t st) {
 
 template <typename T, int V>
 void conv_step_go(const ConvStepParams &p, int width, hipStream_t st) {
-    const int chan_blocks = (p.dim + 256 * V - 1) / (256 * V);
+    const int chan_blocks = (int)step_blocks(p.dim);
     const dim3 grid((uint32_t)((int64_t)p.batch * chan_blocks));
 #define M3_GO(W) hipLaunchKernelGGL((k_conv_step<T, W, V>), grid, dim3(256), 0, st, p, chan_blocks)
     M3_CONV_WIDTHS(width, M3_GO)
@@ -511,14 +525,24 @@ void conv_step_go(const ConvStepParams &p, int width, hipStream_t st) {
 
 }  // namespace
 
+int64_t conv_workgroups(const mamba3_conv_args *a, bool back) {
+    const int64_t total = (int64_t)a->batch * a->seqlen, nseq = a->cu_seqlens ? a->nseq : a->batch;
+    const int64_t walk = main_blocks(total, a->dim, conv_vec(a->dtype, a->dim, back), back) +
+                         state_blocks(nseq, a->width, a->dim);
+    return std::max(walk, back ? ((int64_t)a->dim * (a->width + 1) + 15) / 16 : 0);
+}
+
+int64_t conv_step_workgroups(const mamba3_conv_step_args *a) { return (int64_t)a->batch * step_blocks(a->dim); }
+
 mamba3_status launch_conv(const mamba3_conv_args *a, hipStream_t st) {
     const ConvParams p = conv_params(a);
+    const bool one = conv_vec(a->dtype, p.dim, false) == 1;
     if (a->dtype == MAMBA3_F32) {
-        if (p.dim >= 4) conv_go<float, 4, false>(p, a->width, st);
-        else conv_go<float, 1, false>(p, a->width, st);
+        if (one) conv_go<float, 1, false>(p, a->width, st);
+        else conv_go<float, 4, false>(p, a->width, st);
     } else {
-        if (p.dim >= 8) conv_go<bf16, 8, false>(p, a->width, st);
-        else conv_go<bf16, 1, false>(p, a->width, st);
+        if (one) conv_go<bf16, 1, false>(p, a->width, st);
+        else conv_go<bf16, 8, false>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
@@ -534,12 +558,13 @@ mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st) {
     p.dy = b->dy; p.dconv_out = b->dconv_out; p.dx = b->dx; p.dconv_in = b->dconv_in;
     p.dy_row = b->dy_row ? b->dy_row : a->dim;
     p.part = (float *)b->workspace;
+    const bool one = conv_vec(a->dtype, p.dim, true) == 1;
     if (a->dtype == MAMBA3_F32) {
-        if (p.dim >= 4) conv_go<float, 4, true>(p, a->width, st);
-        else conv_go<float, 1, true>(p, a->width, st);
+        if (one) conv_go<float, 1, true>(p, a->width, st);
+        else conv_go<float, 4, true>(p, a->width, st);
     } else {
-        if (p.dim >= 4) conv_go<bf16, 4, true>(p, a->width, st);
-        else conv_go<bf16, 1, true>(p, a->width, st);
+        if (one) conv_go<bf16, 1, true>(p, a->width, st);
+        else conv_go<bf16, 4, true>(p, a->width, st);
     }
     const int64_t n = (int64_t)p.dim * (a->width + 1);
     hipLaunchKernelGGL(k_conv_reduce, dim3((uint32_t)((n + 15) / 16)), dim3(256), 0, st, p.part,
@@ -553,12 +578,13 @@ mamba3_status launch_conv_step(const mamba3_conv_step_args *a, hipStream_t st) {
     p.slots = a->slots; p.nslots = a->nslots;
     p.x_row = a->x_row ? a->x_row : a->dim;
     p.batch = a->batch; p.dim = a->dim; p.silu = a->silu;
+    const bool one = step_vec(p.dim) == 1;
     if (a->dtype == MAMBA3_F32) {
-        if (p.dim % 4 == 0) conv_step_go<float, 4>(p, a->width, st);
-        else conv_step_go<float, 1>(p, a->width, st);
+        if (one) conv_step_go<float, 1>(p, a->width, st);
+        else conv_step_go<float, 4>(p, a->width, st);
     } else {
-        if (p.dim % 4 == 0) conv_step_go<bf16, 4>(p, a->width, st);
-        else conv_step_go<bf16, 1>(p, a->width, st);
+        if (one) conv_step_go<bf16, 1>(p, a->width, st);
+        else conv_step_go<bf16, 4>(p, a->width, st);
     }
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }

@@ -83,16 +83,14 @@ mamba3_status check_batch(int32_t batch, int32_t seqlen, const int32_t *cu, int3
 }
 
 // ---- convolution ----
-mamba3_status conv_shape(const mamba3_conv_args *a, int64_t *S, int64_t *T) {
+mamba3_status conv_shape(const mamba3_conv_args *a, bool back, int64_t *S, int64_t *T) {
     if (!a) return MAMBA3_EINVAL;
     if (!dtype_ok(a->dtype) || !flag(a->silu) || a->dim < 1 || a->width < 1 || !row_ok(a->x_row, a->dim))
         return MAMBA3_EINVAL;
     const mamba3_status st = check_batch(a->batch, a->seqlen, a->cu_seqlens, a->nseq, S, T);
     if (st != MAMBA3_OK) return st;
-    // workgroups of 64 tokens and 64 channels at least, and of 256 state values
-    if ((*T / 64 + 1) * ((int64_t)a->dim / 64 + 1) + *S * (std::min(a->width, 8) - 1) * a->dim / 256 + 1 > kMaxBlocks)
-        return MAMBA3_EINVAL;
-    return a->width >= 2 && a->width <= 8 ? MAMBA3_OK : MAMBA3_EUNSUPPORTED;
+    if (a->width < 2 || a->width > 8) return MAMBA3_EUNSUPPORTED;
+    return m3::conv_workgroups(a, back) <= kMaxBlocks ? MAMBA3_OK : MAMBA3_EINVAL;
 }
 
 }  // namespace
@@ -101,7 +99,7 @@ extern "C" {
 
 mamba3_status mamba3_conv_validate(const mamba3_conv_args *a) {
     int64_t S, T;
-    const mamba3_status st = conv_shape(a, &S, &T);
+    const mamba3_status st = conv_shape(a, false, &S, &T);
     if (st != MAMBA3_OK) return st;
     const int64_t es = esize(a->dtype), D = a->dim, W = a->width;
     const Arr in[] = {rows_of(a->x, T, a->x_row, D, es, true), dense_of(a->weight, D * W, 4, true),
@@ -118,14 +116,14 @@ mamba3_status mamba3_conv_fwd(const mamba3_conv_args *a, void *stream) {
 
 size_t mamba3_conv_bwd_workspace_size(const mamba3_conv_bwd_args *b) {
     int64_t S, T;
-    return b && conv_shape(&b->fwd, &S, &T) == MAMBA3_OK ? m3::conv_bwd_workspace_bytes(b) : 0;
+    return b && conv_shape(&b->fwd, true, &S, &T) == MAMBA3_OK ? m3::conv_bwd_workspace_bytes(b) : 0;
 }
 
 mamba3_status mamba3_conv_bwd_validate(const mamba3_conv_bwd_args *b) {
     int64_t S, T;
     if (!b) return MAMBA3_EINVAL;
     const mamba3_conv_args *a = &b->fwd;
-    mamba3_status st = conv_shape(a, &S, &T);
+    mamba3_status st = conv_shape(a, true, &S, &T);
     if (st != MAMBA3_OK) return st;
     if (!row_ok(b->dy_row, a->dim) || (b->dconv_in && !a->conv_in)) return MAMBA3_EINVAL;
     const int64_t es = esize(a->dtype), D = a->dim, W = a->width;
@@ -149,8 +147,8 @@ mamba3_status mamba3_conv_step_validate(const mamba3_conv_step_args *a) {
     if (!dtype_ok(a->dtype) || !flag(a->silu) || a->batch < 0 || a->dim < 1 || a->width < 1 ||
         !row_ok(a->x_row, a->dim) || (a->slots && a->nslots < 0))
         return MAMBA3_EINVAL;
-    if ((int64_t)a->batch * (a->dim / 256 + 1) > kMaxBlocks) return MAMBA3_EINVAL;
     if (a->width < 2 || a->width > 8) return MAMBA3_EUNSUPPORTED;
+    if (m3::conv_step_workgroups(a) > kMaxBlocks) return MAMBA3_EINVAL;
     const int64_t es = esize(a->dtype), D = a->dim, W = a->width, b = a->batch;
     const Arr in[] = {rows_of(a->x, b, a->x_row, D, es, true), dense_of(a->weight, D * W, 4, true),
                       dense_of(a->bias, D, 4, false), dense_of(a->slots, a->slots ? b : 0, 4, false)};
@@ -166,7 +164,7 @@ mamba3_status mamba3_conv_step(const mamba3_conv_step_args *a, void *stream) {
 }
 
 // ---- selective scan ----
-static mamba3_status sel_shape(const mamba3_selective_scan_args *a, int64_t *S, int64_t *T) {
+static mamba3_status sel_shape(const mamba3_selective_scan_args *a, bool back, int64_t *S, int64_t *T) {
     if (!a) return MAMBA3_EINVAL;
     if (!dtype_ok(a->dtype) || !flag(a->dt_softplus) || a->dim < 1 || a->dstate < 1 || a->ngroups < 1 ||
         a->dim % a->ngroups)
@@ -178,22 +176,17 @@ static mamba3_status sel_shape(const mamba3_selective_scan_args *a, int64_t *S, 
     const mamba3_status st = check_batch(a->batch, a->seqlen, a->cu_seqlens, a->nseq, S, T);
     if (st != MAMBA3_OK) return st;
     if (a->dstate > 128) return MAMBA3_EUNSUPPORTED;
-    // workgroups of 16 channels of a group at least; the backward's sums
-    const int64_t tiles = ((int64_t)a->dim / a->ngroups + 15) / 16 * a->ngroups;
-    if ((*S + *T / 64 + 1) * tiles > kMaxBlocks || *S * (((int64_t)a->dim * a->dstate + 255) / 256) > kMaxBlocks ||
-         (*T * 2 * gn + (int64_t)a->dim * (a->dstate + 2)) / 256 + 2 > kMaxBlocks)
-        return MAMBA3_EINVAL;
-    return MAMBA3_OK;
+    return m3::selective_workgroups(a, back) <= kMaxBlocks ? MAMBA3_OK : MAMBA3_EINVAL;
 }
 
 size_t mamba3_selective_scan_workspace_size(const mamba3_selective_scan_args *a) {
     int64_t S, T;
-    return sel_shape(a, &S, &T) == MAMBA3_OK ? m3::selective_workspace_bytes(a) : 0;
+    return sel_shape(a, false, &S, &T) == MAMBA3_OK ? m3::selective_workspace_bytes(a) : 0;
 }
 
 mamba3_status mamba3_selective_scan_validate(const mamba3_selective_scan_args *a) {
     int64_t S, T;
-    mamba3_status st = sel_shape(a, &S, &T);
+    mamba3_status st = sel_shape(a, false, &S, &T);
     if (st != MAMBA3_OK) return st;
     const int64_t es = esize(a->dtype), D = a->dim, N = a->dstate, gn = a->ngroups * N;
     const Arr in[] = {rows_of(a->x, T, a->x_row, D, es, true), rows_of(a->dt, T, a->dt_row, D, es, true),
@@ -216,14 +209,14 @@ mamba3_status mamba3_selective_scan_fwd(const mamba3_selective_scan_args *a, voi
 
 size_t mamba3_selective_scan_bwd_workspace_size(const mamba3_selective_scan_bwd_args *b) {
     int64_t S, T;
-    return b && sel_shape(&b->fwd, &S, &T) == MAMBA3_OK ? m3::selective_bwd_workspace_bytes(b) : 0;
+    return b && sel_shape(&b->fwd, true, &S, &T) == MAMBA3_OK ? m3::selective_bwd_workspace_bytes(b) : 0;
 }
 
 mamba3_status mamba3_selective_scan_bwd_validate(const mamba3_selective_scan_bwd_args *b) {
     int64_t S, T;
     if (!b) return MAMBA3_EINVAL;
     const mamba3_selective_scan_args *a = &b->fwd;
-    mamba3_status st = sel_shape(a, &S, &T);
+    mamba3_status st = sel_shape(a, true, &S, &T);
     if (st != MAMBA3_OK) return st;
     if (!row_ok(b->dy_row, a->dim) || (b->dz && !a->z)) return MAMBA3_EINVAL;
     const int64_t es = esize(a->dtype), D = a->dim, N = a->dstate, gn = a->ngroups * N;
@@ -257,8 +250,8 @@ mamba3_status mamba3_selective_step_validate(const mamba3_selective_step_args *a
     if (!row_ok(a->x_row, D) || !row_ok(a->dt_row, D) || !row_ok(a->z_row, D) || !row_ok(a->B_row, gn) ||
         !row_ok(a->C_row, gn) || gn > INT32_MAX)
         return MAMBA3_EINVAL;
-    if (b * (D / 16 + 1) > kMaxBlocks) return MAMBA3_EINVAL;
     if (N > 128) return MAMBA3_EUNSUPPORTED;
+    if (m3::selective_step_workgroups(a) > kMaxBlocks) return MAMBA3_EINVAL;
     const Arr in[] = {rows_of(a->x, b, a->x_row, D, es, true), rows_of(a->dt, b, a->dt_row, D, es, true),
                       rows_of(a->z, b, a->z_row, D, es, false), rows_of(a->B, b, a->B_row, gn, es, true),
                       rows_of(a->C, b, a->C_row, gn, es, true), dense_of(a->A, D * N, 4, true, 16),

@@ -113,7 +113,12 @@ int64_t segment_rows_packed(int64_t nseq, int64_t seqlen, int64_t seg_tokens);
 mamba3_status launch_segment_table(const int32_t *cu, int32_t nseq, int32_t seqlen, int32_t seg_tokens,
                                    int32_t *seg_cu, hipStream_t st);
 
-// The layer operators (layer_api.hip validates; each launcher's file holds its kernels).
+// The layer operators (layer_api.hip validates; each launcher's file holds its kernels). *_workgroups: the
+// workgroups of the largest launch that a call makes, for sizes that are valid otherwise.
+int64_t conv_workgroups(const mamba3_conv_args *a, bool back);
+int64_t conv_step_workgroups(const mamba3_conv_step_args *a);
+int64_t selective_workgroups(const mamba3_selective_scan_args *a, bool back);
+int64_t selective_step_workgroups(const mamba3_selective_step_args *a);
 mamba3_status launch_conv(const mamba3_conv_args *a, hipStream_t st);
 size_t conv_bwd_workspace_bytes(const mamba3_conv_bwd_args *b);
 mamba3_status launch_conv_bwd(const mamba3_conv_bwd_args *b, hipStream_t st);

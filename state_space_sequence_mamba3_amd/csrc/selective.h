@@ -183,6 +183,9 @@ Access sel_access(const SelParams &p, int64_t es);
 // Rows of a call (p.rows, nseg, seg_tokens): whole sequences, or segments where those leave the GPU
 // empty. True if segments; they need seg_bytes of workspace for the parts that `sel_segments` lays out.
 bool sel_plan(SelParams &p, bool back);
+// Workgroups of the backward's last launch: dB and dC, and the sums over rows.
+inline int64_t sel_reduce_blocks(const SelParams &p) { return ((int64_t)p.total * p.G * 2 * p.N + 255) / 256; }
+inline int64_t sel_sum_blocks(const SelParams &p) { return ((int64_t)p.dim * (p.N + 2) + 255) / 256; }
 size_t sel_segment_bytes(const SelParams &p);
 void sel_segments(SelParams &p, char *ws);
 // Enqueue: a packed batch's segment table; the scan that writes p.ckpt (and segments' ends) and no

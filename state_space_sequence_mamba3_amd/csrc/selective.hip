@@ -543,6 +543,14 @@ bool sel_plan(SelParams &p, bool back) {
     return true;
 }
 
+static int64_t chain_blocks(const SelParams &p) { return ((int64_t)p.dim * p.N + 255) / 256; }
+// Workgroups that cover the channels of one row of a step
+static int64_t step_tiles(int dim, int N) {
+    int npl, lpc;
+    sel_shape(N, false, npl, lpc);
+    return (dim + 256 / lpc - 1) / (256 / lpc);
+}
+
 static size_t al256(int64_t v) { return (size_t)((v + 255) / 256 * 256); }
 
 size_t sel_segment_bytes(const SelParams &p) {
@@ -567,8 +575,7 @@ void launch_sel_table(const SelParams &p, hipStream_t st) {
 }
 
 void launch_sel_chain(const SelParams &p, const float *dh_out, hipStream_t st) {
-    const int64_t blocks = ((int64_t)p.dim * p.N + 255) / 256;
-    hipLaunchKernelGGL(k_selchain, dim3((uint32_t)(blocks * p.nseq), p.seg_g ? 2 : 1), dim3(256), 0, st, p, dh_out);
+    hipLaunchKernelGGL(k_selchain, dim3((uint32_t)(chain_blocks(p) * p.nseq), p.seg_g ? 2 : 1), dim3(256), 0, st, p, dh_out);
 }
 
 mamba3_status launch_selective_scan(const mamba3_selective_scan_args *a, hipStream_t st) {
@@ -586,6 +593,16 @@ mamba3_status launch_selective_scan(const mamba3_selective_scan_args *a, hipStre
     else scan_go<bf16, FULL>(p, acc, st);
     return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
 }
+
+int64_t selective_workgroups(const mamba3_selective_scan_args *a, bool back) {
+    SelParams p = sel_params(a);
+    const bool segments = sel_plan(p, back);
+    int64_t n = (int64_t)p.rows * p.tiles * p.G;
+    if (segments) n = std::max(n, chain_blocks(p) * p.nseq);
+    return back ? std::max(n, sel_reduce_blocks(p) + sel_sum_blocks(p)) : n;
+}
+
+int64_t selective_step_workgroups(const mamba3_selective_step_args *a) { return (int64_t)a->batch * step_tiles(a->dim, a->dstate); }
 
 size_t selective_workspace_bytes(const mamba3_selective_scan_args *a) {
     SelParams p = sel_params(a);
@@ -609,7 +626,7 @@ static void step_go(const mamba3_selective_step_args *a, const SelStepParams &p,
     const bool al = p.N % 4 == 0 && quads(p.B, p.B_row, es) && quads(p.C, p.C_row, es);
 #define M3_GO(NPL, LPC)                                                                                        \
     do {                                                                                                       \
-        const int tiles = (p.dim + 256 / LPC - 1) / (256 / LPC);                                               \
+        const int tiles = (int)step_tiles(p.dim, p.N);                                                         \
         const dim3 grid((uint32_t)a->batch * tiles);                                                           \
         if (al) hipLaunchKernelGGL((k_selstep<T, NPL, LPC, ALIGNED>), grid, dim3(256), 0, st, p, tiles);       \
         else hipLaunchKernelGGL((k_selstep<T, NPL, LPC, ANY>), grid, dim3(256), 0, st, p, tiles);              \

@@ -459,7 +459,7 @@ void bwd_go(SelBwdParams &q, Access acc, hipStream_t st) {
     } while (0)
     if (p.rows > 0) M3_SELBWD_DISPATCH(p.N, M3_GO);
 #undef M3_GO
-    const int64_t bc = ((int64_t)p.total * p.G * 2 * p.N + 255) / 256, a = ((int64_t)p.dim * (p.N + 2) + 255) / 256;
+    const int64_t bc = sel_reduce_blocks(p), a = sel_sum_blocks(p);
     hipLaunchKernelGGL((k_selbwd_reduce<T>), dim3((uint32_t)(bc + a)), dim3(256), 0, st, q, (int)bc);
 }
 
