@@ -414,7 +414,10 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  * the conventions above (device pointers, host validation, no allocation, the
  * given stream, one token dtype, fp32 states, weights and sums). Every call
  * writes all of a workspace that it reads; calls that may run at the same time
- * need workspaces of their own. No argument struct above changed with them.
+ * need workspaces of their own. No argument struct above changed with them, and
+ * neither did the ABI number: MAMBA3_LAYER_OPERATORS says at compile time that they
+ * are declared, and a program that loads the library at run time looks for
+ * mamba3_conv_fwd (all of them came together).
  *
  * Token rows. Token arrays are [batch, seqlen, n] with n innermost. Those with
  * a `_row` field may be views of wider rows (the halves of one projection's
@@ -442,6 +445,8 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *     step          batch ceil(D / c)
  *   RMS norm        its rows
  */
+
+#define MAMBA3_LAYER_OPERATORS 1
 
 /* Short causal convolution over every channel by itself, width W = 2..8:
  *   p_t[d] = bias[d] + sum_{j < W} weight[d, j] x_{t - W + 1 + j}[d]
