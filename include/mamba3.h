@@ -527,7 +527,8 @@ mamba3_status mamba3_conv_step(const mamba3_conv_step_args *args, void *stream);
  * B, C         [batch, seqlen, G, N] token dtype, N = 1..128
  * A            [D, N] fp32, 16-byte aligned;  D, dt_bias [D] fp32 or NULL
  * h_in, h_out  [S, D, N] fp32, 16-byte aligned, or NULL (zero, not written)
- * softplus(v) = log(1 + e^v), v itself above 20. y overlaps no input; h_out
+ * softplus(v) = log(1 + e^v), v itself above 20. s A is below zero in a layer that
+ * forgets; states that grow are computed as far as fp32 holds them. y overlaps no input; h_out
  * may be h_in exactly. workspace: at least
  * mamba3_selective_scan_workspace_size(args) bytes (0 for many shapes),
  * 256-byte aligned: where a few long sequences would leave the GPU empty, they
@@ -560,8 +561,11 @@ mamba3_status mamba3_selective_scan_fwd(const mamba3_selective_scan_args *args, 
  * dD, ddt_bias [D] fp32 or NULL; dh_in [S, D, N] fp32 or NULL. dh_in and
  * dh_out are 16-byte aligned. No output overlaps an input or another output.
  * workspace: at least mamba3_selective_scan_bwd_workspace_size(args) bytes,
- * 256-byte aligned: the states at the start of every tile of tokens and partial
- * sums, added in a fixed order (bitwise reproducible). */
+ * 256-byte aligned: the states before every eighth token, N' / 2 bytes a token and
+ * channel (N' = N rounded up to 4, 8, 16, .. 128), and partial sums, added in a fixed
+ * order (bitwise reproducible), of which dB's and dC's take 8 N / c bytes (c as under
+ * Sizes). Together about 10 bytes a token and channel at N = 16, 64 at N = 64 and 128
+ * at N = 128: 8 x 2048 tokens of 4096 channels need 0.7, 4.3 and 8.6 GB. */
 typedef struct {
     mamba3_selective_scan_args fwd;
     int64_t dy_row;

@@ -150,7 +150,8 @@ __device__ __forceinline__ void store_states(const float (&h)[NPL], float *row, 
 
 // The lane arrangement of N states: as few lanes a channel as leave 4 or 8 states a lane. The backward
 // keeps the states and decays of 8 tokens, and with 8 states a lane that takes more than 256
-// registers, one wave a SIMD at half its rate: it takes 4 a lane up to 64 states.
+// registers, one wave a SIMD at half its rate: it takes 4 a lane up to 64 states (see k_selbwd for what
+// that leaves).
 #define M3_SEL_DISPATCH(N, CALL)              \
     do {                                      \
         if ((N) <= 4) CALL(4, 1);             \

@@ -10,6 +10,9 @@
 // unit and not the memory bounds the scan: 8 x 4096 tokens of 4096 channels at N = 16 take 0.58 ms
 // (1.86 TB/s of what has to move; the vector unit 87 % busy, two waves a SIMD), one sequence of 32768
 // tokens of 2048 channels in 32 segments 0.44 ms (0.19 first pass, 0.01 chain, 0.24 scan; saturated).
+// More states cost in proportion: 8 x 2048 tokens of 4096 channels, bf16, at N = 4, 8, 16, 32, 64, 128 take 0.26, 0.25,
+// 0.30, 0.52, 1.03, 2.18 ms; fp32 the same from N = 16 on but for N = 128, whose 260 registers leave one wave
+// a SIMD (3.26 ms).
 // The step streams the states: 256 x 4096 channels in 30 us, 4.76 TB/s (27 with states that some cache still
 // holds; then 38 with 15 states, whose rows are taken in unaligned fours and a rest, 45 state by state).
 #include <cmath>

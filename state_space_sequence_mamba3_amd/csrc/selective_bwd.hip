@@ -5,14 +5,25 @@
 //   dx_t = du_t s_t + D r_t,  ddt_t = ds_t softplus'(dt_t + bias),  dz_t = dy_t y_t SiLU'(z_t)
 //
 // The forward pass keeps nothing: a first pass (k_selscan's STORE form) writes the state before every 8
-// tokens in fp32 (N / 2 bytes a token and channel: at N = 16 as much as four bf16 token arrays), and
-// this pass walks those pieces backwards. A piece's states and decays are computed again and stay in
-// registers while its tokens are taken in reverse. The vector unit
-// bounds it: about 20 issue slots for every token, channel and state.
-// 8 x 2048 tokens of 4096 channels at N = 16, bf16: 1.16 ms, of which 0.22 the states, 0.91 this pass
+// tokens in fp32, and this pass walks those pieces backwards. A piece's states and decays are computed again
+// and stay in registers while its tokens are taken in reverse.
+//
+// Workspace, a token and channel: N' / 2 bytes of states (N' = N rounded up to 4, 8, .. 128), and 8 N / c bytes of
+// dB and dC's sums over the c channels of a workgroup (256, 128, 64, 32, 16, 16): 2.1, 4.5, 10, 24, 64, 128 bytes at
+// N = 4, 8, .. 128, where a bf16 token array has 2 (segments add half a byte and their states). Both are written
+// and read once.
+//
+// Up to N = 16 the vector unit bounds it: about 20 issue slots for every token, channel and state.
+// 8 x 2048 tokens of 4096 channels at N = 16, bf16: 1.14 ms, of which 0.22 the states, 0.89 this pass
 // (the vector unit 86 % busy, two waves a SIMD) and 0.03 the sums over workgroups. Pieces of 16 tokens took
 // 342 registers, one wave a SIMD and 0.4 ms more; the matrix unit's fp32 products for the sums over
 // channels take their cycles from the vector unit and cost 0.35 ms.
+// Two waves a SIMD are left at N = 9 .. 32 only (88 % busy at 32; fp32 at N = 17 .. 32 with 4 to 10 registers spilled).
+// Below, tiles of 16 tokens of 64 and 32 channels a wave take 294 to 458 registers; above, the staged tiles leave room in
+// the LDS for one workgroup a CU (105 KB at N = 33 .. 64; 102 at 65 .. 128, with 410 registers and more). One wave a
+// SIMD keeps the vector unit 57 % (N = 4), 59 (8), 52 (64) and 42 (128) busy; at 128 LDS bank conflicts take a
+// third of the cycles besides. The same tokens at N = 4, 8, 32, 64, 128: 0.67, 0.97, 2.37, 7.5, 19.7 ms; fp32 at
+// 4 .. 128: 0.86, 1.09, 1.24, 2.47, 7.7, 19.2.
 #include <type_traits>
 
 #include "selective.h"
