@@ -444,9 +444,19 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *                   ceil(2 T G N / 256) + ceil(D (N + 2) / 256)
  *     step          batch ceil(D / c)
  *   RMS norm        its rows
+ * and for the operators of the gated layer
+ *   gated scan      R ceil(D / 128), D / 64 for an odd D; R = S, or at most 2048 / ceil(D / 128) + 2 S segments
+ *     backward      the same with R = S ceil(seqlen / 64) (padded) or S + ceil(seqlen / 64) (packed), 32 with fp32;
+ *                   and S ceil(D / 64)
+ *     step          ceil(batch ceil(D / 4) / 256)
+ *   group norm      at most 2048 or G, whatever its rows (fewer than 2^31)
+ *   state cache     n ceil(values / 2048)
  */
 
-#define MAMBA3_LAYER_OPERATORS 1
+/* 1: the convolution, the selective scan and the RMS norm; 2: the gated scan, the
+ * group norm and the state cache too (which came together: a program that loads the
+ * library at run time looks for mamba3_gated_scan_fwd). */
+#define MAMBA3_LAYER_OPERATORS 2
 
 /* Short causal convolution over every channel by itself, width W = 2..8:
  *   p_t[d] = bias[d] + sum_{j < W} weight[d, j] x_{t - W + 1 + j}[d]
@@ -669,6 +679,183 @@ typedef struct {
 mamba3_status mamba3_rmsnorm_bwd_validate(const mamba3_rmsnorm_bwd_args *args);
 size_t mamba3_rmsnorm_bwd_workspace_size(const mamba3_rmsnorm_bwd_args *args);
 mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *args, void *stream);
+
+/* ---- Operators of a gated recurrent layer -----------------------------------
+ *
+ * Gated linear recurrence: one state a channel, its decay a gate of its own. Per
+ * sequence and channel d
+ *   h_t = a_t h_{t-1} + u_t v_t,  v_t = x_t, sigmoid(i_t) x_t with i
+ *   y_t = h_t, h_t SiLU(z_t) with z
+ *   MAMBA3_GATE_DECAY   a_t = exp(-rate softplus(weight[d]) sigmoid(gate_t)),
+ *                       u_t = sqrt(1 - a_t^2)
+ *   MAMBA3_GATE_FORGET  a_t = l + (1 - l) sigmoid(gate_t),  u_t = 1 - a_t, with the
+ *                       least decay l = weight[d] of [0, 1] (0 without weight)
+ * x, gate, i, z, y  [batch, seqlen, D] token dtype; i and z may be NULL
+ * weight            [D] fp32; with MAMBA3_GATE_FORGET it may be NULL
+ * rate              finite and >= 0 (not read with MAMBA3_GATE_FORGET)
+ * h_in, h_out       [S, D] fp32 or NULL (zero, not written)
+ * Token rows, cu_seqlens, nseq and tokens outside the sequences are as above. Sigmoids
+ * take their arguments at -87 at least. States are fp32, and 1 - a^2 keeps its relative
+ * precision where a is next to 1, down to 2^-126 (a u below 2^-63 may count as 0). y overlaps no input; h_out may be h_in
+ * exactly. workspace: at least mamba3_gated_scan_workspace_size(args) bytes (0 for
+ * many shapes), 256-byte aligned: where few sequences would leave the GPU empty, they run
+ * as segments and it holds their decays, states and token ranges. */
+typedef enum { MAMBA3_GATE_DECAY = 0, MAMBA3_GATE_FORGET = 1 } mamba3_gate_form;
+
+typedef struct {
+    int32_t batch, seqlen, dim;
+    int32_t dtype;
+    int32_t form;
+    float rate;
+    const int32_t *cu_seqlens;
+    int32_t nseq;
+    int64_t x_row, gate_row, i_row, z_row;
+    const void *x, *gate, *i, *z;
+    const float *weight;
+    const float *h_in;
+    void *y;
+    float *h_out;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_gated_scan_args;
+
+mamba3_status mamba3_gated_scan_validate(const mamba3_gated_scan_args *args);
+size_t mamba3_gated_scan_workspace_size(const mamba3_gated_scan_args *args);
+mamba3_status mamba3_gated_scan_fwd(const mamba3_gated_scan_args *args, void *stream);
+
+/* Its backward. fwd is the forward call's (y, h_out and workspace are ignored; nothing of
+ * the forward pass needs to be kept). dy [batch, seqlen, D] (dy_row as x_row), dh_out
+ * [S, D] fp32 or NULL (zero).
+ * Outputs, overwritten, dense: dx, dgate, di (only with i, or NULL) and dz (only with z, or
+ * NULL) [batch, seqlen, D] token dtype; dweight [D] fp32 or NULL (only with weight);
+ * dh_in [S, D] fp32 or NULL. Where u counts as 0 no gradient reaches gate and weight
+ * through it. No output overlaps an input or another
+ * output. workspace: at least mamba3_gated_scan_bwd_workspace_size(args) bytes, 256-byte
+ * aligned: decays, states and gradients between runs of 64 tokens (32 with fp32) and partial
+ * sums of dweight, 16 bytes a run and channel; all sums have a fixed order
+ * (bitwise reproducible). */
+typedef struct {
+    mamba3_gated_scan_args fwd;
+    int64_t dy_row;
+    const void *dy;
+    const float *dh_out;
+    void *dx, *dgate, *di, *dz;
+    float *dweight;
+    float *dh_in;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_gated_scan_bwd_args;
+
+mamba3_status mamba3_gated_scan_bwd_validate(const mamba3_gated_scan_bwd_args *args);
+size_t mamba3_gated_scan_bwd_workspace_size(const mamba3_gated_scan_bwd_args *args);
+mamba3_status mamba3_gated_scan_bwd(const mamba3_gated_scan_bwd_args *args, void *stream);
+
+/* One token for a batch, states updated in place. x, gate, i, z, y [batch, D]; h [batch,
+ * D] fp32, or [nslots, D] with slots (as in mamba3_conv_step). */
+typedef struct {
+    int32_t batch, dim;
+    int32_t dtype;
+    int32_t form;
+    float rate;
+    int64_t x_row, gate_row, i_row, z_row;
+    const void *x, *gate, *i, *z;
+    const float *weight;
+    float *h;
+    void *y;
+    const int32_t *slots;
+    int32_t nslots;
+} mamba3_gated_step_args;
+
+mamba3_status mamba3_gated_step_validate(const mamba3_gated_step_args *args);
+mamba3_status mamba3_gated_step(const mamba3_gated_step_args *args, void *stream);
+
+/* Group norm of rows with an activation or gate, in fp32. A row's dim channels are G = groups
+ * groups of M = dim / G consecutive ones (the heads of a layer, channels innermost); a
+ * group has its statistics from its own row alone, so a token never reaches an earlier one:
+ *   t = x, x SiLU(z) with MAMBA3_GN_PREGATE
+ *   n = (t - mean(t)) / sqrt(mean((t - mean(t))^2) + eps)   center = 1
+ *   n = t / sqrt(mean(t^2) + eps)                           center = 0
+ *   v = n weight + bias
+ *   y = v, v sigmoid(v) with MAMBA3_GN_SILU, v SiLU(z) with MAMBA3_GN_GATE
+ * x, z, y       [rows, dim] token dtype; z with MAMBA3_GN_GATE and MAMBA3_GN_PREGATE only
+ * weight, bias  [dim] fp32 or NULL (ones, zeros)
+ * groups divides dim, M <= 8192; rows < 2^31; eps is finite and >= 0. The mean is taken off before
+ * squares are summed. As in the RMS norm, a group whose mean square leaves fp32's range is
+ * summed scaled by a power of two. Outputs overlap neither each other nor any input. */
+typedef enum { MAMBA3_GN_NONE = 0, MAMBA3_GN_SILU = 1, MAMBA3_GN_GATE = 2, MAMBA3_GN_PREGATE = 3 } mamba3_gn_act;
+
+typedef struct {
+    int64_t rows;
+    int32_t dim, groups;
+    int32_t dtype;
+    int32_t act, center;
+    float eps;
+    int64_t x_row, z_row;
+    const void *x, *z;
+    const float *weight, *bias;
+    void *y;
+} mamba3_groupnorm_args;
+
+mamba3_status mamba3_groupnorm_validate(const mamba3_groupnorm_args *args);
+mamba3_status mamba3_groupnorm_fwd(const mamba3_groupnorm_args *args, void *stream);
+
+/* Its backward. fwd is the forward call's (y is ignored); dy [rows, dim] (dy_row as x_row).
+ * Outputs, overwritten, dense: dx and dz (only with z, or NULL) [rows, dim] token dtype;
+ * dweight, dbias [dim] fp32 or NULL (only with weight, with bias). No output overlaps an
+ * input or another output. workspace: at least mamba3_groupnorm_bwd_workspace_size(args)
+ * bytes, 256-byte aligned: partial sums of dweight and dbias, added in a fixed order (bitwise
+ * reproducible). */
+typedef struct {
+    mamba3_groupnorm_args fwd;
+    int64_t dy_row;
+    const void *dy;
+    void *dx, *dz;
+    float *dweight, *dbias;
+    void *workspace;
+    size_t workspace_bytes;
+} mamba3_groupnorm_bwd_args;
+
+mamba3_status mamba3_groupnorm_bwd_validate(const mamba3_groupnorm_bwd_args *args);
+size_t mamba3_groupnorm_bwd_workspace_size(const mamba3_groupnorm_bwd_args *args);
+mamba3_status mamba3_groupnorm_bwd(const mamba3_groupnorm_bwd_args *args, void *stream);
+
+/* Cache of recurrent states in 8 or 4 bits: the states of sequences that are put aside (a
+ * shared prompt's, a preempted sequence's), written from the pool that the steps work on and
+ * read back into it. Row k of a call moves state slots[k] of the pool h (or k without slots)
+ * to (store) or from (load) entry entries[k] of the cache (or k):
+ *   scale = max(largest |value| of a block / top, 2^-126),  q = round(value / scale)
+ *   value = q scale
+ * kind   MAMBA3_CACHE_E4M3 (OCP e4m3, top 448), MAMBA3_CACHE_INT8 (top 127), MAMBA3_CACHE_INT4
+ *        (top 7; two a byte, the even value in the low half, two's complement)
+ * block  32, 64, 128 or 256 consecutive values a scale, the last block of a state as many as
+ *        are left
+ * h      [nslots, values] in dtype (states are fp32; the convolution's and the previous
+ *        token's have the token dtype)
+ * q      [nentries, values] bytes, ceil(values / 2) with INT4;  scale [nentries, ceil(values / block)] fp32
+ * The scale and the quotient are rounded to fp32, then the quotient to the nearest of the kind, ties to
+ * even; value is rounded once to dtype. A block that holds an infinity or a NaN has
+ * the scale NaN and reads back as NaN. slots and entries are int32 [n] on the device; a row
+ * with either outside its range is skipped, and whatever is not named stays as it was. Rows of
+ * one call name different entries (store) or different slots (load). n values < 2^35 (see Sizes);
+ * h overlaps neither q nor scale, and those not each other. Loading reads any bytes: an INT4
+ * half of -8 is -8, an INT8 byte of -128 is -128, an e4m3 NaN is a NaN. */
+typedef enum { MAMBA3_CACHE_E4M3 = 0, MAMBA3_CACHE_INT8 = 1, MAMBA3_CACHE_INT4 = 2 } mamba3_cache_kind;
+
+typedef struct {
+    int32_t n;
+    int32_t values;
+    int32_t dtype;
+    int32_t kind, block;
+    int32_t nslots, nentries;
+    const int32_t *slots, *entries;
+    void *h;
+    void *q;
+    float *scale;
+} mamba3_state_cache_args;
+
+mamba3_status mamba3_state_cache_validate(const mamba3_state_cache_args *args);
+mamba3_status mamba3_state_store(const mamba3_state_cache_args *args, void *stream);
+mamba3_status mamba3_state_load(const mamba3_state_cache_args *args, void *stream);
 
 /* Static description of a status code. */
 const char *mamba3_status_string(mamba3_status status);

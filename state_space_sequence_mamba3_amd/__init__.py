@@ -421,9 +421,14 @@ def mamba3_decode_step(x, dt, lam, theta, B, C, A, D=None, *, h, y=None, Bprev=N
 
 
 from . import layer  # noqa: E402  (the layer operators' bindings use the names above)
-from .layer import (LAYER_EXPORTS, MAMBA3_E4M3, MAMBA3_INT8, ConvArgs, ConvBwdArgs, ConvStepArgs,  # noqa: E402, F401
-                    RmsnormArgs, RmsnormBwdArgs, SelectiveScanArgs, SelectiveScanBwdArgs, SelectiveStepArgs,
-                    mamba3_conv_bwd, mamba3_conv_fwd, mamba3_conv_step, mamba3_rmsnorm_bwd, mamba3_rmsnorm_fwd,
-                    mamba3_selective_scan_bwd, mamba3_selective_scan_fwd, mamba3_selective_step)
+from .layer import (LAYER_EXPORTS, MAMBA3_CACHE_E4M3, MAMBA3_CACHE_INT4, MAMBA3_CACHE_INT8,  # noqa: E402, F401
+                    MAMBA3_E4M3, MAMBA3_GATE_DECAY, MAMBA3_GATE_FORGET, MAMBA3_GN_GATE, MAMBA3_GN_NONE,
+                    MAMBA3_GN_PREGATE, MAMBA3_GN_SILU, MAMBA3_INT8, ConvArgs, ConvBwdArgs, ConvStepArgs,
+                    GatedScanArgs, GatedScanBwdArgs, GatedStepArgs, GroupnormArgs, GroupnormBwdArgs, RmsnormArgs,
+                    RmsnormBwdArgs, SelectiveScanArgs, SelectiveScanBwdArgs, SelectiveStepArgs, StateCacheArgs,
+                    mamba3_conv_bwd, mamba3_conv_fwd, mamba3_conv_step, mamba3_gated_scan_bwd, mamba3_gated_scan_fwd,
+                    mamba3_gated_step, mamba3_groupnorm_bwd, mamba3_groupnorm_fwd, mamba3_rmsnorm_bwd,
+                    mamba3_rmsnorm_fwd, mamba3_selective_scan_bwd, mamba3_selective_scan_fwd, mamba3_selective_step,
+                    mamba3_state_load, mamba3_state_store)
 
 EXPORTS += LAYER_EXPORTS

@@ -1,0 +1,283 @@
+// Shared parts of the gated linear recurrence's forward and backward kernels.
+//
+// A wave holds 64 V consecutive channels, V a lane (2 where the channel count is even, so that a token's
+// load is 4 bytes of bf16 or 8 of fp32 a lane, else 1), and K consecutive tokens of each in registers.
+// The recurrence over a run of tokens is h -> P h + H with P the product of their decays and H their
+// state from zero; the gradient's, from its end to its start, is g -> P g + E with the same P. Runs are joined in
+// order: (P2 P1, P2 H1 + H2) and (P1 P2, E1 + P1 E2).
+#pragma once
+
+#include "layer.h"
+
+namespace m3 {
+
+struct GateParams {
+    const void *x, *gate, *i, *z, *dy;
+    const float *weight, *h_in, *dh_out;
+    void *y, *dx, *dgate, *di, *dz;
+    float *h_out, *dh_in;
+    int64_t x_row, gate_row, i_row, z_row, dy_row;    // elements from one token to the next
+    const int32_t *cu;          // packed batches, or NULL
+    int32_t nseq;               // sequences (padded: the batch)
+    int32_t seqlen, total;      // tokens of a padded sequence, tokens of the batch
+    int32_t dim, tiles;         // channels, workgroups that cover them
+    float rate;
+    // Rows of tokens that a workgroup takes: a sequence each (nseg 1), or its runs of seg_tokens tokens: nseg
+    // a sequence of a padded batch, or those of the table of a packed one.
+    int32_t rows, nseg, seg_tokens;
+    const int4 *table;          // t0, t1, sequence (-1: no run), 1 first | 2 last of its sequence
+    const int32_t *seq_row;     // [nseq + 1] a sequence's first row in the table
+    float *P;                   // [rows][D] a run's product of decays
+    float *H;                   // [rows][D] its last state from zero, then the state entering it
+    float *E;                   // [rows][D] its share of the gradient that enters the run before, then the one entering it
+    float *part;                // [rows][D] partial sums of dweight
+};
+
+struct GateRow {
+    int t0, t1, seq;
+    bool first, last;
+};
+
+// Row r, in scalar registers
+__device__ __forceinline__ GateRow gate_row(const GateParams &p, int r) {
+    GateRow o;
+    o.first = o.last = true;
+    if (p.table) {
+        const int4 e = p.table[r];
+        o.t0 = e.x;
+        o.t1 = e.y;
+        o.seq = e.z;
+        o.first = e.w & 1;
+        o.last = e.w & 2;
+    } else if (p.cu) {
+        o.seq = r;
+        packed_bounds(p.cu, r, p.total, o.t0, o.t1);
+    } else {
+        const int k = r % p.nseg, a = r / p.nseg * p.seqlen;
+        o.seq = r / p.nseg;
+        o.t0 = a + (int)min((int64_t)k * p.seg_tokens, (int64_t)p.seqlen);
+        o.t1 = (int)min((int64_t)o.t0 + p.seg_tokens, (int64_t)a + p.seqlen);
+        o.first = k == 0;
+        o.last = k == p.nseg - 1;
+    }
+    o.t0 = __builtin_amdgcn_readfirstlane(o.t0);
+    o.t1 = __builtin_amdgcn_readfirstlane(o.t1);
+    o.seq = __builtin_amdgcn_readfirstlane(o.seq);
+    o.first = __builtin_amdgcn_readfirstlane(o.first);
+    o.last = __builtin_amdgcn_readfirstlane(o.last);
+    return o;
+}
+
+// V elements of a token, at any element: global memory takes loads and stores of 4 and 8 bytes there.
+template <typename T, int V> struct PieceOf { typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T)))); };
+template <typename T, int V> using piece = typename PieceOf<T, V>::type;
+
+// The token's address is the same for all lanes and stays in scalar registers, the lane's offset has 32 bits.
+template <typename T, int V>
+__device__ __forceinline__ piece<T, V> load_piece(const void *base, int64_t elements, uint32_t lane_bytes) {
+    return *(const piece<T, V> *)((const char *)((const T *)base + elements) + lane_bytes);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_piece(void *base, int64_t elements, uint32_t lane_bytes, const float (&v)[V]) {
+    piece<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; e++) o[e] = from_f<T>(v[e]);
+    *(piece<T, V> *)((char *)((T *)base + elements) + lane_bytes) = o;
+}
+
+// e^v to an ulp or so for any v: what the product v log2(e) rounds away is put back.
+__device__ __forceinline__ float exp_full(float v) {
+    const float hi = v * kLog2e, lo = fmaf(v, kLog2e, -hi) + v * 1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e, lo * 0.69314718056f, e);
+}
+
+// A channel's constants. Decay: c0 = -rate softplus(w), c1 = c0 log2(e). Forget: c0 = l, c1 = 1 - l.
+// softplus is taken exactly: an error in it is one of every decay of the channel, and adds up over the
+// length of its memory.
+template <int FORM>
+__device__ __forceinline__ void gate_channel(const GateParams &p, int c, float &c0, float &c1) {
+    if constexpr (FORM == MAMBA3_GATE_DECAY) {
+        const float w = p.weight[c], e = exp_full(fminf(w, 30.f)), u = 1.f + e, r = e - (u - 1.f);
+        const float l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, r * __builtin_amdgcn_rcpf(u));
+        // below 2^-12 the logarithm of 1 + e is e - e^2 / 2, which log2 of a number next to 1 is not
+        const float soft = w > 20.f ? w : e < 0x1p-12f ? fmaf(-0.5f * e, e, e) : l;
+        c0 = -p.rate * soft;
+        c1 = c0 * kLog2e;
+    } else {
+        c0 = p.weight ? p.weight[c] : 0.f;
+        c1 = 1.f - c0;
+    }
+}
+
+// sigmoid(v) and 1 - sigmoid(v), both to their relative precision
+__device__ __forceinline__ void sigmoids(float v, float &s, float &n) {
+    const float e = __builtin_amdgcn_exp2f(fmaxf(v, -87.f) * -kLog2e);
+    s = __builtin_amdgcn_rcpf(1.f + e);
+    n = e * s;
+}
+__device__ __forceinline__ float sigmoid_low(float v) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fmaxf(v, -87.f) * -kLog2e));
+}
+
+// 1 - e^{2 y} for y <= 0: the series where the difference would cancel (its next term is 2^-26 of it at
+// y = -1/8), the difference elsewhere
+__device__ __forceinline__ float one_minus_square(float y, float a) {
+    float s = fmaf(y, 4.f / 315.f, 2.f / 45.f);
+    s = fmaf(y, s, 2.f / 15.f);
+    s = fmaf(y, s, 1.f / 3.f);
+    s = fmaf(y, s, 2.f / 3.f);
+    s = fmaf(y, s, 1.f);
+    s = fmaf(y, s, 1.f);
+    return y > -0.125f ? -2.f * y * s : fmaf(-a, a, 1.f);
+}
+
+// A token's decay and what its input is taken by
+template <int FORM>
+__device__ __forceinline__ void gate_open(float g, float c0, float c1, float &a, float &u) {
+    if constexpr (FORM == MAMBA3_GATE_DECAY) {
+        const float s = sigmoid_low(g);
+        a = __builtin_amdgcn_exp2f(c1 * s);
+        u = __builtin_amdgcn_sqrtf(one_minus_square(c0 * s, a));
+    } else {
+        float s, n;
+        sigmoids(g, s, n);
+        u = c1 * n;
+        a = fmaf(c1, s, c0);
+    }
+}
+
+template <typename T, int V, int FORM, bool IG, int K>
+struct GateRaw {
+    piece<T, V> x[K], g[K], i[IG ? K : 1];
+
+    // tokens t .. t + K - 1, those from `end` on as the one before it
+    template <bool WHOLE>
+    __device__ __forceinline__ void fetch(const GateParams &p, int t, int end, uint32_t lane) {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int64_t at = WHOLE ? t + k : min(t + k, end - 1);
+            g[k] = load_piece<T, V>(p.gate, at * p.gate_row, lane);
+            x[k] = load_piece<T, V>(p.x, at * p.x_row, lane);
+            if (IG) i[k] = load_piece<T, V>(p.i, at * p.i_row, lane);
+        }
+    }
+    __device__ __forceinline__ void open(int k, const float (&c0)[V], const float (&c1)[V], float (&a)[V], float (&b)[V]) const {
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            float u;
+            gate_open<FORM>(to_f(g[k][e]), c0[e], c1[e], a[e], u);
+            b[e] = u * to_f(x[k][e]);
+            if (IG) b[e] *= sigmoid_low(to_f(i[k][e]));
+        }
+    }
+};
+
+template <typename T, int V, int K>
+__device__ __forceinline__ void fetch_rows(piece<T, V> (&o)[K], const void *base, int64_t row, int t, int end, uint32_t lane) {
+#pragma unroll
+    for (int k = 0; k < K; k++) o[k] = load_piece<T, V>(base, (int64_t)min(t + k, end - 1) * row, lane);
+}
+
+// The runs' P and H, and with BACK their E. A workgroup has a run of 64 V channels, W waves with
+// consecutive shares of its tokens.
+template <typename T, int V, int FORM, bool IG, bool ZG, bool BACK, int W>
+__global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
+    constexpr int K = sizeof(T) == 2 ? 8 : 4;
+    __shared__ float join[3][W][V][64];
+    const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const GateRow row = gate_row(p, r);
+    if (row.seq < 0 || (!BACK && row.last)) return;     // (nothing takes up a last run's end)
+    const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
+    const uint32_t at = cc * (uint32_t)sizeof(T);
+    float c0[V], c1[V], P[V], H[V], E[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        gate_channel<FORM>(p, cc + e, c0[e], c1[e]);
+        P[e] = 1.f;
+        H[e] = E[e] = 0.f;
+    }
+    const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
+    const int begin = (int)min((int64_t)row.t0 + (int64_t)wave * share, (int64_t)row.t1);
+    const int end = (int)min((int64_t)begin + share, (int64_t)row.t1);
+    for (int t = begin; t < end; t += K) {
+        GateRaw<T, V, FORM, IG, K> raw;
+        piece<T, V> rd[BACK ? K : 1], rz[BACK && ZG ? K : 1];
+        if (t + K <= end) raw.template fetch<true>(p, t, end, at);
+        else raw.template fetch<false>(p, t, end, at);
+        if constexpr (BACK) fetch_rows<T, V, K>(rd, p.dy, p.dy_row, t, end, at);
+        if constexpr (BACK && ZG) fetch_rows<T, V, K>(rz, p.z, p.z_row, t, end, at);
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            if (t + k >= end) break;
+            float a[V], b[V];
+            raw.open(k, c0, c1, a, b);
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                P[e] *= a[e];
+                H[e] = fmaf(a[e], H[e], b[e]);
+                if constexpr (BACK) {
+                    float d = to_f(rd[k][e]);
+                    if constexpr (ZG) {
+                        const float z = to_f(rz[k][e]);
+                        d *= z * sigmoid_low(z);
+                    }
+                    E[e] = fmaf(P[e], d, E[e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        join[0][wave][e][lane] = P[e];
+        join[1][wave][e][lane] = H[e];
+        if (BACK) join[2][wave][e][lane] = E[e];
+    }
+    __syncthreads();
+    if (wave || c >= p.dim) return;
+#pragma unroll
+    for (int w = 1; w < W; w++)
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            const float a = join[0][w][e][lane];
+            if (BACK) E[e] = fmaf(P[e], join[2][w][e][lane], E[e]);
+            H[e] = fmaf(a, H[e], join[1][w][e][lane]);
+            P[e] *= a;
+        }
+    const int64_t o = (int64_t)r * p.dim + c;
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        p.P[o + e] = P[e];
+        p.H[o + e] = H[e];
+        if (BACK) p.E[o + e] = E[e];
+    }
+}
+
+// Template arguments from a call's values: V, FORM, IG, ZG
+#define M3_GATE_DISPATCH(p, form, CALL)                                        \
+    do {                                                                       \
+        const bool two_ = (p).dim % 2 == 0, ig_ = (p).i, zg_ = (p).z;          \
+        if ((form) == MAMBA3_GATE_DECAY) {                                     \
+            if (two_) M3_GATE_D2(2, MAMBA3_GATE_DECAY, CALL);                  \
+            else M3_GATE_D2(1, MAMBA3_GATE_DECAY, CALL);                       \
+        } else {                                                               \
+            if (two_) M3_GATE_D2(2, MAMBA3_GATE_FORGET, CALL);                 \
+            else M3_GATE_D2(1, MAMBA3_GATE_FORGET, CALL);                      \
+        }                                                                      \
+    } while (0)
+#define M3_GATE_D2(V, FORM, CALL)                                              \
+    do {                                                                       \
+        if (ig_ && zg_) CALL(V, FORM, true, true);                             \
+        else if (ig_) CALL(V, FORM, true, false);                              \
+        else if (zg_) CALL(V, FORM, false, true);                              \
+        else CALL(V, FORM, false, false);                                      \
+    } while (0)
+
+GateParams gate_params(const mamba3_gated_scan_args *a);
+// The parts of a call's workspace that the runs take, and the table's launch
+size_t gate_run_bytes(const GateParams &p, bool back);
+char *gate_runs(GateParams &p, char *ws, bool back);
+void launch_gate_table(const GateParams &p, hipStream_t st);
+void launch_gate_chain(const GateParams &p, hipStream_t st);
+
+}  // namespace m3

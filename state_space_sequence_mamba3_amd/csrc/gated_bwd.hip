@@ -1,0 +1,249 @@
+// Backward of the gated linear recurrence.
+//
+//   G_t = r_t + a_{t+1} G_{t+1},  r = dy SiLU(z)                     (dh_out at a sequence's end)
+//   dv = u G,  dx = dv sigmoid(i),  di = dv x sigmoid'(i),  dz = dy h SiLU'(z)
+//   decay   q = G a la (h_{t-1} - v a / u),  la = log a:  dgate = q (1 - s),  dw = sigmoid(w) / softplus(w) sum q
+//   forget  q = G (h_{t-1} - v) (1 - s):                  dgate = q (1 - l) s, dl = sum q     (s = sigmoid(g))
+//
+// la / u tends to zero where the gate closes and u does, so q needs no case but u = 0 (or 1 - a^2 subnormal).
+// Every run of W K tokens is a workgroup's by itself, with the tokens in registers: k_gate_part reads the
+// inputs for the runs' (P, H, E), k_gate_chain turns them into the state that enters a run and the gradient that
+// enters it from behind, and k_gate_bwd reads the inputs again, joins its waves' shares of the run in both
+// directions, and goes over its tokens forwards for the states and backwards for the gradients. Nothing walks a
+// sequence, so that one long sequence fills the GPU as a batch does, for a second read of the inputs.
+#include <algorithm>
+
+#include "gated.h"
+
+namespace m3 {
+
+constexpr int kGateBwdWaves = 8;
+template <typename T> constexpr int gate_bwd_tokens() { return sizeof(T) == 2 ? 8 : 4; }     // a wave's
+
+template <typename T, int V, int FORM, bool IG, bool ZG>
+__global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p) {
+    constexpr int W = kGateBwdWaves, K = gate_bwd_tokens<T>();
+    __shared__ float join[3][W][V][64];
+    const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const GateRow row = gate_row(p, r);
+    const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
+    const int64_t o = (int64_t)r * p.dim + cc;
+    if (row.seq < 0 || row.t0 >= row.t1) {              // no tokens: nothing but a row of partial sums
+        if (p.part && wave == 0 && c < p.dim)
+#pragma unroll
+            for (int e = 0; e < V; e++) p.part[o + e] = 0.f;
+        return;
+    }
+    const uint32_t at = cc * (uint32_t)sizeof(T);
+    const int t = row.t0 + wave * K, mine = min(row.t1 - t, K);
+    GateRaw<T, V, FORM, IG, K> raw;
+    piece<T, V> rd[K], rz[ZG ? K : 1];
+    if (mine == K) raw.template fetch<true>(p, t, row.t1, at);
+    else if (mine > 0) raw.template fetch<false>(p, t, row.t1, at);
+    if (mine > 0) fetch_rows<T, V, K>(rd, p.dy, p.dy_row, t, row.t1, at);
+    if constexpr (ZG)
+        if (mine > 0) fetch_rows<T, V, K>(rz, p.z, p.z_row, t, row.t1, at);
+    float c0[V], c1[V], s[V], g[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        gate_channel<FORM>(p, cc + e, c0[e], c1[e]);
+        s[e] = p.H[o + e];
+        g[e] = p.E[o + e];
+    }
+    // a, b = u v and r of the wave's tokens
+    float a[K][V], h[K][V], d[K][V], P[V], H[V], E[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        P[e] = 1.f;
+        H[e] = E[e] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        if (k < mine) {
+            raw.open(k, c0, c1, a[k], h[k]);
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                d[k][e] = to_f(rd[k][e]);
+                if constexpr (ZG) {
+                    const float z = to_f(rz[k][e]);
+                    d[k][e] *= z * sigmoid_low(z);
+                }
+                P[e] *= a[k][e];
+                H[e] = fmaf(a[k][e], H[e], h[k][e]);
+                E[e] = fmaf(P[e], d[k][e], E[e]);
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        join[0][wave][e][lane] = P[e];
+        join[1][wave][e][lane] = H[e];
+        join[2][wave][e][lane] = E[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W - 1; w++)
+        if (w < wave)
+#pragma unroll
+            for (int e = 0; e < V; e++) s[e] = fmaf(join[0][w][e][lane], s[e], join[1][w][e][lane]);
+#pragma unroll
+    for (int w = W - 1; w > 0; w--)
+        if (w > wave)
+#pragma unroll
+            for (int e = 0; e < V; e++) g[e] = fmaf(join[0][w][e][lane], g[e], join[2][w][e][lane]);
+    // the states before the tokens; dz from those behind them
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        if (k < mine) {
+            float dz[V];
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float was = s[e];
+                s[e] = fmaf(a[k][e], s[e], h[k][e]);
+                h[k][e] = was;
+                if constexpr (ZG) {
+                    const float z = to_f(rz[k][e]), q = sigmoid_low(z);
+                    dz[e] = to_f(rd[k][e]) * s[e] * (q * fmaf(z, 1.f - q, 1.f));
+                }
+            }
+            if (ZG && p.dz && c < p.dim) store_piece<T, V>(p.dz, (int64_t)(t + k) * p.dim, at, dz);
+        }
+    float dw[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) dw[e] = 0.f;
+#pragma unroll
+    for (int k = K - 1; k >= 0; k--)
+        if (k < mine) {
+            float dx[V], di[V], dg[V];
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float x = to_f(raw.x[k][e]), G = d[k][e] + g[e];
+                float sg, ng, si = 1.f, ni = 0.f, u, q;
+                sigmoids(to_f(raw.g[k][e]), sg, ng);
+                if (IG) sigmoids(to_f(raw.i[k][e]), si, ni);
+                const float v = x * si;
+                if constexpr (FORM == MAMBA3_GATE_DECAY) {
+                    const float la = c0[e] * sg, w = one_minus_square(la, a[k][e]), i = w >= 0x1p-126f ? __builtin_amdgcn_rsqf(w) : 0.f;
+                    u = w * i;
+                    q = G * (a[k][e] * la) * (h[k][e] - v * (a[k][e] * i));
+                    dg[e] = q * ng;
+                } else {
+                    u = c1[e] * ng;
+                    q = G * (h[k][e] - v) * ng;
+                    dg[e] = q * (c1[e] * sg);
+                }
+                dw[e] += q;
+                const float dv = u * G;
+                dx[e] = dv * si;
+                if (IG) di[e] = dv * v * ni;
+                g[e] = a[k][e] * G;
+            }
+            if (c < p.dim) {
+                const int64_t to = (int64_t)(t + k) * p.dim;
+                store_piece<T, V>(p.dx, to, at, dx);
+                store_piece<T, V>(p.dgate, to, at, dg);
+                if (IG && p.di) store_piece<T, V>(p.di, to, at, di);
+            }
+        }
+    if (!p.part) return;
+    __syncthreads();                                    // (the joins are read)
+#pragma unroll
+    for (int e = 0; e < V; e++) join[0][wave][e][lane] = dw[e];
+    __syncthreads();
+    if (wave || c >= p.dim) return;
+#pragma unroll
+    for (int w = 1; w < W; w++)
+#pragma unroll
+        for (int e = 0; e < V; e++) dw[e] += join[0][w][e][lane];
+#pragma unroll
+    for (int e = 0; e < V; e++) p.part[o + e] = dw[e];
+}
+
+// dweight from the runs' partial sums: 16 channels a workgroup, 16 threads over the rows of each.
+template <int FORM>
+__global__ __launch_bounds__(256) void k_gate_reduce(GateParams p, float *dweight) {
+    __shared__ float red[16][17];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, c = blockIdx.x * 16 + x;
+    float s = 0.f;
+    if (c < p.dim) {
+#pragma unroll 8
+        for (int i = y; i < p.rows; i += 16) s += p.part[(int64_t)i * p.dim + c];
+    }
+    red[y][x] = s;
+    __syncthreads();
+    if (y || c >= p.dim) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i++) s += red[i][x];
+    if constexpr (FORM == MAMBA3_GATE_DECAY) {
+        // sigmoid(w) / softplus(w): 1 - e^w / 2 .. where both are e^w
+        const float w = p.weight[c], e = exp_full(fminf(w, 80.f));
+        const float u = 1.f + e, l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
+        s *= w > 20.f ? 1.f / w : e < 0x1p-12f ? 1.f - 0.5f * e : e / (u * l);
+    }
+    dweight[c] = s;
+}
+
+namespace {
+
+GateParams bwd_plan(const mamba3_gated_scan_bwd_args *b) {
+    const mamba3_gated_scan_args *a = &b->fwd;
+    GateParams p = gate_params(a);
+    p.dy = b->dy;
+    p.dh_out = b->dh_out;
+    p.dy_row = b->dy_row ? b->dy_row : a->dim;
+    p.dx = b->dx; p.dgate = b->dgate; p.di = b->di; p.dz = b->dz;
+    p.dh_in = b->dh_in;
+    p.seg_tokens = kGateBwdWaves * (a->dtype == MAMBA3_BF16 ? gate_bwd_tokens<bf16>() : gate_bwd_tokens<float>());
+    // (at least one run a sequence, also of a sequence without tokens)
+    p.nseg = std::max((p.seqlen + p.seg_tokens - 1) / p.seg_tokens, 1);
+    const int64_t runs = (p.total + p.seg_tokens - 1) / p.seg_tokens;
+    const int64_t rows = p.cu ? p.nseq + runs : (int64_t)p.nseq * p.nseg;
+    p.rows = (int32_t)std::min<int64_t>(rows, INT32_MAX);      // (more are refused for their workgroups)
+    return p;
+}
+
+template <typename T>
+void bwd_go(const GateParams &p, int form, hipStream_t st) {
+    const dim3 grid((uint32_t)((int64_t)p.rows * p.tiles));
+#define M3_GO(V, FORM, IG, ZG) \
+    hipLaunchKernelGGL((k_gate_part<T, V, FORM, IG, ZG, true, 4>), grid, dim3(256), 0, st, p)
+    M3_GATE_DISPATCH(p, form, M3_GO);
+#undef M3_GO
+    launch_gate_chain(p, st);
+#define M3_GO(V, FORM, IG, ZG) \
+    hipLaunchKernelGGL((k_gate_bwd<T, V, FORM, IG, ZG>), grid, dim3(64 * kGateBwdWaves), 0, st, p)
+    M3_GATE_DISPATCH(p, form, M3_GO);
+#undef M3_GO
+}
+
+}  // namespace
+
+size_t gated_scan_bwd_workspace_bytes(const mamba3_gated_scan_bwd_args *b) {
+    const GateParams p = bwd_plan(b);
+    return p.rows ? gate_run_bytes(p, true) : 0;
+}
+
+int64_t gated_scan_bwd_workgroups(const mamba3_gated_scan_bwd_args *b) {
+    const GateParams p = bwd_plan(b);
+    return std::max((int64_t)p.rows * p.tiles, (int64_t)p.nseq * ((p.dim + 63) / 64));
+}
+
+mamba3_status launch_gated_scan_bwd(const mamba3_gated_scan_bwd_args *b, hipStream_t st) {
+    GateParams p = bwd_plan(b);
+    const int form = b->fwd.form;
+    gate_runs(p, (char *)b->workspace, true);
+    if (!b->dweight) p.part = nullptr;
+    if (p.rows) {
+        launch_gate_table(p, st);
+        if (b->fwd.dtype == MAMBA3_F32) bwd_go<float>(p, form, st);
+        else bwd_go<bf16>(p, form, st);
+    }
+    if (b->dweight) {
+        const dim3 grid((uint32_t)((p.dim + 15) / 16));
+        if (form == MAMBA3_GATE_DECAY) hipLaunchKernelGGL(k_gate_reduce<MAMBA3_GATE_DECAY>, grid, dim3(256), 0, st, p, b->dweight);
+        else hipLaunchKernelGGL(k_gate_reduce<MAMBA3_GATE_FORGET>, grid, dim3(256), 0, st, p, b->dweight);
+    }
+    return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+}
+
+}  // namespace m3

@@ -329,4 +329,184 @@ mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *b, void *stream)
     return st != MAMBA3_OK ? st : m3::launch_rmsnorm_bwd(b, (hipStream_t)stream);
 }
 
+// ---- gated linear recurrence ----
+static mamba3_status gated_shape(const mamba3_gated_scan_args *a, int64_t *S, int64_t *T) {
+    if (!a) return MAMBA3_EINVAL;
+    if (!dtype_ok(a->dtype) || (a->form != MAMBA3_GATE_DECAY && a->form != MAMBA3_GATE_FORGET) || a->dim < 1 ||
+        !row_ok(a->x_row, a->dim) || !row_ok(a->gate_row, a->dim) || !row_ok(a->i_row, a->dim) || !row_ok(a->z_row, a->dim))
+        return MAMBA3_EINVAL;
+    if (a->form == MAMBA3_GATE_DECAY && !(a->rate >= 0.f && std::isfinite(a->rate))) return MAMBA3_EINVAL;
+    return check_batch(a->batch, a->seqlen, a->cu_seqlens, a->nseq, S, T);
+}
+static mamba3_status gated_fwd_shape(const mamba3_gated_scan_args *a, int64_t *S, int64_t *T) {
+    const mamba3_status st = gated_shape(a, S, T);
+    if (st != MAMBA3_OK) return st;
+    return m3::gated_scan_workgroups(a) <= kMaxBlocks ? MAMBA3_OK : MAMBA3_EINVAL;
+}
+static mamba3_status gated_bwd_shape(const mamba3_gated_scan_bwd_args *b, int64_t *S, int64_t *T) {
+    if (!b) return MAMBA3_EINVAL;
+    const mamba3_status st = gated_shape(&b->fwd, S, T);
+    if (st != MAMBA3_OK) return st;
+    return m3::gated_scan_bwd_workgroups(b) <= kMaxBlocks ? MAMBA3_OK : MAMBA3_EINVAL;
+}
+
+size_t mamba3_gated_scan_workspace_size(const mamba3_gated_scan_args *a) {
+    int64_t S, T;
+    return gated_fwd_shape(a, &S, &T) == MAMBA3_OK ? m3::gated_scan_workspace_bytes(a) : 0;
+}
+
+mamba3_status mamba3_gated_scan_validate(const mamba3_gated_scan_args *a) {
+    int64_t S, T;
+    mamba3_status st = gated_fwd_shape(a, &S, &T);
+    if (st != MAMBA3_OK) return st;
+    const int64_t es = esize(a->dtype), D = a->dim;
+    const Arr in[] = {rows_of(a->x, T, a->x_row, D, es, true), rows_of(a->gate, T, a->gate_row, D, es, true),
+                      rows_of(a->i, T, a->i_row, D, es, false), rows_of(a->z, T, a->z_row, D, es, false),
+                      dense_of(a->weight, D, 4, a->form == MAMBA3_GATE_DECAY), dense_of(a->h_in, S * D, 4, false),
+                      dense_of(a->cu_seqlens, a->cu_seqlens ? S + 1 : 0, 4, false)};
+    const Arr out[] = {dense_of(a->y, T * D, es, true), dense_of(a->h_out, S * D, 4, false)};
+    if ((st = check_arrays(in, out, 5, 1)) != MAMBA3_OK) return st;
+    return check_workspace(a->workspace, a->workspace_bytes, m3::gated_scan_workspace_bytes(a), in, out);
+}
+
+mamba3_status mamba3_gated_scan_fwd(const mamba3_gated_scan_args *a, void *stream) {
+    const mamba3_status st = mamba3_gated_scan_validate(a);
+    if (st != MAMBA3_OK || (a->cu_seqlens ? a->nseq : a->batch) == 0) return st;
+    return m3::launch_gated_scan(a, (hipStream_t)stream);
+}
+
+size_t mamba3_gated_scan_bwd_workspace_size(const mamba3_gated_scan_bwd_args *b) {
+    int64_t S, T;
+    return gated_bwd_shape(b, &S, &T) == MAMBA3_OK ? m3::gated_scan_bwd_workspace_bytes(b) : 0;
+}
+
+mamba3_status mamba3_gated_scan_bwd_validate(const mamba3_gated_scan_bwd_args *b) {
+    int64_t S, T;
+    mamba3_status st = gated_bwd_shape(b, &S, &T);
+    if (st != MAMBA3_OK) return st;
+    const mamba3_gated_scan_args *a = &b->fwd;
+    if (!row_ok(b->dy_row, a->dim) || (b->di && !a->i) || (b->dz && !a->z) || (b->dweight && !a->weight))
+        return MAMBA3_EINVAL;
+    const int64_t es = esize(a->dtype), D = a->dim;
+    const Arr in[] = {rows_of(a->x, T, a->x_row, D, es, true), rows_of(a->gate, T, a->gate_row, D, es, true),
+                      rows_of(a->i, T, a->i_row, D, es, false), rows_of(a->z, T, a->z_row, D, es, false),
+                      dense_of(a->weight, D, 4, a->form == MAMBA3_GATE_DECAY), dense_of(a->h_in, S * D, 4, false),
+                      dense_of(a->cu_seqlens, a->cu_seqlens ? S + 1 : 0, 4, false),
+                      rows_of(b->dy, T, b->dy_row, D, es, true), dense_of(b->dh_out, S * D, 4, false)};
+    const Arr out[] = {dense_of(b->dx, T * D, es, true), dense_of(b->dgate, T * D, es, true),
+                       dense_of(b->di, T * D, es, false), dense_of(b->dz, T * D, es, false),
+                       dense_of(b->dweight, D, 4, false), dense_of(b->dh_in, S * D, 4, false)};
+    if ((st = check_arrays(in, out)) != MAMBA3_OK) return st;
+    return check_workspace(b->workspace, b->workspace_bytes, m3::gated_scan_bwd_workspace_bytes(b), in, out);
+}
+
+mamba3_status mamba3_gated_scan_bwd(const mamba3_gated_scan_bwd_args *b, void *stream) {
+    const mamba3_status st = mamba3_gated_scan_bwd_validate(b);
+    return st != MAMBA3_OK ? st : m3::launch_gated_scan_bwd(b, (hipStream_t)stream);
+}
+
+mamba3_status mamba3_gated_step_validate(const mamba3_gated_step_args *a) {
+    if (!a) return MAMBA3_EINVAL;
+    if (!dtype_ok(a->dtype) || (a->form != MAMBA3_GATE_DECAY && a->form != MAMBA3_GATE_FORGET) || a->batch < 0 ||
+        a->dim < 1 || (a->slots && a->nslots < 0) || !row_ok(a->x_row, a->dim) || !row_ok(a->gate_row, a->dim) ||
+        !row_ok(a->i_row, a->dim) || !row_ok(a->z_row, a->dim))
+        return MAMBA3_EINVAL;
+    if (a->form == MAMBA3_GATE_DECAY && !(a->rate >= 0.f && std::isfinite(a->rate))) return MAMBA3_EINVAL;
+    if (m3::gated_step_workgroups(a) > kMaxBlocks) return MAMBA3_EINVAL;
+    const int64_t es = esize(a->dtype), D = a->dim, b = a->batch;
+    const Arr in[] = {rows_of(a->x, b, a->x_row, D, es, true), rows_of(a->gate, b, a->gate_row, D, es, true),
+                      rows_of(a->i, b, a->i_row, D, es, false), rows_of(a->z, b, a->z_row, D, es, false),
+                      dense_of(a->weight, D, 4, a->form == MAMBA3_GATE_DECAY), dense_of(a->slots, a->slots ? b : 0, 4, false)};
+    const Arr out[] = {dense_of(a->y, b * D, es, true), dense_of(a->h, (a->slots ? a->nslots : b) * D, 4, b > 0)};
+    return check_arrays(in, out);
+}
+
+mamba3_status mamba3_gated_step(const mamba3_gated_step_args *a, void *stream) {
+    const mamba3_status st = mamba3_gated_step_validate(a);
+    if (st != MAMBA3_OK || a->batch == 0) return st;
+    return m3::launch_gated_step(a, (hipStream_t)stream);
+}
+
+// ---- group norm ----
+static mamba3_status gn_shape(const mamba3_groupnorm_args *a) {
+    if (!a) return MAMBA3_EINVAL;
+    if (a->rows < 0 || a->dim < 1 || a->groups < 1 || a->dim % a->groups || !dtype_ok(a->dtype) || !flag(a->center) ||
+        a->act < MAMBA3_GN_NONE || a->act > MAMBA3_GN_PREGATE || !row_ok(a->x_row, a->dim) || !row_ok(a->z_row, a->dim))
+        return MAMBA3_EINVAL;
+    if (!(a->eps >= 0.f && std::isfinite(a->eps))) return MAMBA3_EINVAL;
+    const bool gated = a->act == MAMBA3_GN_GATE || a->act == MAMBA3_GN_PREGATE;
+    if (a->z && !gated) return MAMBA3_EINVAL;
+    if (a->rows > INT32_MAX) return MAMBA3_EINVAL;    // (workgroups walk rows: launches stay small)
+    return a->dim / a->groups <= 8192 ? MAMBA3_OK : MAMBA3_EUNSUPPORTED;
+}
+
+mamba3_status mamba3_groupnorm_validate(const mamba3_groupnorm_args *a) {
+    const mamba3_status st = gn_shape(a);
+    if (st != MAMBA3_OK) return st;
+    const int64_t es = esize(a->dtype), D = a->dim;
+    const bool gated = a->act == MAMBA3_GN_GATE || a->act == MAMBA3_GN_PREGATE;
+    const Arr in[] = {rows_of(a->x, a->rows, a->x_row, D, es, true), rows_of(a->z, a->rows, a->z_row, D, es, gated),
+                      dense_of(a->weight, D, 4, false), dense_of(a->bias, D, 4, false)};
+    const Arr out[] = {dense_of(a->y, a->rows * D, es, true)};
+    return check_arrays(in, out);
+}
+
+mamba3_status mamba3_groupnorm_fwd(const mamba3_groupnorm_args *a, void *stream) {
+    const mamba3_status st = mamba3_groupnorm_validate(a);
+    if (st != MAMBA3_OK || a->rows == 0) return st;
+    return m3::launch_groupnorm(a, (hipStream_t)stream);
+}
+
+size_t mamba3_groupnorm_bwd_workspace_size(const mamba3_groupnorm_bwd_args *b) {
+    return b && gn_shape(&b->fwd) == MAMBA3_OK ? m3::groupnorm_bwd_workspace_bytes(b) : 0;
+}
+
+mamba3_status mamba3_groupnorm_bwd_validate(const mamba3_groupnorm_bwd_args *b) {
+    if (!b) return MAMBA3_EINVAL;
+    const mamba3_groupnorm_args *a = &b->fwd;
+    mamba3_status st = gn_shape(a);
+    if (st != MAMBA3_OK) return st;
+    if (!row_ok(b->dy_row, a->dim) || (b->dz && !a->z) || (b->dweight && !a->weight) || (b->dbias && !a->bias))
+        return MAMBA3_EINVAL;
+    const int64_t es = esize(a->dtype), D = a->dim;
+    const bool gated = a->act == MAMBA3_GN_GATE || a->act == MAMBA3_GN_PREGATE;
+    const Arr in[] = {rows_of(a->x, a->rows, a->x_row, D, es, true), rows_of(a->z, a->rows, a->z_row, D, es, gated),
+                      dense_of(a->weight, D, 4, false), dense_of(a->bias, D, 4, false),
+                      rows_of(b->dy, a->rows, b->dy_row, D, es, true)};
+    const Arr out[] = {dense_of(b->dx, a->rows * D, es, true), dense_of(b->dz, a->rows * D, es, false),
+                       dense_of(b->dweight, D, 4, false), dense_of(b->dbias, D, 4, false)};
+    if ((st = check_arrays(in, out)) != MAMBA3_OK) return st;
+    return check_workspace(b->workspace, b->workspace_bytes, m3::groupnorm_bwd_workspace_bytes(b), in, out);
+}
+
+mamba3_status mamba3_groupnorm_bwd(const mamba3_groupnorm_bwd_args *b, void *stream) {
+    const mamba3_status st = mamba3_groupnorm_bwd_validate(b);
+    return st != MAMBA3_OK ? st : m3::launch_groupnorm_bwd(b, (hipStream_t)stream);
+}
+
+// ---- state cache ----
+mamba3_status mamba3_state_cache_validate(const mamba3_state_cache_args *a) {
+    if (!a) return MAMBA3_EINVAL;
+    if (!dtype_ok(a->dtype) || a->kind < MAMBA3_CACHE_E4M3 || a->kind > MAMBA3_CACHE_INT4 || a->n < 0 || a->values < 1 ||
+        a->nslots < 0 || a->nentries < 0 || (!a->slots && a->nslots < a->n) || (!a->entries && a->nentries < a->n))
+        return MAMBA3_EINVAL;
+    if (a->block != 32 && a->block != 64 && a->block != 128 && a->block != 256) return MAMBA3_EUNSUPPORTED;
+    if (a->values > (1 << 30) || m3::state_cache_workgroups(a) > kMaxBlocks) return MAMBA3_EINVAL;
+    const int64_t n = a->n, blocks = ((int64_t)a->values + a->block - 1) / a->block;
+    const int64_t bytes = a->kind == MAMBA3_CACHE_INT4 ? ((int64_t)a->values + 1) / 2 : a->values;
+    const Arr in[] = {dense_of(a->slots, a->slots ? n : 0, 4, false), dense_of(a->entries, a->entries ? n : 0, 4, false)};
+    const Arr out[] = {dense_of(a->h, (int64_t)a->nslots * a->values, esize(a->dtype), n > 0),
+                       dense_of(a->q, a->nentries * bytes, 1, n > 0), dense_of(a->scale, a->nentries * blocks, 4, n > 0)};
+    return check_arrays(in, out);
+}
+
+static mamba3_status cache_call(const mamba3_state_cache_args *a, bool store, void *stream) {
+    const mamba3_status st = mamba3_state_cache_validate(a);
+    if (st != MAMBA3_OK || a->n == 0 || a->nslots == 0 || a->nentries == 0) return st;
+    return m3::launch_state_cache(a, store, (hipStream_t)stream);
+}
+
+mamba3_status mamba3_state_store(const mamba3_state_cache_args *a, void *stream) { return cache_call(a, true, stream); }
+mamba3_status mamba3_state_load(const mamba3_state_cache_args *a, void *stream) { return cache_call(a, false, stream); }
+
 }  // extern "C"

@@ -131,5 +131,18 @@ mamba3_status launch_selective_step(const mamba3_selective_step_args *a, hipStre
 mamba3_status launch_rmsnorm(const mamba3_rmsnorm_args *a, hipStream_t st);
 size_t rmsnorm_bwd_workspace_bytes(const mamba3_rmsnorm_bwd_args *b);
 mamba3_status launch_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *b, hipStream_t st);
+int64_t gated_scan_workgroups(const mamba3_gated_scan_args *a);
+int64_t gated_scan_bwd_workgroups(const mamba3_gated_scan_bwd_args *b);
+int64_t gated_step_workgroups(const mamba3_gated_step_args *a);
+int64_t state_cache_workgroups(const mamba3_state_cache_args *a);
+mamba3_status launch_gated_scan(const mamba3_gated_scan_args *a, hipStream_t st);
+size_t gated_scan_workspace_bytes(const mamba3_gated_scan_args *a);
+mamba3_status launch_gated_scan_bwd(const mamba3_gated_scan_bwd_args *b, hipStream_t st);
+size_t gated_scan_bwd_workspace_bytes(const mamba3_gated_scan_bwd_args *b);
+mamba3_status launch_gated_step(const mamba3_gated_step_args *a, hipStream_t st);
+mamba3_status launch_groupnorm(const mamba3_groupnorm_args *a, hipStream_t st);
+size_t groupnorm_bwd_workspace_bytes(const mamba3_groupnorm_bwd_args *b);
+mamba3_status launch_groupnorm_bwd(const mamba3_groupnorm_bwd_args *b, hipStream_t st);
+mamba3_status launch_state_cache(const mamba3_state_cache_args *a, bool store, hipStream_t st);
 
 }  // namespace m3

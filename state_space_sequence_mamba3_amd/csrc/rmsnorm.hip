@@ -15,11 +15,9 @@
 // dweight's third (51 us); 4096 x 8200 104 and 261, where dweight's 129 workgroups leave half the CUs idle (91 us).
 #include <type_traits>
 
-#include "layer.h"
+#include "norm.h"
 
 namespace m3 {
-
-constexpr int kNV = 8;    // consecutive values of a lane
 
 struct NormParams {
     const void *x, *res, *dy, *dres;     // (backward: x is s)
@@ -31,73 +29,6 @@ struct NormParams {
     float eps;
 };
 
-// 8 values at any element: global memory takes loads and stores of 8 or 16 bytes there, in one
-// instruction each, which rows of odd lengths (VEC false) use up to their last piece.
-template <typename T> struct Loose8 { typedef T type __attribute__((ext_vector_type(8), aligned(sizeof(T)))); };
-
-// 8 values of a row from column c on; zeros behind the row's end
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(float (&o)[kNV], const T *row, int c, int n) {
-    if constexpr (VEC) {
-        if (c < n) {
-            if constexpr (sizeof(T) == 2) {
-                const bf16x8 v = *(const bf16x8 *)(row + c);
-#pragma unroll
-                for (int e = 0; e < 8; e++) o[e] = to_f(v[e]);
-            } else {
-                const f32x4 a = *(const f32x4 *)(row + c), b = *(const f32x4 *)(row + c + 4);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    o[e] = a[e];
-                    o[e + 4] = b[e];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++) o[e] = 0.f;
-        }
-    } else if (c + 8 <= n) {
-        const typename Loose8<T>::type v = *(const typename Loose8<T>::type *)(row + c);
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = to_f(v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = c + e < n ? to_f(row[c + e]) : 0.f;
-    }
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *row, int c, int n, const float (&o)[kNV]) {
-    if constexpr (VEC) {
-        if (c < n) {
-            if constexpr (sizeof(T) == 2) {
-                bf16x8 v;
-#pragma unroll
-                for (int e = 0; e < 8; e++) v[e] = from_f<bf16>(o[e]);
-                *(bf16x8 *)(row + c) = v;
-            } else {
-                *(f32x4 *)(row + c) = f32x4{o[0], o[1], o[2], o[3]};
-                *(f32x4 *)(row + c + 4) = f32x4{o[4], o[5], o[6], o[7]};
-            }
-        }
-    } else if (c + 8 <= n) {
-        typename Loose8<T>::type v;
-#pragma unroll
-        for (int e = 0; e < 8; e++) v[e] = from_f<T>(o[e]);
-        *(typename Loose8<T>::type *)(row + c) = v;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (c + e < n) row[c + e] = from_f<T>(o[e]);
-    }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-    v += dpp_move<0xB1>(v);
-    v += dpp_move<0x4E>(v);
-    v += dpp_move<0x141>(v);    // half-row mirror: the other quad of 8
-    v += dpp_move<0x140>(v);    // row mirror: the other 8 of 16
-    return sum_across_rows(v);
-}
 // The larger of two values, NaN if either is (a NaN in a block shows in its scale).
 __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
 
@@ -129,13 +60,6 @@ __device__ __forceinline__ float row_max(float v, float *red) {
     }
     return v;
 }
-
-// Squares leave fp32's range long before the values do: a row whose mean square + eps is no number of
-// [2^-80, infinity) is summed again with its values times a power of two, `row_scale` of that mean, which
-// brings every finite row back inside.
-constexpr float kLeastMean = 0x1p-80f;
-__device__ __forceinline__ bool in_range(float mean) { return mean >= kLeastMean && mean < INFINITY; }
-__device__ __forceinline__ float row_scale(float mean) { return mean < kLeastMean ? 0x1p100f : 0x1p-80f; }
 
 constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126: a block of zeros divides by it
 
@@ -273,25 +197,6 @@ __global__ __launch_bounds__(256) void k_norm(NormParams p) {
     }
 }
 
-// 8 values as loaded, converted where they are used: the next row's loads are in flight while a row is
-// worked on.
-template <typename T> struct Raw8 { typedef T type __attribute__((ext_vector_type(8), aligned(16))); };
-template <typename T, bool VEC>
-__device__ __forceinline__ typename Raw8<T>::type raw8(const T *row, int c, int n) {
-    typename Raw8<T>::type v;
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = from_f<T>(0.f);
-    if constexpr (VEC) {
-        if (c < n) v = *(const typename Raw8<T>::type *)(row + c);
-    } else if (c + 8 <= n) {
-        v = *(const typename Loose8<T>::type *)(row + c);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (c + e < n) v[e] = row[c + e];
-    }
-    return v;
-}
 // Two sums over the waves of a row, with one barrier: `red` is the row's half of two, used in turn.
 template <int WPR>
 __device__ __forceinline__ void row_sums(float &a, float &b, float2 *red) {

@@ -1,5 +1,6 @@
 """Bindings of the layer operators around the recurrence (``include/mamba3.h``, "Operators of the
-layers"): the short causal convolution, the selective scan and the residual RMS norm.
+layers" and "Operators of a gated recurrent layer"): the short causal convolution, the selective scan and
+the residual RMS norm; the gated linear recurrence, the group norm and the cache of states in 8 or 4 bits.
 
 As in the package's other bindings, every step of the computation runs in the library's HIP kernels;
 this module checks shapes, types and devices, allocates outputs and workspaces where they are not
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import struct
 
 from . import MAMBA3_BF16, MAMBA3_F32, MAMBA3_OK, Mamba3Error, lib
@@ -22,6 +24,12 @@ _f32 = ctypes.c_float
 _size = ctypes.c_size_t
 
 MAMBA3_E4M3, MAMBA3_INT8 = 0, 1
+MAMBA3_GATE_DECAY, MAMBA3_GATE_FORGET = 0, 1
+MAMBA3_GN_NONE, MAMBA3_GN_SILU, MAMBA3_GN_GATE, MAMBA3_GN_PREGATE = range(4)
+MAMBA3_CACHE_E4M3, MAMBA3_CACHE_INT8, MAMBA3_CACHE_INT4 = range(3)
+
+_FORMS = {"decay": MAMBA3_GATE_DECAY, "forget": MAMBA3_GATE_FORGET}
+_ACTS = {"none": MAMBA3_GN_NONE, "silu": MAMBA3_GN_SILU, "gate": MAMBA3_GN_GATE, "pregate": MAMBA3_GN_PREGATE}
 
 
 @functools.lru_cache(None)
@@ -34,6 +42,13 @@ def _dtypes():
 def _qtypes():
     import torch
     return {"e4m3": (MAMBA3_E4M3, torch.float8_e4m3fn), "int8": (MAMBA3_INT8, torch.int8)}
+
+
+@functools.lru_cache(None)
+def _kinds():
+    import torch
+    return {"e4m3": (MAMBA3_CACHE_E4M3, torch.float8_e4m3fn), "int8": (MAMBA3_CACHE_INT8, torch.int8),
+            "int4": (MAMBA3_CACHE_INT4, torch.uint8)}
 
 
 class ConvArgs(ctypes.Structure):
@@ -95,15 +110,61 @@ class RmsnormBwdArgs(ctypes.Structure):
                 ("dresidual", _vp), ("dweight", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
 
 
+class GatedScanArgs(ctypes.Structure):
+    """Mirror of ``mamba3_gated_scan_args``."""
+    _fields_ = [("batch", _i32), ("seqlen", _i32), ("dim", _i32), ("dtype", _i32), ("form", _i32), ("rate", _f32),
+                ("cu_seqlens", _vp), ("nseq", _i32), ("x_row", _i64), ("gate_row", _i64), ("i_row", _i64),
+                ("z_row", _i64), ("x", _vp), ("gate", _vp), ("i", _vp), ("z", _vp), ("weight", _vp), ("h_in", _vp),
+                ("y", _vp), ("h_out", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class GatedScanBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba3_gated_scan_bwd_args``."""
+    _fields_ = [("fwd", GatedScanArgs), ("dy_row", _i64), ("dy", _vp), ("dh_out", _vp), ("dx", _vp), ("dgate", _vp),
+                ("di", _vp), ("dz", _vp), ("dweight", _vp), ("dh_in", _vp), ("workspace", _vp),
+                ("workspace_bytes", _size)]
+
+
+class GatedStepArgs(ctypes.Structure):
+    """Mirror of ``mamba3_gated_step_args``."""
+    _fields_ = [("batch", _i32), ("dim", _i32), ("dtype", _i32), ("form", _i32), ("rate", _f32), ("x_row", _i64),
+                ("gate_row", _i64), ("i_row", _i64), ("z_row", _i64), ("x", _vp), ("gate", _vp), ("i", _vp),
+                ("z", _vp), ("weight", _vp), ("h", _vp), ("y", _vp), ("slots", _vp), ("nslots", _i32)]
+
+
+class GroupnormArgs(ctypes.Structure):
+    """Mirror of ``mamba3_groupnorm_args``."""
+    _fields_ = [("rows", _i64), ("dim", _i32), ("groups", _i32), ("dtype", _i32), ("act", _i32), ("center", _i32),
+                ("eps", _f32), ("x_row", _i64), ("z_row", _i64), ("x", _vp), ("z", _vp), ("weight", _vp),
+                ("bias", _vp), ("y", _vp)]
+
+
+class GroupnormBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba3_groupnorm_bwd_args``."""
+    _fields_ = [("fwd", GroupnormArgs), ("dy_row", _i64), ("dy", _vp), ("dx", _vp), ("dz", _vp), ("dweight", _vp),
+                ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class StateCacheArgs(ctypes.Structure):
+    """Mirror of ``mamba3_state_cache_args``."""
+    _fields_ = [("n", _i32), ("values", _i32), ("dtype", _i32), ("kind", _i32), ("block", _i32), ("nslots", _i32),
+                ("nentries", _i32), ("slots", _vp), ("entries", _vp), ("h", _vp), ("q", _vp), ("scale", _vp)]
+
+
 # name -> (argument struct, whether there is a workspace query)
 _OPS = {"conv": (ConvArgs, "fwd", False), "conv_bwd": (ConvBwdArgs, "", True), "conv_step": (ConvStepArgs, "", False),
         "selective_scan": (SelectiveScanArgs, "fwd", True), "selective_scan_bwd": (SelectiveScanBwdArgs, "", True),
         "selective_step": (SelectiveStepArgs, "", False), "rmsnorm": (RmsnormArgs, "fwd", False),
-        "rmsnorm_bwd": (RmsnormBwdArgs, "", True)}
+        "rmsnorm_bwd": (RmsnormBwdArgs, "", True), "gated_scan": (GatedScanArgs, "fwd", True),
+        "gated_scan_bwd": (GatedScanBwdArgs, "", True), "gated_step": (GatedStepArgs, "", False),
+        "groupnorm": (GroupnormArgs, "fwd", False), "groupnorm_bwd": (GroupnormBwdArgs, "", True)}
+# entry points with one struct and one validation between them
+_CACHE = ("state_store", "state_load")
 
 LAYER_EXPORTS = tuple(n for op, (_, tail, ws) in _OPS.items()
                       for n in (f"mamba3_{op}_validate", f"mamba3_{op}" + (f"_{tail}" if tail else ""),
-                                *([f"mamba3_{op}_workspace_size"] if ws else [])))
+                                *([f"mamba3_{op}_workspace_size"] if ws else []))) + \
+    ("mamba3_state_cache_validate", *(f"mamba3_{op}" for op in _CACHE))
 
 
 def declare(l) -> None:
@@ -116,6 +177,10 @@ def declare(l) -> None:
         if ws:
             f = getattr(l, f"mamba3_{op}_workspace_size")
             f.argtypes, f.restype = [ctypes.POINTER(args)], _size
+    for name in ("mamba3_state_cache_validate", *(f"mamba3_{op}" for op in _CACHE)):
+        f = getattr(l, name)
+        f.argtypes = [ctypes.POINTER(StateCacheArgs)] + ([] if name.endswith("validate") else [_vp])
+        f.restype = ctypes.c_int
 
 
 def _bad(what):
@@ -128,7 +193,7 @@ class _Op:
     _CODES = {_i32: "i", _i64: "q", _f32: "f", _vp: "P", _size: "N"}
 
     def __init__(self, op):
-        args, tail, ws = _OPS[op]
+        args, tail, ws = _OPS[op] if op in _OPS else (StateCacheArgs, "", False)
         fields = [f for _, k in args._fields_ for f in ([c for _, c in k._fields_] if hasattr(k, "_fields_") else [k])]
         inner = [k for _, k in args._fields_ if hasattr(k, "_fields_")]
         # native alignment as in C; an inner struct ends at a multiple of 8 bytes
@@ -559,3 +624,259 @@ def mamba3_rmsnorm_bwd(s, weight=None, *, dy, dresidual_out=None, eps=1e-5, want
     ws, wp, wn = _workspace(op, a, workspace, dev)
     _call(op, op.pack(*a, wp, wn), dev)
     return g
+
+
+# ----------------------------------------------------------------------------- gated linear recurrence
+def _form(form, rate):
+    if form not in _FORMS:
+        _bad(f"form must be one of {sorted(_FORMS)}, got {form!r}")
+    return _FORMS[form], float(rate)
+
+
+def _gated_args(x, gate, weight, form, rate, i, z, h_in, cu_seqlens):
+    import torch
+    code, ty, dev = _token(x, 3)
+    b, L, D = x.shape
+    fc, rate = _form(form, rate)
+    cu, nseq, S = _packed(x, cu_seqlens)
+    xp, xr = _rows(x, x.shape, 2, ty, dev, "x")
+    gp, gr = _rows(gate, x.shape, 2, ty, dev, "gate")
+    ip, ir = _rows(i, x.shape, 2, ty, dev, "i")
+    zp, zr = _rows(z, x.shape, 2, ty, dev, "z")
+    f = torch.float32
+    a = (b, L, D, code, fc, rate, cu, nseq, xr, gr, ir, zr, xp, gp, ip, zp, _dense(weight, (D,), f, dev, "weight"),
+         _dense(h_in, (S, D), f, dev, "h_in"))
+    return a, ty, dev, S
+
+
+def mamba3_gated_scan_fwd(x, gate, weight=None, *, form="decay", rate=8.0, i=None, z=None, h_in=None, cu_seqlens=None,
+                          y=None, h_out=None, want_state=True, workspace=None, stream=None):
+    """Gated linear recurrence: h_t = a_t h_{t-1} + u_t sigmoid(i_t) x_t (x_t alone without i), y_t = h_t
+    (h_t SiLU(z_t) with z). form "decay": a = exp(-rate softplus(weight) sigmoid(gate)), u = sqrt(1 -
+    a^2); "forget": a = l + (1 - l) sigmoid(gate) with the least decay l = weight (0 without), u = 1 - a.
+    x, gate, i, z [batch, seqlen, D]; weight [D], h_in [S, D] fp32. Returns (y, h_out [S, D] or None with
+    want_state=False)."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_gated_scan_fwd(x, gate, weight, form=form, rate=rate, i=i, z=z, h_in=h_in,
+                                         cu_seqlens=cu_seqlens, y=y, h_out=h_out, want_state=want_state,
+                                         workspace=workspace)
+    a, ty, dev, S = _gated_args(x, gate, weight, form, rate, i, z, h_in, cu_seqlens)
+    if y is None:
+        y = _new(x, ty)
+    if h_out is None and want_state:
+        h_out = torch.empty((S, x.shape[2]), dtype=torch.float32, device=x.device)
+    a += (_dense(y, x.shape, ty, dev, "y"), _dense(h_out, (S, x.shape[2]), torch.float32, dev, "h_out"))
+    op = _op("gated_scan")
+    ws, wp, wn = _workspace(op, a, workspace, dev)
+    _call(op, op.pack(*a, wp, wn), dev)
+    return y, h_out
+
+
+def mamba3_gated_scan_bwd(x, gate, weight=None, *, dy, dh_out=None, form="decay", rate=8.0, i=None, z=None, h_in=None,
+                          cu_seqlens=None, want_dh_in=None, workspace=None, stream=None):
+    """Gradients of mamba3_gated_scan_fwd from dy and dh_out [S, D] (None: zero): a dict of dx, dgate, and di,
+    dz, dweight, dh_in where the input exists (dh_in always with want_dh_in=True)."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_gated_scan_bwd(x, gate, weight, dy=dy, dh_out=dh_out, form=form, rate=rate, i=i, z=z,
+                                         h_in=h_in, cu_seqlens=cu_seqlens, want_dh_in=want_dh_in, workspace=workspace)
+    a, ty, dev, S = _gated_args(x, gate, weight, form, rate, i, z, h_in, cu_seqlens)
+    g = dict(dx=_new(x, ty), dgate=_new(x, ty))
+    if i is not None:
+        g["di"] = _new(x, ty)
+    if z is not None:
+        g["dz"] = _new(x, ty)
+    if weight is not None:
+        g["dweight"] = torch.empty_like(weight)
+    if h_in is not None if want_dh_in is None else want_dh_in:
+        g["dh_in"] = torch.empty((S, x.shape[2]), dtype=torch.float32, device=x.device)
+    yp, yr = _rows(dy, x.shape, 2, ty, dev, "dy")
+    p = {k: v.data_ptr() for k, v in g.items()}
+    q = (*a, 0, 0, 0, 0, yr, yp, _dense(dh_out, (S, x.shape[2]), torch.float32, dev, "dh_out"),
+         *[p.get(k, 0) for k in ("dx", "dgate", "di", "dz", "dweight", "dh_in")])
+    op = _op("gated_scan_bwd")
+    ws, wp, wn = _workspace(op, q, workspace, dev)
+    _call(op, op.pack(*q, wp, wn), dev)
+    return g
+
+
+def mamba3_gated_step(x, gate, weight=None, *, h, form="decay", rate=8.0, i=None, z=None, slots=None, y=None,
+                      stream=None):
+    """One token of the gated linear recurrence: x, gate, i, z [batch, D]; h [batch, D] (fp32) is updated
+    in place. With slots (int32 [batch] on the device) h is a pool [nslots, D]; rows with a slot outside the
+    pool are skipped (their y rows stay as they were). Returns y."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_gated_step(x, gate, weight, h=h, form=form, rate=rate, i=i, z=z, slots=slots, y=y)
+    code, ty, dev = _token(x, 2)
+    b, D = x.shape
+    fc, rate = _form(form, rate)
+    if y is None:
+        y = _new(x, ty)
+    f = torch.float32
+    sp, ns, states = _slots(slots, b, h, dev)
+    xp, xr = _rows(x, x.shape, 1, ty, dev, "x")
+    gp, gr = _rows(gate, x.shape, 1, ty, dev, "gate")
+    ip, ir = _rows(i, x.shape, 1, ty, dev, "i")
+    zp, zr = _rows(z, x.shape, 1, ty, dev, "z")
+    op = _op("gated_step")
+    a = op.pack(b, D, code, fc, rate, xr, gr, ir, zr, xp, gp, ip, zp, _dense(weight, (D,), f, dev, "weight"),
+                _dense(h, (states, D), f, dev, "h"), _dense(y, (b, D), ty, dev, "y"), sp, ns)
+    _call(op, a, dev)
+    return y
+
+
+# ----------------------------------------------------------------------------- group norm
+def _groupnorm_args(x, weight, bias, groups, z, act, center, eps):
+    import torch
+    dim = x.shape[-1] if x.dim() else 0
+    if act not in _ACTS:
+        _bad(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    flat = x if x.dim() == 2 else x.reshape(-1, dim) if dim else x
+    code, ty, dev = _token(flat, 2)
+    rows = flat.shape[0]
+    if z is not None and z.shape != x.shape:
+        _bad(f"z must have shape {tuple(x.shape)}, got {tuple(z.shape)}")
+    xp, xr = _rows(flat, (rows, dim), 1, ty, dev, "x")
+    # (kept until the call: a view of more dimensions may have been copied)
+    zf = z if z is None or z.dim() == 2 else z.reshape(-1, dim)
+    zp, zr = _rows(zf, (rows, dim), 1, ty, dev, "z")
+    f = torch.float32
+    a = (rows, dim, groups, code, _ACTS[act], 1 if center else 0, eps, xr, zr, xp, zp,
+         _dense(weight, (dim,), f, dev, "weight"), _dense(bias, (dim,), f, dev, "bias"))
+    return a, ty, dev, (flat, zf)
+
+
+def mamba3_groupnorm_fwd(x, weight=None, bias=None, *, groups, z=None, act="none", center=True, eps=1e-5, y=None,
+                         stream=None):
+    """Group norm over the last dimension of x [..., dim], whose channels are `groups` groups of consecutive
+    ones with statistics of their own row: v = (t - mean) / sqrt(var + eps) weight + bias (center=False: t /
+    sqrt(mean t^2 + eps) weight + bias), t = x. act "none": v; "silu": v sigmoid(v); "gate": v SiLU(z);
+    "pregate": v of t = x SiLU(z). weight, bias [dim] fp32. Returns y."""
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_groupnorm_fwd(x, weight, bias, groups=groups, z=z, act=act, center=center, eps=eps, y=y)
+    a, ty, dev, kept = _groupnorm_args(x, weight, bias, groups, z, act, center, eps)
+    if y is None:
+        y = _new(x, ty)
+    op = _op("groupnorm")
+    _call(op, op.pack(*a, _dense(y, x.shape, ty, dev, "y")), dev)
+    return y
+
+
+def mamba3_groupnorm_bwd(x, weight=None, bias=None, *, dy, groups, z=None, act="none", center=True, eps=1e-5,
+                         workspace=None, stream=None):
+    """Gradients of mamba3_groupnorm_fwd from dy: a dict of dx, and dz, dweight, dbias where the input
+    exists."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return mamba3_groupnorm_bwd(x, weight, bias, dy=dy, groups=groups, z=z, act=act, center=center, eps=eps,
+                                        workspace=workspace)
+    if dy.shape != x.shape:
+        _bad(f"dy must have shape {tuple(x.shape)}, got {tuple(dy.shape)}")
+    a, ty, dev, kept = _groupnorm_args(x, weight, bias, groups, z, act, center, eps)
+    g = dict(dx=_new(x, ty))
+    if z is not None:
+        g["dz"] = _new(x, ty)
+    if weight is not None:
+        g["dweight"] = torch.empty_like(weight)
+    if bias is not None:
+        g["dbias"] = torch.empty_like(bias)
+    df = dy if dy.dim() == 2 else dy.reshape(-1, x.shape[-1])
+    yp, yr = _rows(df, kept[0].shape, 1, ty, dev, "dy")
+    p = {k: v.data_ptr() for k, v in g.items()}
+    q = (*a, 0, yr, yp, *[p.get(k, 0) for k in ("dx", "dz", "dweight", "dbias")])
+    op = _op("groupnorm_bwd")
+    ws, wp, wn = _workspace(op, q, workspace, dev)
+    _call(op, op.pack(*q, wp, wn), dev)
+    return g
+
+
+# ----------------------------------------------------------------------------- state cache
+def _cache_index(t, name, dev):
+    import torch
+    if t is None:
+        return 0, None
+    if t.dim() != 1:
+        _bad(f"{name} must have one dimension, got {tuple(t.shape)}")
+    return _dense(t, t.shape, torch.int32, dev, name), t.shape[0]
+
+
+def _cache_call(op, h, kind, block, slots, entries, q, scale):
+    import torch
+    if kind not in _kinds():
+        _bad(f"kind must be one of {sorted(_kinds())}, got {kind!r}")
+    if h.dim() < 2:
+        _bad(f"h must be [slots, ...], got {tuple(h.shape)}")
+    if not h.is_cuda:
+        _bad("tensors must be in device memory")
+    ty = h.dtype
+    code = _dtypes().get(ty)
+    if code is None:
+        raise TypeError(f"states must be float32 or bfloat16, got {ty}")
+    dev = h.get_device()
+    kc, qt = _kinds()[kind]
+    values = math.prod(h.shape[1:])
+    if values < 1:
+        _bad(f"a state has no values: {tuple(h.shape)}")
+    if block not in (32, 64, 128, 256):
+        _bad(f"block must be 32, 64, 128 or 256, got {block}")
+    sp, n = _cache_index(slots, "slots", dev)
+    ep, m = _cache_index(entries, "entries", dev)
+    if n is not None and m is not None and n != m:
+        _bad(f"slots and entries must be equally many, got {n} and {m}")
+    bytes_, blocks = (values + 1) // 2 if kind == "int4" else values, -(-values // block)
+    if n is None:
+        n = m if m is not None else h.shape[0]
+    if q is None:
+        if m is not None:
+            _bad("entries are places in a cache: q and scale are needed with them")
+        q = torch.empty((n, bytes_), dtype=qt, device=h.device)
+        scale = torch.empty((n, blocks), dtype=torch.float32, device=h.device)
+    if q.dim() != 2:
+        _bad(f"q must be [entries, bytes of a state], got {tuple(q.shape)}")
+    nentries = q.shape[0]
+    if (slots is None and h.shape[0] < n) or (entries is None and nentries < n):
+        _bad(f"{n} rows do not lie in {h.shape[0]} slots and {nentries} entries")
+    o = _op(op)
+    a = o.pack(n, values, code, kc, block, h.shape[0], nentries, sp, ep, _dense(h, h.shape, ty, dev, "h"),
+               _dense(q, (nentries, bytes_), qt, dev, "q"),
+               _dense(scale, (nentries, blocks), torch.float32, dev, "scale"))
+    _call(o, a, dev)
+    return q, scale
+
+
+def mamba3_state_store(h, *, kind="int8", block=64, slots=None, entries=None, q=None, scale=None, stream=None):
+    """Writes states of the pool h [nslots, ...] (fp32 or bf16) into a cache in 8 or 4 bits: state slots[k] (k
+    without slots) into entry entries[k] (k without entries) of q and scale, with one scale for each `block`
+    (32, 64, 128, 256) consecutive values. kind "e4m3" and "int8": q [nentries, values]; "int4": uint8
+    [nentries, (values + 1) // 2], two values a byte; scale [nentries, blocks] fp32. Without q a
+    cache of as many entries as rows is made. slots, entries: int32 [n] on the device; rows with either
+    outside its range are skipped. Returns (q, scale)."""
+    if stream is not None:
+        with _on(stream, h):
+            return mamba3_state_store(h, kind=kind, block=block, slots=slots, entries=entries, q=q, scale=scale)
+    if (q is None) != (scale is None):
+        _bad("q and scale come together")
+    return _cache_call("state_store", h, kind, block, slots, entries, q, scale)
+
+
+def mamba3_state_load(q, scale, *, h, kind="int8", block=64, slots=None, entries=None, stream=None):
+    """Reads cache entries back into the pool h [nslots, ...]: entry entries[k] into state slots[k], as
+    mamba3_state_store wrote them. Other states stay as they were. Returns h."""
+    if stream is not None:
+        with _on(stream, h):
+            return mamba3_state_load(q, scale, h=h, kind=kind, block=block, slots=slots, entries=entries)
+    if q is None or scale is None:
+        _bad("q and scale are needed")
+    if slots is None and entries is None:
+        # (whole caches: as many as there are of both)
+        if q.dim() == 2 and h.dim() and q.shape[0] != h.shape[0]:
+            _bad(f"{q.shape[0]} entries and {h.shape[0]} slots: slots or entries are needed")
+    _cache_call("state_load", h, kind, block, slots, entries, q, scale)
+    return h
