@@ -446,8 +446,8 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *   RMS norm        its rows
  * and for the operators of the gated layer
  *   gated scan      R ceil(D / 128), D / 64 for an odd D; R = S, or at most 2048 / ceil(D / 128) + 2 S segments
- *     backward      the same with R = S ceil(seqlen / 64) (padded) or S + ceil(seqlen / 64) (packed), 32 with fp32;
- *                   and S ceil(D / 64)
+ *     backward      the same with R = S ceil(seqlen / 32) (padded) or S + ceil(seqlen / 32) (packed); and
+ *                   S ceil(D / 64)
  *     step          ceil(batch ceil(D / 4) / 256)
  *   group norm      at most 2048 or G, whatever its rows (fewer than 2^31)
  *   state cache     n ceil(values / 2048)
@@ -694,8 +694,8 @@ mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *args, void *stre
  * weight            [D] fp32; with MAMBA3_GATE_FORGET it may be NULL
  * rate              finite and >= 0 (not read with MAMBA3_GATE_FORGET)
  * h_in, h_out       [S, D] fp32 or NULL (zero, not written)
- * Token rows, cu_seqlens, nseq and tokens outside the sequences are as above. Sigmoids
- * take their arguments at -87 at least. States are fp32, and 1 - a^2 keeps its relative
+ * Token rows, cu_seqlens, nseq and tokens outside the sequences are as above. A sigmoid
+ * below 2^-126 may count as 0. States are fp32, and 1 - a^2 keeps its relative
  * precision where a is next to 1, down to 2^-126 (a u below 2^-63 may count as 0). y overlaps no input; h_out may be h_in
  * exactly. workspace: at least mamba3_gated_scan_workspace_size(args) bytes (0 for
  * many shapes), 256-byte aligned: where few sequences would leave the GPU empty, they run
@@ -731,7 +731,7 @@ mamba3_status mamba3_gated_scan_fwd(const mamba3_gated_scan_args *args, void *st
  * dh_in [S, D] fp32 or NULL. Where u counts as 0 no gradient reaches gate and weight
  * through it. No output overlaps an input or another
  * output. workspace: at least mamba3_gated_scan_bwd_workspace_size(args) bytes, 256-byte
- * aligned: decays, states and gradients between runs of 64 tokens (32 with fp32) and partial
+ * aligned: decays, states and gradients between runs of 32 tokens and partial
  * sums of dweight, 16 bytes a run and channel; all sums have a fixed order
  * (bitwise reproducible). */
 typedef struct {

@@ -30,6 +30,7 @@ struct GateParams {
     float *P;                   // [rows][D] a run's product of decays
     float *H;                   // [rows][D] its last state from zero, then the state entering it
     float *E;                   // [rows][D] its share of the gradient that enters the run before, then the one entering it
+    float *channel;             // [D] the channels' first constants, for the backward's second pass
     float *part;                // [rows][D] partial sums of dweight
 };
 
@@ -85,6 +86,16 @@ __device__ __forceinline__ void store_piece(void *base, int64_t elements, uint32
     *(piece<T, V> *)((char *)((T *)base + elements) + lane_bytes) = o;
 }
 
+// V floats of a lane in LDS
+template <int V> struct Piece32Of { typedef float type __attribute__((ext_vector_type(V))); };
+template <int V> using piece32 = typename Piece32Of<V>::type;
+template <int V> __device__ __forceinline__ piece32<V> to_piece(const float (&v)[V]) {
+    piece32<V> o;
+#pragma unroll
+    for (int e = 0; e < V; e++) o[e] = v[e];
+    return o;
+}
+
 // e^v to an ulp or so for any v: what the product v log2(e) rounds away is put back.
 __device__ __forceinline__ float exp_full(float v) {
     const float hi = v * kLog2e, lo = fmaf(v, kLog2e, -hi) + v * 1.92596299e-8f;
@@ -95,6 +106,9 @@ __device__ __forceinline__ float exp_full(float v) {
 // A channel's constants. Decay: c0 = -rate softplus(w), c1 = c0 log2(e). Forget: c0 = l, c1 = 1 - l.
 // softplus is taken exactly: an error in it is one of every decay of the channel, and adds up over the
 // length of its memory.
+template <int FORM> __device__ __forceinline__ float gate_second(float c0) {
+    return FORM == MAMBA3_GATE_DECAY ? c0 * kLog2e : 1.f - c0;
+}
 template <int FORM>
 __device__ __forceinline__ void gate_channel(const GateParams &p, int c, float &c0, float &c1) {
     if constexpr (FORM == MAMBA3_GATE_DECAY) {
@@ -103,40 +117,35 @@ __device__ __forceinline__ void gate_channel(const GateParams &p, int c, float &
         // below 2^-12 the logarithm of 1 + e is e - e^2 / 2, which log2 of a number next to 1 is not
         const float soft = w > 20.f ? w : e < 0x1p-12f ? fmaf(-0.5f * e, e, e) : l;
         c0 = -p.rate * soft;
-        c1 = c0 * kLog2e;
     } else {
         c0 = p.weight ? p.weight[c] : 0.f;
-        c1 = 1.f - c0;
     }
+    c1 = gate_second<FORM>(c0);
 }
 
-// sigmoid(v) and 1 - sigmoid(v), both to their relative precision
+// sigmoid(v) and 1 - sigmoid(v), both to their relative precision (e^-v leaves fp32's range below -88, where the
+// sigmoid is zero)
 __device__ __forceinline__ void sigmoids(float v, float &s, float &n) {
-    const float e = __builtin_amdgcn_exp2f(fmaxf(v, -87.f) * -kLog2e);
+    const float e = exp_hw(-v);
     s = __builtin_amdgcn_rcpf(1.f + e);
-    n = e * s;
-}
-__device__ __forceinline__ float sigmoid_low(float v) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fmaxf(v, -87.f) * -kLog2e));
+    n = s > 0.f ? e * s : 1.f;
 }
 
-// 1 - e^{2 y} for y <= 0: the series where the difference would cancel (its next term is 2^-26 of it at
-// y = -1/8), the difference elsewhere
+// 1 - e^{2 y} for y <= 0: a polynomial where the difference would cancel (fitted to (1 - e^{2 y}) / y on
+// [-1/8, 0] with -2 at zero, within 2^-28 of it), the difference elsewhere
 __device__ __forceinline__ float one_minus_square(float y, float a) {
-    float s = fmaf(y, 4.f / 315.f, 2.f / 45.f);
-    s = fmaf(y, s, 2.f / 15.f);
-    s = fmaf(y, s, 1.f / 3.f);
-    s = fmaf(y, s, 2.f / 3.f);
-    s = fmaf(y, s, 1.f);
-    s = fmaf(y, s, 1.f);
-    return y > -0.125f ? -2.f * y * s : fmaf(-a, a, 1.f);
+    float s = fmaf(y, -0.24096550f, -0.66400212f);
+    s = fmaf(y, s, -1.33322310f);
+    s = fmaf(y, s, -1.99999857f);
+    s = fmaf(y, s, -2.f);
+    return y > -0.125f ? y * s : fmaf(-a, a, 1.f);
 }
 
 // A token's decay and what its input is taken by
 template <int FORM>
 __device__ __forceinline__ void gate_open(float g, float c0, float c1, float &a, float &u) {
     if constexpr (FORM == MAMBA3_GATE_DECAY) {
-        const float s = sigmoid_low(g);
+        const float s = sigmoid_hw(g);
         a = __builtin_amdgcn_exp2f(c1 * s);
         u = __builtin_amdgcn_sqrtf(one_minus_square(c0 * s, a));
     } else {
@@ -168,7 +177,7 @@ struct GateRaw {
             float u;
             gate_open<FORM>(to_f(g[k][e]), c0[e], c1[e], a[e], u);
             b[e] = u * to_f(x[k][e]);
-            if (IG) b[e] *= sigmoid_low(to_f(i[k][e]));
+            if (IG) b[e] *= sigmoid_hw(to_f(i[k][e]));
         }
     }
 };
@@ -187,7 +196,6 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     __shared__ float join[3][W][V][64];
     const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const GateRow row = gate_row(p, r);
-    if (row.seq < 0 || (!BACK && row.last)) return;     // (nothing takes up a last run's end)
     const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
     const uint32_t at = cc * (uint32_t)sizeof(T);
     float c0[V], c1[V], P[V], H[V], E[V];
@@ -197,6 +205,10 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
         P[e] = 1.f;
         H[e] = E[e] = 0.f;
     }
+    if (BACK && r == 0 && wave == 0 && c < p.dim)
+#pragma unroll
+        for (int e = 0; e < V; e++) p.channel[c + e] = c0[e];
+    if (row.seq < 0 || (!BACK && row.last)) return;     // (nothing takes up a last run's end)
     const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
     const int begin = (int)min((int64_t)row.t0 + (int64_t)wave * share, (int64_t)row.t1);
     const int end = (int)min((int64_t)begin + share, (int64_t)row.t1);
@@ -220,7 +232,7 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
                     float d = to_f(rd[k][e]);
                     if constexpr (ZG) {
                         const float z = to_f(rz[k][e]);
-                        d *= z * sigmoid_low(z);
+                        d *= z * sigmoid_hw(z);
                     }
                     E[e] = fmaf(P[e], d, E[e]);
                 }

@@ -22,7 +22,7 @@ namespace m3 {
 template <typename T, int V, int FORM, bool IG, bool ZG, int W>
 __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
     constexpr int K = sizeof(T) == 2 ? 8 : 4;
-    __shared__ float join[2][2][W][V][64];
+    __shared__ piece32<V> join[2][2][W][64];
     const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const GateRow row = gate_row(p, r);
     if (row.seq < 0) return;
@@ -73,9 +73,9 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
                 P[e] *= a[k][e];
                 H[e] = fmaf(a[k][e], H[e], b[k][e]);
             }
-            join[turn][0][wave][e][lane] = P[e];
-            join[turn][1][wave][e][lane] = H[e];
         }
+        join[turn][0][wave][lane] = to_piece<V>(P);
+        join[turn][1][wave][lane] = to_piece<V>(H);
         __syncthreads();
         float s[V];
 #pragma unroll
@@ -83,8 +83,9 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
             if (w == wave)
 #pragma unroll
                 for (int e = 0; e < V; e++) s[e] = h[e];
+            const piece32<V> A = join[turn][0][w][lane], B = join[turn][1][w][lane];
 #pragma unroll
-            for (int e = 0; e < V; e++) h[e] = fmaf(join[turn][0][w][e][lane], h[e], join[turn][1][w][e][lane]);
+            for (int e = 0; e < V; e++) h[e] = fmaf(A[e], h[e], B[e]);
         }
         auto out = [&](int k) {
             float y[V];
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
                 y[e] = s[e];
                 if constexpr (ZG) {
                     const float v = to_f(z[k][e]);
-                    y[e] *= v * sigmoid_low(v);
+                    y[e] *= v * sigmoid_hw(v);
                 }
             }
             if (c < p.dim) store_piece<T, V>(p.y, (t + wave * K + k) * p.dim, at, y);
@@ -233,10 +234,10 @@ __global__ __launch_bounds__(256) void k_gate_step(GateStepParams p) {
         gate_channel<FORM>(q, e, c0, c1);
         gate_open<FORM>(g[e], c0, c1, a, u);
         float v = u * x[e];
-        if (p.i) v *= sigmoid_low(i[e]);
+        if (p.i) v *= sigmoid_hw(i[e]);
         h[e] = fmaf(a, h[e], v);
         y[e] = h[e];
-        if (p.z) y[e] *= z[e] * sigmoid_low(z[e]);
+        if (p.z) y[e] *= z[e] * sigmoid_hw(z[e]);
     }
     T *yp = (T *)p.y + (int64_t)b * p.dim + c;
     if (n == 4) {
@@ -330,7 +331,7 @@ void scan_go(const GateParams &p, int form, hipStream_t st) {
 }  // namespace
 
 size_t gate_run_bytes(const GateParams &p, bool back) {
-    return (back ? 4 : 2) * al256((int64_t)p.rows * p.dim * 4) +
+    return (back ? 4 : 2) * al256((int64_t)p.rows * p.dim * 4) + (back ? al256((int64_t)p.dim * 4) : 0) +
            (p.cu ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0);
 }
 
@@ -341,8 +342,11 @@ char *gate_runs(GateParams &p, char *ws, bool back) {
     if (back) {
         p.E = (float *)(ws += n);
         p.part = (float *)(ws += n);
+        p.channel = (float *)(ws += n);
+        ws += al256((int64_t)p.dim * 4);
+    } else {
+        ws += n;
     }
-    ws += n;
     if (p.cu) {
         p.table = (const int4 *)ws;
         ws += al256((int64_t)p.rows * 16);

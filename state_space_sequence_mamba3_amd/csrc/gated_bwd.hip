@@ -17,14 +17,16 @@
 
 namespace m3 {
 
-constexpr int kGateBwdWaves = 8;
-template <typename T> constexpr int gate_bwd_tokens() { return sizeof(T) == 2 ? 8 : 4; }     // a wave's
+constexpr int kGateBwdWaves = 8, kGateBwdTokens = 4;      // a workgroup's waves, a wave's tokens
+constexpr int kGateBwdOccupancy = 5;                      // waves a SIMD
 
 template <typename T, int V, int FORM, bool IG, bool ZG>
-__global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p) {
-    constexpr int W = kGateBwdWaves, K = gate_bwd_tokens<T>();
-    __shared__ float join[3][W][V][64];
-    const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_bwd(GateParams p) {
+    constexpr int W = kGateBwdWaves, K = kGateBwdTokens;
+    __shared__ piece32<V> join[3][W][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the last runs first: they were read last and may still lie in the cache
+    const int r = p.rows - 1 - (int)(blockIdx.x / p.tiles);
     const GateRow row = gate_row(p, r);
     const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
     const int64_t o = (int64_t)r * p.dim + cc;
@@ -35,23 +37,24 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p
         return;
     }
     const uint32_t at = cc * (uint32_t)sizeof(T);
-    const int t = row.t0 + wave * K, mine = min(row.t1 - t, K);
+    const int t = row.t0 + wave * K, n = min(row.t1 - t, K);        // the wave's tokens, or none
     GateRaw<T, V, FORM, IG, K> raw;
     piece<T, V> rd[K], rz[ZG ? K : 1];
-    if (mine == K) raw.template fetch<true>(p, t, row.t1, at);
-    else if (mine > 0) raw.template fetch<false>(p, t, row.t1, at);
-    if (mine > 0) fetch_rows<T, V, K>(rd, p.dy, p.dy_row, t, row.t1, at);
-    if constexpr (ZG)
-        if (mine > 0) fetch_rows<T, V, K>(rz, p.z, p.z_row, t, row.t1, at);
+    raw.template fetch<false>(p, t, row.t1, at);
+    fetch_rows<T, V, K>(rd, p.dy, p.dy_row, t, row.t1, at);
+    if constexpr (ZG) fetch_rows<T, V, K>(rz, p.z, p.z_row, t, row.t1, at);
     float c0[V], c1[V], s[V], g[V];
 #pragma unroll
     for (int e = 0; e < V; e++) {
-        gate_channel<FORM>(p, cc + e, c0[e], c1[e]);
+        c0[e] = p.channel[cc + e];
+        c1[e] = gate_second<FORM>(c0[e]);
         s[e] = p.H[o + e];
         g[e] = p.E[o + e];
     }
-    // a, b = u v and r of the wave's tokens
-    float a[K][V], h[K][V], d[K][V], P[V], H[V], E[V];
+    // Of every token what both directions need: a, b = u v (then h_{t-1} less q's second term), r, and the factors of
+    // G in dx, di, q and dgate. They take 64 registers, and computing them again would take a third more
+    // operations.
+    float a[K][V], h[K][V], d[K][V], fx[K][V], fi[K][V], fq[K][V], fh[K][V], fg[K][V], P[V], H[V], E[V];
 #pragma unroll
     for (int e = 0; e < V; e++) {
         P[e] = 1.f;
@@ -59,50 +62,71 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p
     }
 #pragma unroll
     for (int k = 0; k < K; k++)
-        if (k < mine) {
-            raw.open(k, c0, c1, a[k], h[k]);
+        if (k < n)
 #pragma unroll
             for (int e = 0; e < V; e++) {
+                const float x = to_f(raw.x[k][e]);
+                float sg, ng, si = 1.f, ni = 0.f, u;
+                sigmoids(to_f(raw.g[k][e]), sg, ng);
+                if (IG) sigmoids(to_f(raw.i[k][e]), si, ni);
+                const float v = x * si;
+                if constexpr (FORM == MAMBA3_GATE_DECAY) {
+                    const float la = c0[e] * sg;
+                    a[k][e] = __builtin_amdgcn_exp2f(c1[e] * sg);
+                    const float w = one_minus_square(la, a[k][e]), i = w >= 0x1p-126f ? __builtin_amdgcn_rsqf(w) : 0.f;
+                    u = w * i;
+                    fq[k][e] = a[k][e] * la;
+                    fh[k][e] = v * (a[k][e] * i);
+                    fg[k][e] = ng;
+                } else {
+                    u = c1[e] * ng;
+                    a[k][e] = fmaf(c1[e], sg, c0[e]);
+                    fq[k][e] = ng;
+                    fh[k][e] = v;
+                    fg[k][e] = c1[e] * sg;
+                }
+                h[k][e] = u * v;
+                fx[k][e] = u * si;
+                if (IG) fi[k][e] = h[k][e] * ni;
                 d[k][e] = to_f(rd[k][e]);
                 if constexpr (ZG) {
                     const float z = to_f(rz[k][e]);
-                    d[k][e] *= z * sigmoid_low(z);
+                    d[k][e] *= z * sigmoid_hw(z);
                 }
                 P[e] *= a[k][e];
                 H[e] = fmaf(a[k][e], H[e], h[k][e]);
                 E[e] = fmaf(P[e], d[k][e], E[e]);
             }
-        }
-#pragma unroll
-    for (int e = 0; e < V; e++) {
-        join[0][wave][e][lane] = P[e];
-        join[1][wave][e][lane] = H[e];
-        join[2][wave][e][lane] = E[e];
-    }
+    join[0][wave][lane] = to_piece<V>(P);
+    join[1][wave][lane] = to_piece<V>(H);
+    join[2][wave][lane] = to_piece<V>(E);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < W - 1; w++)
-        if (w < wave)
+        if (w < wave) {
+            const piece32<V> A = join[0][w][lane], B = join[1][w][lane];
 #pragma unroll
-            for (int e = 0; e < V; e++) s[e] = fmaf(join[0][w][e][lane], s[e], join[1][w][e][lane]);
+            for (int e = 0; e < V; e++) s[e] = fmaf(A[e], s[e], B[e]);
+        }
 #pragma unroll
     for (int w = W - 1; w > 0; w--)
-        if (w > wave)
+        if (w > wave) {
+            const piece32<V> A = join[0][w][lane], B = join[2][w][lane];
 #pragma unroll
-            for (int e = 0; e < V; e++) g[e] = fmaf(join[0][w][e][lane], g[e], join[2][w][e][lane]);
-    // the states before the tokens; dz from those behind them
+            for (int e = 0; e < V; e++) g[e] = fmaf(A[e], g[e], B[e]);
+        }
 #pragma unroll
     for (int k = 0; k < K; k++)
-        if (k < mine) {
+        if (k < n) {
             float dz[V];
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float was = s[e];
+                const float was = s[e] - fh[k][e];
                 s[e] = fmaf(a[k][e], s[e], h[k][e]);
                 h[k][e] = was;
                 if constexpr (ZG) {
-                    const float z = to_f(rz[k][e]), q = sigmoid_low(z);
-                    dz[e] = to_f(rd[k][e]) * s[e] * (q * fmaf(z, 1.f - q, 1.f));
+                    const float v = to_f(rz[k][e]), q = sigmoid_hw(v);
+                    dz[e] = to_f(rd[k][e]) * s[e] * (q * fmaf(v, 1.f - q, 1.f));
                 }
             }
             if (ZG && p.dz && c < p.dim) store_piece<T, V>(p.dz, (int64_t)(t + k) * p.dim, at, dz);
@@ -112,29 +136,15 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p
     for (int e = 0; e < V; e++) dw[e] = 0.f;
 #pragma unroll
     for (int k = K - 1; k >= 0; k--)
-        if (k < mine) {
+        if (k < n) {
             float dx[V], di[V], dg[V];
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float x = to_f(raw.x[k][e]), G = d[k][e] + g[e];
-                float sg, ng, si = 1.f, ni = 0.f, u, q;
-                sigmoids(to_f(raw.g[k][e]), sg, ng);
-                if (IG) sigmoids(to_f(raw.i[k][e]), si, ni);
-                const float v = x * si;
-                if constexpr (FORM == MAMBA3_GATE_DECAY) {
-                    const float la = c0[e] * sg, w = one_minus_square(la, a[k][e]), i = w >= 0x1p-126f ? __builtin_amdgcn_rsqf(w) : 0.f;
-                    u = w * i;
-                    q = G * (a[k][e] * la) * (h[k][e] - v * (a[k][e] * i));
-                    dg[e] = q * ng;
-                } else {
-                    u = c1[e] * ng;
-                    q = G * (h[k][e] - v) * ng;
-                    dg[e] = q * (c1[e] * sg);
-                }
+                const float G = d[k][e] + g[e], q = G * fq[k][e] * h[k][e];
                 dw[e] += q;
-                const float dv = u * G;
-                dx[e] = dv * si;
-                if (IG) di[e] = dv * v * ni;
+                dx[e] = G * fx[k][e];
+                dg[e] = q * fg[k][e];
+                if (IG) di[e] = G * fi[k][e];
                 g[e] = a[k][e] * G;
             }
             if (c < p.dim) {
@@ -146,14 +156,15 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, 4) void k_gate_bwd(GateParams p
         }
     if (!p.part) return;
     __syncthreads();                                    // (the joins are read)
-#pragma unroll
-    for (int e = 0; e < V; e++) join[0][wave][e][lane] = dw[e];
+    join[0][wave][lane] = to_piece<V>(dw);
     __syncthreads();
     if (wave || c >= p.dim) return;
 #pragma unroll
-    for (int w = 1; w < W; w++)
+    for (int w = 1; w < W; w++) {
+        const piece32<V> other = join[0][w][lane];
 #pragma unroll
-        for (int e = 0; e < V; e++) dw[e] += join[0][w][e][lane];
+        for (int e = 0; e < V; e++) dw[e] += other[e];
+    }
 #pragma unroll
     for (int e = 0; e < V; e++) p.part[o + e] = dw[e];
 }
@@ -193,7 +204,7 @@ GateParams bwd_plan(const mamba3_gated_scan_bwd_args *b) {
     p.dy_row = b->dy_row ? b->dy_row : a->dim;
     p.dx = b->dx; p.dgate = b->dgate; p.di = b->di; p.dz = b->dz;
     p.dh_in = b->dh_in;
-    p.seg_tokens = kGateBwdWaves * (a->dtype == MAMBA3_BF16 ? gate_bwd_tokens<bf16>() : gate_bwd_tokens<float>());
+    p.seg_tokens = kGateBwdWaves * kGateBwdTokens;
     // (at least one run a sequence, also of a sequence without tokens)
     p.nseg = std::max((p.seqlen + p.seg_tokens - 1) / p.seg_tokens, 1);
     const int64_t runs = (p.total + p.seg_tokens - 1) / p.seg_tokens;

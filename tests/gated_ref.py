@@ -9,19 +9,18 @@ import torch
 from tests.layer_bounds import off   # noqa: F401  (the tests' measure)
 from tests.layer_ref import spans
 
-LEAST = -87.0       # sigmoids' least argument
-
 
 def sigmoid(v):
-    """sigmoid(v), 1 - sigmoid(v) and the relative error of both: the exponent's product and constant (2 |v|),
-    exp2, the sum, the reciprocal and a product."""
-    c = v.clamp(min=LEAST)
-    return 1 / (1 + torch.exp(-c)), 1 / (1 + torch.exp(c)), 2 * c.abs() + 6
+    """sigmoid(v), 1 - sigmoid(v) and their relative errors: the exponent's product and constant (2 |v|), exp2,
+    the sum, the reciprocal and a product. One below 2^-126 may count as zero."""
+    s, n = 1 / (1 + torch.exp(-v)), 1 / (1 + torch.exp(v))
+    k, all_ = 2 * v.abs() + 6, torch.full_like(v, 2.0 ** 24)
+    return s, n, torch.where(s < 2.0 ** -125, all_, k), torch.where(n < 2.0 ** -125, all_, k)
 
 
 def silu(z):
     """SiLU, its relative error, its derivative and the error of that."""
-    s, n, k = sigmoid(z)
+    s, n, k, _ = sigmoid(z)
     d, terms = s * (1 + z * n), s * (1 + z.abs() * n)
     # 1 - s by a subtraction: off by s's error and a rounding, both relative to one; then two operations and a product
     ed = s * (1 + z.abs() * n) * k + s * z.abs() * (s * k + 2) + 3 * terms
@@ -29,9 +28,9 @@ def silu(z):
 
 
 def gates(g, w, form, rate):
-    """a, u, 1 / u (0 for u = 0), log a (decay form), sigmoid and its complement, and the relative errors of a and
-    u; `ks` that of the sigmoids, `kl` that of log a."""
-    s, n, ks = sigmoid(g)
+    """a, u, 1 / u (0 for u = 0), log a (decay form), sigmoid and its complement, and the relative errors of a, u, the
+    sigmoid, its complement and log a."""
+    s, n, ks, kn = sigmoid(g)
     if form == "decay":
         soft = torch.logaddexp(w, torch.zeros_like(w))
         la = -rate * soft * s
@@ -49,9 +48,9 @@ def gates(g, w, form, rate):
         u = (1 - l) * n
         a = l + (1 - l) * s
         la, kl = None, None
-        ka, ku = ks + 3, ks + 2
+        ka, ku = ks.minimum(2 * g.abs() + 6) + 3, kn + 2       # (a sum with l, or zero itself)
     inv = torch.where(u > 0, 1 / u.clamp(min=1e-300), torch.zeros_like(u))
-    return a, u, inv, la, s, n, ka, ku, ks, kl
+    return a, u, inv, la, s, n, ka, ku, ks, kn, kl
 
 
 def scan(x, gate, weight, form, rate, i, z, h_in, cu, dy=None, dh_out=None, spoil=None):
@@ -62,9 +61,9 @@ def scan(x, gate, weight, form, rate, i, z, h_in, cu, dy=None, dh_out=None, spoi
     fl = lambda t: t.double().reshape(-1, D)   # noqa: E731
     T = lead[0] * lead[1]
     w = weight.double() if weight is not None else None
-    a, u, inv, la, s, n, ka, ku, ks, kl = gates(fl(gate), w, form, rate)
+    a, u, inv, la, s, n, ka, ku, ks, kc, kl = gates(fl(gate), w, form, rate)
     xd = fl(x)
-    si, ni, ki = sigmoid(fl(i)) if i is not None else (torch.ones_like(xd), None, torch.zeros_like(xd))
+    si, ni, ki, kj = sigmoid(fl(i)) if i is not None else (torch.ones_like(xd), None, torch.zeros_like(xd), None)
     v, kv = si * xd, ki + 1
     b, kb = u * v, ku + kv + 1
     zd = fl(z) if z is not None else None
@@ -110,24 +109,23 @@ def scan(x, gate, weight, form, rate, i, z, h_in, cu, dy=None, dh_out=None, spoi
             V["dx"][t], E["dx"][t] = dv * si[t], dve * si[t] + dvm * si[t] * (ki[t] + 1)
             if i is not None:
                 V["di"][t] = dv * v[t] * ni[t]
-                E["di"][t] = (dve + dvm * (kv[t] + ki[t] + 2)) * (v[t] * ni[t]).abs()
+                E["di"][t] = (dve + dvm * (kv[t] + kj[t] + 4)) * (v[t] * ni[t]).abs()
             if form == "decay":
                 f, kf = (a[t] * la[t]).abs(), ka[t] + kl[t] + 1
                 back = v[t] * a[t] * inv[t]
                 inner, im = hp - back, hpm + back.abs()
                 ie = hpe + back.abs() * (kv[t] + ka[t] + ku[t] + 4) + im
                 Q = G * a[t] * la[t] * inner
-                V["dgate"][t], share, kn = Q * n[t], 1.0, ks[t] + 1
+                V["dgate"][t], mul, kn = Q * n[t], n[t], kc[t] + 1
             else:
-                f, kf = n[t], ks[t]
+                f, kf = n[t], kc[t]
                 inner, im = hp - v[t], hpm + v[t].abs()
                 ie = hpe + v[t].abs() * kv[t] + im
                 Q = G * inner * n[t]
                 sl = (1 - w if w is not None else 1) * s[t]
-                V["dgate"][t], share, kn = Q * sl, sl, ks[t] + 3
+                V["dgate"][t], mul, kn = Q * sl, sl, ks[t] + 3
             Qm = Gm * f * im
             Qe = Ge * f * im + Gm * f * ie + Qm * (kf + 2)
-            mul = n[t] if form == "decay" else share
             E["dgate"][t] = (Qe + Qm * kn) * mul
             dw += Q
             # 16 additions a run's share, runs one by one over 16 threads
