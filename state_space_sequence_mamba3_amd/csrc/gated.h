@@ -22,50 +22,77 @@ struct GateParams {
     int32_t seqlen, total;      // tokens of a padded sequence, tokens of the batch
     int32_t dim, tiles;         // channels, workgroups that cover them
     float rate;
-    // Rows of tokens that a workgroup takes: a sequence each (nseg 1), or its runs of seg_tokens tokens: nseg
-    // a sequence of a padded batch, or those of the table of a packed one.
+    // Rows of tokens that a workgroup takes: a sequence each (nseg 1), or its runs of seg_tokens tokens, nseg
+    // of them in a padded sequence and as many as it needs in a packed one (nseg 0).
     int32_t rows, nseg, seg_tokens;
-    const int4 *table;          // t0, t1, sequence (-1: no run), 1 first | 2 last of its sequence
+    int32_t alone;              // whether a row joins the runs around it itself, without k_gate_chain
+    const int4 *table;          // the rows of a packed batch of more than 64 sequences, t0, t1, sequence (-1: no run)
     const int32_t *seq_row;     // [nseq + 1] a sequence's first row in the table
     float *P;                   // [rows][D] a run's product of decays
-    float *H;                   // [rows][D] its last state from zero, then the state entering it
-    float *E;                   // [rows][D] its share of the gradient that enters the run before, then the one entering it
+    float *H;                   // [rows][D] its last state from zero (after k_gate_chain: the state entering it)
+    float *E;                   // [rows][D] its share of the gradient that enters the run before (after: the one entering it)
     float *channel;             // [D] the channels' first constants, for the backward's second pass
     float *part;                // [rows][D] partial sums of dweight
 };
 
+// A row: its tokens, its sequence (-1: no row), its place among the sequence's rows and how many those are
 struct GateRow {
-    int t0, t1, seq;
-    bool first, last;
+    int t0, t1, seq, k, n;
 };
 
-// Row r, in scalar registers
+// Row r, in scalar registers. Every lane of the wave takes part.
 __device__ __forceinline__ GateRow gate_row(const GateParams &p, int r) {
     GateRow o;
-    o.first = o.last = true;
-    if (p.table) {
+    if (!p.cu) {
+        o.seq = r / p.nseg;
+        o.k = r % p.nseg;
+        o.n = p.nseg;
+        const int a = o.seq * p.seqlen;
+        o.t0 = a + (int)min((int64_t)o.k * p.seg_tokens, (int64_t)p.seqlen);
+        o.t1 = (int)min((int64_t)o.t0 + p.seg_tokens, (int64_t)a + p.seqlen);
+    } else if (p.nseg == 1) {
+        o.seq = r;
+        o.k = 0;
+        o.n = 1;
+        packed_bounds(p.cu, r, p.total, o.t0, o.t1);
+    } else if (p.table) {
         const int4 e = p.table[r];
         o.t0 = e.x;
         o.t1 = e.y;
         o.seq = e.z;
-        o.first = e.w & 1;
-        o.last = e.w & 2;
-    } else if (p.cu) {
-        o.seq = r;
-        packed_bounds(p.cu, r, p.total, o.t0, o.t1);
+        const int s = max(e.z, 0), first = p.seq_row[s];
+        o.k = r - first;
+        o.n = p.seq_row[s + 1] - first;
     } else {
-        const int k = r % p.nseg, a = r / p.nseg * p.seqlen;
-        o.seq = r / p.nseg;
-        o.t0 = a + (int)min((int64_t)k * p.seg_tokens, (int64_t)p.seqlen);
-        o.t1 = (int)min((int64_t)o.t0 + p.seg_tokens, (int64_t)a + p.seqlen);
-        o.first = k == 0;
-        o.last = k == p.nseg - 1;
+        // up to 64 sequences: every lane counts the rows of one
+        const int s = threadIdx.x & 63;
+        int a = 0, b = 0, n = 0;
+        if (s < p.nseq) {
+            packed_bounds(p.cu, s, p.total, a, b);
+            n = max(1, (b - a + p.seg_tokens - 1) / p.seg_tokens);
+        }
+        int before = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(before, d, 64);
+            if (s >= d) before += v;
+        }
+        before -= n;
+        const uint64_t mine = __ballot(r >= before && r < before + n);
+        const int from = mine ? __builtin_ctzll(mine) : 0;
+        o.seq = mine ? from : -1;
+        o.k = r - __builtin_amdgcn_readlane(before, from);
+        // (decreasing entries may count more rows than there are)
+        o.n = min(__builtin_amdgcn_readlane(n, from), p.rows - (r - o.k));
+        o.t1 = __builtin_amdgcn_readlane(b, from);
+        o.t0 = (int)min((int64_t)__builtin_amdgcn_readlane(a, from) + (int64_t)o.k * p.seg_tokens, (int64_t)o.t1);
+        o.t1 = (int)min((int64_t)o.t0 + p.seg_tokens, (int64_t)o.t1);
     }
     o.t0 = __builtin_amdgcn_readfirstlane(o.t0);
     o.t1 = __builtin_amdgcn_readfirstlane(o.t1);
     o.seq = __builtin_amdgcn_readfirstlane(o.seq);
-    o.first = __builtin_amdgcn_readfirstlane(o.first);
-    o.last = __builtin_amdgcn_readfirstlane(o.last);
+    o.k = __builtin_amdgcn_readfirstlane(o.k);
+    o.n = __builtin_amdgcn_readfirstlane(o.n);
     return o;
 }
 
@@ -208,7 +235,7 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     if (BACK && r == 0 && wave == 0 && c < p.dim)
 #pragma unroll
         for (int e = 0; e < V; e++) p.channel[c + e] = c0[e];
-    if (row.seq < 0 || (!BACK && row.last)) return;     // (nothing takes up a last run's end)
+    if (row.seq < 0 || (!BACK && row.k == row.n - 1)) return;     // (nothing takes up a last run's end)
     const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
     const int begin = (int)min((int64_t)row.t0 + (int64_t)wave * share, (int64_t)row.t1);
     const int end = (int)min((int64_t)begin + share, (int64_t)row.t1);
@@ -262,6 +289,42 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
         p.P[o + e] = P[e];
         p.H[o + e] = H[e];
         if (BACK) p.E[o + e] = E[e];
+    }
+}
+
+// The waves' shares of `count` rows on one side of row r (those from row `first` on, `step` apart, in the order in
+// which they are joined), left in LDS: join[0] the products, join[1] the sums. The caller's barrier, then join_runs.
+template <int V, int W>
+__device__ __forceinline__ void share_runs(const GateParams &p, const float *X, int first, int step, int count, int cc, int wave,
+                                           piece32<V> (*join)[W][64]) {
+    const int lane = threadIdx.x & 63, share = (count + W - 1) / W;
+    const int begin = min(wave * share, count), end = min(begin + share, count);
+    float A[V], B[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        A[e] = 1.f;
+        B[e] = 0.f;
+    }
+    for (int k = begin; k < end; k++) {
+        const int64_t q = (int64_t)(first + k * step) * p.dim + cc;
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            const float a = p.P[q + e];
+            A[e] *= a;
+            B[e] = fmaf(a, B[e], X[q + e]);
+        }
+    }
+    join[0][wave][lane] = to_piece<V>(A);
+    join[1][wave][lane] = to_piece<V>(B);
+}
+template <int V, int W>
+__device__ __forceinline__ void join_runs(float (&v)[V], const piece32<V> (*join)[W][64]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+        const piece32<V> A = join[0][w][lane], B = join[1][w][lane];
+#pragma unroll
+        for (int e = 0; e < V; e++) v[e] = fmaf(A[e], v[e], B[e]);
     }
 }
 

@@ -42,9 +42,14 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
 #pragma unroll
     for (int e = 0; e < V; e++) {
         gate_channel<FORM>(p, cc + e, c0[e], c1[e]);
-        h[e] = p.H ? p.H[(int64_t)r * p.dim + cc + e] : p.h_in ? p.h_in[(int64_t)row.seq * p.dim + cc + e] : 0.f;
+        h[e] = p.H && !p.alone ? p.H[(int64_t)r * p.dim + cc + e] : p.h_in ? p.h_in[(int64_t)row.seq * p.dim + cc + e] : 0.f;
     }
     int turn = 0;
+    if (p.alone && row.k > 0) {                          // (the same for the workgroup)
+        share_runs<V, W>(p, p.H, r - row.k, 1, row.k, cc, wave, join[1]);
+        __syncthreads();
+        join_runs<V, W>(h, join[1]);                     // (join[1] is written again behind the next barrier)
+    }
     for (int64_t t = row.t0; t < row.t1; t += W * K, turn ^= 1) {
         const int mine = (int)min((int64_t)row.t1 - (t + wave * K), (int64_t)K);     // the wave's tokens, or none
         float a[K][V], b[K][V], P[V], H[V];
@@ -109,7 +114,7 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
                 if (k < mine) out(k);
         }
     }
-    if (row.last && p.h_out && wave == 0 && c < p.dim)
+    if (row.k == row.n - 1 && p.h_out && wave == 0 && c < p.dim)
 #pragma unroll
         for (int e = 0; e < V; e++) p.h_out[(int64_t)row.seq * p.dim + c + e] = h[e];
 }
@@ -123,7 +128,27 @@ __global__ __launch_bounds__(64 * kChainWaves) void k_gate_chain(GateParams p) {
     const int blocks = (p.dim + 63) / 64, s = blockIdx.x / blocks;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = blockIdx.x % blocks * 64 + lane, cc = min(c, p.dim - 1);
-    const int r0 = p.table ? p.seq_row[s] : s * p.nseg, r1 = p.table ? p.seq_row[s + 1] : r0 + p.nseg;
+    int r0 = s * p.nseg, r1 = r0 + p.nseg;
+    if (p.table) {
+        r0 = p.seq_row[s];
+        r1 = p.seq_row[s + 1];
+    } else if (p.cu) {                                   // up to 64 sequences: every lane counts the rows of one
+        int n = 0;
+        if (lane < p.nseq) {
+            int a, b;
+            packed_bounds(p.cu, lane, p.total, a, b);
+            n = max(1, (b - a + p.seg_tokens - 1) / p.seg_tokens);
+        }
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
+        }
+        // (decreasing entries may count more rows than there are)
+        r1 = min(__builtin_amdgcn_readlane(upto, s), p.rows);
+        r0 = min(r1, __builtin_amdgcn_readlane(upto, s) - __builtin_amdgcn_readlane(n, s));
+    }
     const int share = (r1 - r0 + kChainWaves - 1) / kChainWaves;
     // (the gradient's runs are counted from the last)
     const bool back = blockIdx.y;
@@ -285,6 +310,7 @@ GateParams gate_params(const mamba3_gated_scan_args *a) {
 namespace {
 
 size_t al256(int64_t v) { return (size_t)((v + 255) / 256 * 256); }
+constexpr int kGateAloneFwd = 64;
 
 // Whole sequences, or segments of a multiple of 128 tokens where those leave less than a workgroup of 16 waves
 // a CU; segments fill two.
@@ -296,12 +322,10 @@ bool fwd_plan(GateParams &p) {
     const int64_t len = ((tokens + cut - 1) / cut + 127) / 128 * 128;
     if (len >= tokens) return false;
     p.seg_tokens = (int32_t)len;
-    if (p.cu) {
-        p.rows = (int32_t)(p.nseq + (tokens + len - 1) / len);
-    } else {
-        p.nseg = (int32_t)((tokens + len - 1) / len);
-        p.rows = p.nseq * p.nseg;
-    }
+    p.nseg = (int32_t)((tokens + len - 1) / len);
+    p.rows = p.cu ? p.nseq + p.nseg : p.nseq * p.nseg;
+    p.alone = p.nseg <= kGateAloneFwd;                  // (of a packed sequence, at most)
+    if (p.cu) p.nseg = 0;
     return true;
 }
 
@@ -330,9 +354,12 @@ void scan_go(const GateParams &p, int form, hipStream_t st) {
 
 }  // namespace
 
+// Rows of packed sequences that no wave can count by itself
+static bool gate_has_table(const GateParams &p) { return p.cu && p.nseg != 1 && p.nseq > 64; }
+
 size_t gate_run_bytes(const GateParams &p, bool back) {
     return (back ? 4 : 2) * al256((int64_t)p.rows * p.dim * 4) + (back ? al256((int64_t)p.dim * 4) : 0) +
-           (p.cu ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0);
+           (gate_has_table(p) ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0);
 }
 
 char *gate_runs(GateParams &p, char *ws, bool back) {
@@ -347,7 +374,7 @@ char *gate_runs(GateParams &p, char *ws, bool back) {
     } else {
         ws += n;
     }
-    if (p.cu) {
+    if (gate_has_table(p)) {
         p.table = (const int4 *)ws;
         ws += al256((int64_t)p.rows * 16);
         p.seq_row = (const int32_t *)ws;
@@ -373,6 +400,7 @@ void launch_gate_table(const GateParams &p, hipStream_t st) {
 static int64_t chain_blocks(const GateParams &p) { return (int64_t)p.nseq * ((p.dim + 63) / 64); }
 
 void launch_gate_chain(const GateParams &p, hipStream_t st) {
+    if (p.alone) return;
     hipLaunchKernelGGL(k_gate_chain, dim3((uint32_t)chain_blocks(p), p.E ? 2 : 1), dim3(64 * kChainWaves), 0, st, p);
 }
 

@@ -19,11 +19,12 @@ namespace m3 {
 
 constexpr int kGateBwdWaves = 8, kGateBwdTokens = 4;      // a workgroup's waves, a wave's tokens
 constexpr int kGateBwdOccupancy = 5;                      // waves a SIMD
+constexpr int kGateAlone = 32;
 
 template <typename T, int V, int FORM, bool IG, bool ZG>
 __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_bwd(GateParams p) {
     constexpr int W = kGateBwdWaves, K = kGateBwdTokens;
-    __shared__ piece32<V> join[3][W][64];
+    __shared__ piece32<V> join[3][W][64], around[4][W][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the last runs first: they were read last and may still lie in the cache
     const int r = p.rows - 1 - (int)(blockIdx.x / p.tiles);
@@ -31,9 +32,16 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
     const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
     const int64_t o = (int64_t)r * p.dim + cc;
     if (row.seq < 0 || row.t0 >= row.t1) {              // no tokens: nothing but a row of partial sums
-        if (p.part && wave == 0 && c < p.dim)
+        if (wave == 0 && c < p.dim) {
 #pragma unroll
-            for (int e = 0; e < V; e++) p.part[o + e] = 0.f;
+            for (int e = 0; e < V; e++) {
+                if (p.part) p.part[o + e] = 0.f;
+                if (p.alone && p.dh_in && row.seq >= 0) {
+                    const int64_t h = (int64_t)row.seq * p.dim + c + e;
+                    p.dh_in[h] = p.dh_out ? p.dh_out[h] : 0.f;
+                }
+            }
+        }
         return;
     }
     const uint32_t at = cc * (uint32_t)sizeof(T);
@@ -48,8 +56,13 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
     for (int e = 0; e < V; e++) {
         c0[e] = p.channel[cc + e];
         c1[e] = gate_second<FORM>(c0[e]);
-        s[e] = p.H[o + e];
-        g[e] = p.E[o + e];
+        const int64_t h = (int64_t)row.seq * p.dim + cc + e;
+        s[e] = !p.alone ? p.H[o + e] : p.h_in ? p.h_in[h] : 0.f;
+        g[e] = !p.alone ? p.E[o + e] : p.dh_out ? p.dh_out[h] : 0.f;
+    }
+    if (p.alone) {
+        share_runs<V, W>(p, p.H, r - row.k, 1, row.k, cc, wave, around);
+        share_runs<V, W>(p, p.E, r - row.k + row.n - 1, -1, row.n - 1 - row.k, cc, wave, around + 2);
     }
     // Of every token what both directions need: a, b = u v (then h_{t-1} less q's second term), r, and the factors of
     // G in dx, di, q and dgate. They take 64 registers, and computing them again would take a third more
@@ -101,6 +114,13 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
     join[1][wave][lane] = to_piece<V>(H);
     join[2][wave][lane] = to_piece<V>(E);
     __syncthreads();
+    if (p.alone) {
+        join_runs<V, W>(s, around);
+        join_runs<V, W>(g, around + 2);
+        if (row.k == 0 && p.dh_in && wave == 0 && c < p.dim)
+#pragma unroll
+            for (int e = 0; e < V; e++) p.dh_in[(int64_t)row.seq * p.dim + c + e] = fmaf(p.P[o + e], g[e], p.E[o + e]);
+    }
 #pragma unroll
     for (int w = 0; w < W - 1; w++)
         if (w < wave) {
@@ -207,9 +227,11 @@ GateParams bwd_plan(const mamba3_gated_scan_bwd_args *b) {
     p.seg_tokens = kGateBwdWaves * kGateBwdTokens;
     // (at least one run a sequence, also of a sequence without tokens)
     p.nseg = std::max((p.seqlen + p.seg_tokens - 1) / p.seg_tokens, 1);
-    const int64_t runs = (p.total + p.seg_tokens - 1) / p.seg_tokens;
+    const int64_t runs = ((int64_t)p.total + p.seg_tokens - 1) / p.seg_tokens;
+    p.alone = (p.cu ? runs : p.nseg) <= kGateAlone;
     const int64_t rows = p.cu ? p.nseq + runs : (int64_t)p.nseq * p.nseg;
     p.rows = (int32_t)std::min<int64_t>(rows, INT32_MAX);      // (more are refused for their workgroups)
+    if (p.cu) p.nseg = 0;
     return p;
 }
 
