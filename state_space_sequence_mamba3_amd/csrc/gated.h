@@ -7,6 +7,8 @@
 // order: (P2 P1, P2 H1 + H2) and (P1 P2, E1 + P1 E2).
 #pragma once
 
+#include <type_traits>
+
 #include "layer.h"
 
 namespace m3 {
@@ -183,6 +185,24 @@ __device__ __forceinline__ void gate_open(float g, float c0, float c1, float &a,
     }
 }
 
+// The rows of tokens t .. t + K - 1. WHOLE: all of them are before `end`, and a row's address is the one before it
+// plus their distance; else those from `end` on are the one before it.
+template <typename T, int V, int K, bool WHOLE = false>
+__device__ __forceinline__ void fetch_rows(piece<T, V> (&o)[K], const void *base, int64_t row, int t, int end, uint32_t lane) {
+    if constexpr (WHOLE) {
+        const char *q = (const char *)((const T *)base + (int64_t)t * row);
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            asm("" : "+s"(q));                           // (not K distances carried in scalar registers)
+            o[k] = *(const piece<T, V> *)(q + lane);
+            q += row * (int64_t)sizeof(T);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; k++) o[k] = load_piece<T, V>(base, (int64_t)min(t + k, end - 1) * row, lane);
+    }
+}
+
 template <typename T, int V, int FORM, bool IG, int K>
 struct GateRaw {
     piece<T, V> x[K], g[K], i[IG ? K : 1];
@@ -190,13 +210,9 @@ struct GateRaw {
     // tokens t .. t + K - 1, those from `end` on as the one before it
     template <bool WHOLE>
     __device__ __forceinline__ void fetch(const GateParams &p, int t, int end, uint32_t lane) {
-#pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int64_t at = WHOLE ? t + k : min(t + k, end - 1);
-            g[k] = load_piece<T, V>(p.gate, at * p.gate_row, lane);
-            x[k] = load_piece<T, V>(p.x, at * p.x_row, lane);
-            if (IG) i[k] = load_piece<T, V>(p.i, at * p.i_row, lane);
-        }
+        fetch_rows<T, V, K, WHOLE>(g, p.gate, p.gate_row, t, end, lane);
+        fetch_rows<T, V, K, WHOLE>(x, p.x, p.x_row, t, end, lane);
+        if constexpr (IG) fetch_rows<T, V, K, WHOLE>(i, p.i, p.i_row, t, end, lane);
     }
     __device__ __forceinline__ void open(int k, const float (&c0)[V], const float (&c1)[V], float (&a)[V], float (&b)[V]) const {
 #pragma unroll
@@ -209,12 +225,6 @@ struct GateRaw {
     }
 };
 
-template <typename T, int V, int K>
-__device__ __forceinline__ void fetch_rows(piece<T, V> (&o)[K], const void *base, int64_t row, int t, int end, uint32_t lane) {
-#pragma unroll
-    for (int k = 0; k < K; k++) o[k] = load_piece<T, V>(base, (int64_t)min(t + k, end - 1) * row, lane);
-}
-
 // The runs' P and H, and with BACK their E. A workgroup has a run of 64 V channels, W waves with
 // consecutive shares of its tokens.
 template <typename T, int V, int FORM, bool IG, bool ZG, bool BACK, int W>
@@ -224,7 +234,7 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     const int r = blockIdx.x / p.tiles, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const GateRow row = gate_row(p, r);
     const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
-    const uint32_t at = cc * (uint32_t)sizeof(T);
+    uint32_t at = cc * (uint32_t)sizeof(T);
     float c0[V], c1[V], P[V], H[V], E[V];
 #pragma unroll
     for (int e = 0; e < V; e++) {
@@ -239,16 +249,19 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
     const int begin = (int)min((int64_t)row.t0 + (int64_t)wave * share, (int64_t)row.t1);
     const int end = (int)min((int64_t)begin + share, (int64_t)row.t1);
-    for (int t = begin; t < end; t += K) {
+    // (a lane's offset that is unknown to the compiler, which would otherwise carry 64-bit addresses of every array)
+    auto tokens = [&](auto whole, int t) __attribute__((always_inline)) {
+        constexpr bool WHOLE = decltype(whole)::value;
         GateRaw<T, V, FORM, IG, K> raw;
         piece<T, V> rd[BACK ? K : 1], rz[BACK && ZG ? K : 1];
-        if (t + K <= end) raw.template fetch<true>(p, t, end, at);
-        else raw.template fetch<false>(p, t, end, at);
-        if constexpr (BACK) fetch_rows<T, V, K>(rd, p.dy, p.dy_row, t, end, at);
-        if constexpr (BACK && ZG) fetch_rows<T, V, K>(rz, p.z, p.z_row, t, end, at);
+        asm("" : "+v"(at));
+        raw.template fetch<WHOLE>(p, t, end, at);
+        if constexpr (BACK) fetch_rows<T, V, K, WHOLE>(rd, p.dy, p.dy_row, t, end, at);
+        if constexpr (BACK && ZG) fetch_rows<T, V, K, WHOLE>(rz, p.z, p.z_row, t, end, at);
+        __builtin_amdgcn_sched_barrier(0);               // all loads before the first token
 #pragma unroll
         for (int k = 0; k < K; k++) {
-            if (t + k >= end) break;
+            if (!WHOLE && t + k >= end) break;
             float a[V], b[V];
             raw.open(k, c0, c1, a, b);
 #pragma unroll
@@ -265,7 +278,10 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
                 }
             }
         }
-    }
+    };
+    int t = begin;
+    for (; t + K <= end; t += K) tokens(std::integral_constant<bool, true>(), t);
+    if (t < end) tokens(std::integral_constant<bool, false>(), t);
 #pragma unroll
     for (int e = 0; e < V; e++) {
         join[0][wave][e][lane] = P[e];

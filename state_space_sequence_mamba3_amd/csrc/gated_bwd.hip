@@ -18,7 +18,7 @@
 namespace m3 {
 
 constexpr int kGateBwdWaves = 8, kGateBwdTokens = 4;      // a workgroup's waves, a wave's tokens
-constexpr int kGateBwdOccupancy = 5;                      // waves a SIMD
+constexpr int kGateBwdOccupancy = 4;                      // waves a SIMD: two workgroups a CU
 constexpr int kGateAlone = 32;
 
 template <typename T, int V, int FORM, bool IG, bool ZG>
