@@ -445,8 +445,8 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *     step          batch ceil(D / c)
  *   RMS norm        its rows
  * and for the operators of the gated layer
- *   gated scan      R ceil(D / 128), D / 64 for an odd D; R = S, or at most 2048 / ceil(D / 128) + 2 S segments
- *     backward      the same with R = S ceil(seqlen / 32) (padded) or S + ceil(seqlen / 32) (packed); and
+ *   gated scan      S ceil(D / 128), D / 64 for an odd D, or fewer than 2^23 where few sequences are cut
+ *     backward      the same with S ceil(seqlen / 32) (padded) or S + ceil(seqlen / 32) (packed) for S; and
  *                   S ceil(D / 64)
  *     step          ceil(batch ceil(D / 4) / 256)
  *   group norm      at most 2048 or G, whatever its rows (fewer than 2^31)
@@ -699,7 +699,8 @@ mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *args, void *stre
  * precision where a is next to 1, down to 2^-126 (a u below 2^-63 may count as 0). y overlaps no input; h_out may be h_in
  * exactly. workspace: at least mamba3_gated_scan_workspace_size(args) bytes (0 for
  * many shapes), 256-byte aligned: where few sequences would leave the GPU empty, they run
- * as segments and it holds their decays, states and token ranges. */
+ * as segments and it holds what those hand on, at most 9 bytes for a channel of 32 tokens
+ * or of a sequence. Results do not depend on timing (bitwise reproducible). */
 typedef enum { MAMBA3_GATE_DECAY = 0, MAMBA3_GATE_FORGET = 1 } mamba3_gate_form;
 
 typedef struct {

@@ -35,6 +35,9 @@ struct GateParams {
     float *E;                   // [rows][D] its share of the gradient that enters the run before (after: the one entering it)
     float *channel;             // [D] the channels' first constants, for the backward's second pass
     float *part;                // [rows][D] partial sums of dweight
+    // One pass over the inputs (gated_pass.hip): what the runs publish
+    uint64_t *runs, *checkpoints;
+    uint32_t *counter;
 };
 
 // A row: its tokens, its sequence (-1: no row), its place among the sequence's rows and how many those are
@@ -370,5 +373,9 @@ size_t gate_run_bytes(const GateParams &p, bool back);
 char *gate_runs(GateParams &p, char *ws, bool back);
 void launch_gate_table(const GateParams &p, hipStream_t st);
 void launch_gate_chain(const GateParams &p, hipStream_t st);
+// The scan in one pass over runs of gate_pass_tokens tokens, and its workspace
+int gate_pass_tokens(bool f32);
+size_t gate_pass_bytes(const GateParams &p);
+void launch_gate_pass(GateParams p, int32_t dtype, int form, char *ws, hipStream_t st);
 
 }  // namespace m3

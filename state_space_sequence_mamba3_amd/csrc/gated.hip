@@ -9,9 +9,9 @@
 // tokens' a and b = u v stay in registers while the waves exchange their runs' (P, H) through LDS with one
 // barrier a round, every wave joins all of them in order (so that all carry the same state) and goes
 // over its tokens again from the state that enters them: every input is read once. The next round's loads are
-// in flight meanwhile. Where whole sequences are too few workgroups to fill the GPU they run as
-// segments: k_gate_part reads the inputs for the segments' (P, H), k_gate_chain joins those, and the walk starts
-// from the states that enter the segments.
+// in flight meanwhile. Where whole sequences are too few workgroups to fill the GPU they run in one pass
+// over short runs (gated_pass.hip), or as segments: k_gate_part reads the inputs for the segments' (P, H), a row
+// joins those before it or k_gate_chain does for all, and the walk starts from the states that enter the segments.
 #include <algorithm>
 
 #include "gated.h"
@@ -311,27 +311,36 @@ namespace {
 
 size_t al256(int64_t v) { return (size_t)((v + 255) / 256 * 256); }
 constexpr int kGateAlone = 64;
+constexpr int64_t kGatePass = 1 << 22;
 
-// Whole sequences, or segments where those leave less than a workgroup a CU and are longer than two rounds of 16
-// waves. Segments of a multiple of 32 tokens (a round of four waves) that give 1024 workgroups, as long as a
-// row can join those before it by itself (up to 64); else of a multiple of 128 (a round of 16 waves), which leave
-// fewer to join. One sequence, whole, in segments of 128 and by this rule: 512 tokens of 1024 channels 29.7,
-// 19.3, 17.3 us, 2048 of 4096 101, 39.6, 32.3, 16384 of 256 (tens of times more whole) 25.6 in 128s, 29.8 in 32s.
-bool fwd_plan(GateParams &p) {
+// Whole sequences, or runs where those leave less than a workgroup a CU and are longer than two rounds of 16 waves.
+// PASS (gated_pass.hip) reads every input once and needs two launches, but a sequence's runs wait for each other:
+// about 2 us for every 1024 tokens, which 1024 channels of bf16 hide. SEGMENTS takes the others: segments of a
+// multiple of 32 tokens (a round of four waves) that give 1024 workgroups, as long as a row can join those before it
+// by itself (up to 64); else of a multiple of 128 (a round of 16 waves), which leave fewer to join.
+// In us, decay form with i, bf16: one sequence of 512 tokens of 1024 channels whole 29.7, segments of 128 19.3, by
+// this rule 17.3; 2048 of 4096 101, 39.6, 32.3, pass 29.3; 1024 of 4096 segments 21.6, pass 19.6; 4096 of 4096 58.5,
+// pass 46.9; 32768 of 1024 115, pass 83; 65536 of 256 68, pass 126.
+enum Plan { WHOLE, SEGMENTS, PASS };
+Plan fwd_plan(GateParams &p, bool f32) {
     const int64_t whole = (int64_t)p.nseq * p.tiles, tokens = p.cu ? p.total : p.seqlen;
-    if (p.nseq == 0 || whole >= (p.cu ? 512 : 256) || tokens <= 256) return false;
+    if (p.nseq == 0 || whole >= (p.cu ? 512 : 256) || tokens <= 256) return WHOLE;
     const int64_t cut = std::max<int64_t>(1024 / (p.cu ? p.tiles : whole), 2);
     auto length = [&](int64_t unit) { return ((tokens + cut - 1) / cut + unit - 1) / unit * unit; };
     auto count = [&](int64_t len) { return (tokens + len - 1) / len; };
     int64_t len = length(32);
     if (count(len) > kGateAlone) len = length(128);
-    if (len >= tokens) return false;
+    const int64_t run = gate_pass_tokens(f32);
+    const bool pass = (int64_t)p.total * p.dim >= kGatePass && (p.cu ? 1 : (int64_t)p.nseq) * p.dim >= 1024 &&
+                      count(run) * whole < (1 << 23);
+    if (pass) len = run;
+    if (len >= tokens) return WHOLE;
     p.seg_tokens = (int32_t)len;
     p.nseg = (int32_t)count(len);
     p.rows = p.cu ? p.nseq + p.nseg : p.nseq * p.nseg;
     p.alone = p.nseg <= kGateAlone;                     // (of a packed sequence, at most)
     if (p.cu) p.nseg = 0;
-    return true;
+    return pass ? PASS : SEGMENTS;
 }
 
 template <typename T>
@@ -366,9 +375,12 @@ void scan_go(const GateParams &p, int form, hipStream_t st) {
 // Rows of packed sequences that no wave can count by itself
 static bool gate_has_table(const GateParams &p) { return p.cu && p.nseg != 1 && p.nseq > 64; }
 
+static size_t gate_table_bytes(const GateParams &p) {
+    return gate_has_table(p) ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0;
+}
 size_t gate_run_bytes(const GateParams &p, bool back) {
     return (back ? 4 : 2) * al256((int64_t)p.rows * p.dim * 4) + (back ? al256((int64_t)p.dim * 4) : 0) +
-           (gate_has_table(p) ? al256((int64_t)p.rows * 16) + al256(((int64_t)p.nseq + 1) * 4) : 0);
+           gate_table_bytes(p);
 }
 
 char *gate_runs(GateParams &p, char *ws, bool back) {
@@ -385,9 +397,8 @@ char *gate_runs(GateParams &p, char *ws, bool back) {
     }
     if (gate_has_table(p)) {
         p.table = (const int4 *)ws;
-        ws += al256((int64_t)p.rows * 16);
-        p.seq_row = (const int32_t *)ws;
-        ws += al256(((int64_t)p.nseq + 1) * 4);
+        p.seq_row = (const int32_t *)(ws + al256((int64_t)p.rows * 16));
+        ws += gate_table_bytes(p);
     }
     return ws;
 }
@@ -416,7 +427,12 @@ void launch_gate_chain(const GateParams &p, hipStream_t st) {
 mamba3_status launch_gated_scan(const mamba3_gated_scan_args *a, hipStream_t st) {
     GateParams p = gate_params(a);
     const bool f32 = a->dtype == MAMBA3_F32;
-    if (fwd_plan(p)) {
+    const Plan plan = fwd_plan(p, f32);
+    if (plan == PASS) {                                 // (1024 channels are at most 64 sequences: no table)
+        launch_gate_pass(p, a->dtype, a->form, (char *)a->workspace, st);
+        return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
+    }
+    if (plan == SEGMENTS) {
         gate_runs(p, (char *)a->workspace, false);
         launch_gate_table(p, st);
         if (f32) part_go<float>(p, a->form, st);
@@ -430,13 +446,16 @@ mamba3_status launch_gated_scan(const mamba3_gated_scan_args *a, hipStream_t st)
 
 size_t gated_scan_workspace_bytes(const mamba3_gated_scan_args *a) {
     GateParams p = gate_params(a);
-    return fwd_plan(p) ? gate_run_bytes(p, false) : 0;
+    const Plan plan = fwd_plan(p, a->dtype == MAMBA3_F32);
+    return plan == PASS ? gate_pass_bytes(p) : plan == SEGMENTS ? gate_run_bytes(p, false) : 0;
 }
 
 int64_t gated_scan_workgroups(const mamba3_gated_scan_args *a) {
     GateParams p = gate_params(a);
-    const bool segments = fwd_plan(p);
-    return std::max((int64_t)p.rows * p.tiles, segments ? chain_blocks(p) : 0);
+    const Plan plan = fwd_plan(p, a->dtype == MAMBA3_F32);
+    const int64_t n = (int64_t)p.rows * p.tiles;
+    if (plan == PASS) return std::max(n, (int64_t)(gate_pass_bytes(p) + 4095) / 4096);
+    return std::max(n, plan == SEGMENTS ? chain_blocks(p) : 0);
 }
 
 int64_t gated_step_workgroups(const mamba3_gated_step_args *a) {

@@ -248,3 +248,63 @@ def test_empty():
         c["h_in"] = back["dh_out"] = None
         got, g = call(c), call(c, back)
         assert not got["h_out"].any() and not g["dh_in"].any()
+
+
+# few sequences of many channels, long enough for one pass over short runs: several groups of eight runs, sequences that
+# end inside, at the end and one token behind a run, more tokens behind the last
+PASS = [  # batch, seqlen, dim, cu
+    (1, 1300, 8192, None), (1, 2048, 4096, None), (1, 2049, 2050, None), (2, 1100, 2600, None), (3, 700, 4094, None),
+    (1, 1200, 8193, None), (1, 2600, 2048, [0, 0, 128, 257, 1400, 1400, 2600]), (1, 2100, 2050, [3, 700, 2095]),
+    (8, 1100, 520, None),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", PASS)
+@pytest.mark.parametrize("form", ["decay", "forget"])
+def test_one_pass(case, form, dtype):
+    b, L, D, cu = case
+    note(f"gated scan in one pass b {b} L {L} D {D} packed {cu is not None} {form} {dtype}")
+    full = form == "decay"
+    c, _ = inputs(b, L, D, cu, form, dtype, full, not full, True, memory=2.0)
+    ref = R.scan(**c)
+    room = torch.full((b * L * D + 2,), 7.0, dtype=dtype, device=device())
+    got = call(c, y=room[1:-1].view(b, L, D))
+    lo, hi = (cu[0], cu[-1]) if cu else (0, L)
+    assert R.off(got["y"][:, lo:hi], tuple(t[:, lo:hi] for t in ref["y"])) <= 1
+    assert R.off(got["h_out"], ref["h_out"]) <= 1
+    assert bool((got["y"][:, :lo] == 7).all()) and bool((got["y"][:, hi:] == 7).all())
+    assert float(room[0]) == 7.0 and float(room[-1]) == 7.0
+
+
+def test_one_pass_repeats():
+    """The same bits however the runs are timed: alone, beside other work on another stream, with h_out in h_in's
+    place; a workspace of any content."""
+    c, _ = inputs(1, 3000, 4096, None, "decay", BF16, True, True, True)
+    one = call(c)
+    a = {k: up(c[k]) for k in ("x", "gate", "weight", "i", "z", "h_in")}
+    torch.cuda.synchronize()
+    side, busy = torch.cuda.Stream(), torch.randn(2048, 2048, device=device())
+    for k in range(12):
+        with torch.cuda.stream(side):
+            for _ in range(k):
+                busy = torch.mm(busy, busy) * 1e-3
+        ws = torch.full((4 << 20,), (0, 255, 77)[k % 3], dtype=torch.uint8, device=device())
+        h = a["h_in"].clone()
+        y, out = m3.mamba3_gated_scan_fwd(a["x"], a["gate"], a["weight"], i=a["i"], z=a["z"], h_in=h, h_out=h, workspace=ws)
+        assert torch.equal(y, one["y"]) and torch.equal(out, one["h_out"]), k
+
+
+def test_one_pass_not_finite():
+    """Infinities and NaNs, of any bits, stay in their channels and reach the tokens behind them."""
+    c, _ = inputs(1, 2100, 4096, None, "forget", F32, False, False, False)
+    clean = call(c)
+    bad = torch.tensor([-1], dtype=torch.int32).view(F32)        # a NaN of ones
+    c["x"][0, 5, 7], c["gate"][0, 600, 9], c["x"][0, 1000, 11] = bad[0], bad[0], float("inf")
+    got = call(c)
+    hit = [7, 9, 11]
+    keep = torch.ones(4096, dtype=torch.bool)
+    keep[hit] = False
+    assert torch.equal(got["y"][..., keep], clean["y"][..., keep]) and torch.equal(got["h_out"][:, keep], clean["h_out"][:, keep])
+    for ch, t in zip(hit, (5, 600, 1000)):
+        assert torch.equal(got["y"][0, :t, ch], clean["y"][0, :t, ch]) and not got["y"][0, t:, ch].isfinite().any()

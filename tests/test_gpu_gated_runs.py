@@ -136,6 +136,9 @@ def calls(g, dtype):
                 return [t[:, :end] if t.dim() == 3 else t for t in r.values()]
 
             out[f"scan {form} {tag}"], out[f"scan_bwd {form} {tag}"] = (v, fwd), (v, bwd)
+    v = {k: rand(g, 1, 1100, 4096, dtype=dtype) for k in ("x", "gate", "i")}
+    v.update(w=rand(g, 4096) - 4, h=rand(g, 1, 4096))
+    out["scan one pass"] = (v, lambda v: m3.mamba3_gated_scan_fwd(v["x"], v["gate"], v["w"], i=v["i"], h_in=v["h"]))
     for size in (32, 300, 1500):
         v = {k: rand(g, 37, 2 * size, dtype=dtype) for k in ("x", "z", "dy")}
         v.update(w=rand(g, 2 * size), b=rand(g, 2 * size))
@@ -165,7 +168,7 @@ def calls(g, dtype):
 
 
 NAMES = [f"{k} {f} {t}" for k in ("scan", "scan_bwd") for f in ("decay", "forget") for t in ("padded", "packed")] + \
-    [f"{k} {s}" for k in ("norm", "norm_bwd") for s in (32, 300, 1500)] + ["step", "cache"]
+    [f"{k} {s}" for k in ("norm", "norm_bwd") for s in (32, 300, 1500)] + ["step", "cache", "scan one pass"]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
