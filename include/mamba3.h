@@ -450,7 +450,7 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *                   S ceil(D / 64)
  *     step          ceil(batch ceil(D / 4) / 256)
  *   group norm      at most 2048 or G, whatever its rows (fewer than 2^31)
- *   state cache     n ceil(values / 2048)
+ *   state cache     n ceil(values / 2048), 4096 with bf16
  */
 
 /* 1: the convolution, the selective scan and the RMS norm; 2: the gated scan, the

@@ -173,7 +173,7 @@ def apart(lib, a, want):  # noqa: F811
 def test_documented_workgroups(lib, dtype):  # noqa: F811
     """The header's formulas decide, at the last size taken and the first refused."""
     run = 32
-    for dim in (1, 2, 63, 64, 129, 1000, 4096):
+    for dim in (1, 2, 63, 64, 129, 1000, 4096):      # (whole sequences of two tokens: nothing is cut)
         tiles = ceil(dim, 64 if dim % 2 else 128)
         for b in (MOST // tiles, MOST // tiles + 1):
             if b * 2 <= 1 << 30:
@@ -192,8 +192,9 @@ def test_documented_workgroups(lib, dtype):  # noqa: F811
                 apart(lib, step(batch=b, dim=dim, dtype=dtype), OK if ceil(b * quads, 256) <= MOST else EINVAL)
     apart(lib, norm(rows=(1 << 31) - 1, groups=100, dim=400, dtype=dtype), OK)
     for values in (1, 2048, 2049, 1 << 20):
-        for n in (MOST // ceil(values, 2048), MOST // ceil(values, 2048) + 1):
-            apart(lib, cache(n=n, values=values, nslots=9, nentries=9, dtype=dtype), OK if n * ceil(values, 2048) <= MOST else EINVAL)
+        per = ceil(values, 4096 if dtype == BF16 else 2048)
+        for n in (MOST // per, MOST // per + 1):
+            apart(lib, cache(n=n, values=values, nslots=9, nentries=9, dtype=dtype), OK if n * per <= MOST else EINVAL)
 
 
 def test_binding_refuses():
