@@ -8,7 +8,12 @@
 // and their outputs, and a workgroup walks rows of the same columns with the next row's loads in flight, so that
 // weights and, backwards, the sums over rows stay in registers too. A lane holds 8 consecutive values. Groups of up
 // to 512 values take as many lanes as hold them (a power of two), several groups a wave, and sum inside
-// the vector unit; longer ones take 4 or 16 waves.
+// the vector unit; longer ones take 2, 4, 8 or 16 waves.
+//
+// 32768 x 2048, 16 groups, gated, bf16: 80 us, 5.0 TB/s (a large copy runs at 4.88); its backward 138 us, 4.85 TB/s;
+// 128 x 4096 in groups of 512 3.6 us. 2^25 values in groups of 64 37 us and 73 backward, of 512 38 and 74, of 600
+// (two waves, 59 % of their lanes) 56 and 97, of 1024 43 and 78, of 4096 44 and 101, of 8192 51 and 110; of 4 (half a
+// lane each) 82 and 137, of 100 54 and 107, of 513 75 and 123, where pieces cross groups and rows start at any value.
 //
 // The mean is taken off before squares are summed, and what its rounding left (the mean of the differences)
 // once more, in the same sums as the squares: a group far from zero keeps its precision.
@@ -73,10 +78,77 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int lanes, float (*red
 __device__ __forceinline__ float silu_of(float v, float s) { return v * s; }
 __device__ __forceinline__ float dsilu_of(float v, float s) { return s * fmaf(v, 1.f - s, 1.f); }
 
-// A lane's place: the group, its first value of the row, how many of the group's values lie from the lane's first on
+// A lane's place: its group's first column, its own first value in the group, the group's values (0: no group)
 struct GnLane {
     int col, c, n;
 };
+
+// A lane's 8 values of a row; those behind its group's end are not zero unless VEC. Rows of 8 values or more are
+// read in full pieces at any element: one that crosses the row's end is taken from its last 8 values and shifted.
+template <typename T, bool VEC>
+__device__ __forceinline__ typename Raw8<T>::type gn_raw(const T *row, const GnLane &l, int dim) {
+    if constexpr (VEC) {
+        return raw8<T, true>(row + l.col, l.c, l.n);
+    } else {
+        typename Raw8<T>::type v;
+        if (dim < kNV) return raw8<T, false>(row + l.col, l.c, l.n);
+        const int from = min(l.col + l.c, dim - kNV), over = l.col + l.c - from;
+        v = *(const typename Loose8<T>::type *)(row + from);
+        if (over) {                                      // by 4, 2 and 1 values
+            if constexpr (sizeof(T) == 2) {
+                typedef uint32_t words __attribute__((ext_vector_type(4)));
+                words u = __builtin_bit_cast(words, v);
+                if (over & 4) u = words{u[2], u[3], 0, 0};
+                if (over & 2) u = words{u[1], u[2], u[3], 0};
+                if (over & 1)
+                    u = words{u[0] >> 16 | u[1] << 16, u[1] >> 16 | u[2] << 16, u[2] >> 16 | u[3] << 16, u[3] >> 16};
+                v = __builtin_bit_cast(typename Raw8<T>::type, u);
+            } else {
+                typedef typename Raw8<T>::type values;
+                if (over & 4) v = values{v[4], v[5], v[6], v[7], 0, 0, 0, 0};
+                if (over & 2) v = values{v[2], v[3], v[4], v[5], v[6], v[7], 0, 0};
+                if (over & 1) v = values{v[1], v[2], v[3], v[4], v[5], v[6], v[7], 0};
+            }
+        }
+        return v;
+    }
+}
+// fp32 rows of dim values (weights and partial sums)
+template <bool VEC>
+__device__ __forceinline__ void gn_floats(float (&o)[kNV], const float *row, const GnLane &l, int dim) {
+    const auto v = gn_raw<float, VEC>(row, l, dim);
+#pragma unroll
+    for (int e = 0; e < kNV; e++) o[e] = l.c + e < l.n ? v[e] : 0.f;
+}
+// The lane's values that its group has: 8, or the last one to seven as pieces of 4, 2 and 1.
+template <typename T, bool VEC>
+__device__ __forceinline__ void gn_store(T *row, const GnLane &l, const float (&o)[kNV]) {
+    if constexpr (VEC) {
+        store8<T, true>(row + l.col, l.c, l.n, o);
+    } else {
+        T *to = row + l.col + l.c;
+        const int n = l.n - l.c;
+        if (n >= kNV) {
+            store8<T, false>(to, 0, kNV, o);
+        } else if (n > 0) {
+            typedef T four __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+            typedef T two __attribute__((ext_vector_type(2), aligned(sizeof(T))));
+            four low = {from_f<T>(o[0]), from_f<T>(o[1]), from_f<T>(o[2]), from_f<T>(o[3])};
+            const four high = {from_f<T>(o[4]), from_f<T>(o[5]), from_f<T>(o[6]), from_f<T>(o[7])};
+            if (n & 4) {
+                *(four *)to = low;
+                to += 4;
+                low = high;
+            }
+            if (n & 2) {
+                *(two *)to = two{low[0], low[1]};
+                to += 2;
+                low[0] = low[2];
+            }
+            if (n & 1) *to = low[0];
+        }
+    }
+}
 template <int WPG>
 __device__ __forceinline__ GnLane gn_lane(const GnParams &p, int tile) {
     GnLane l;
@@ -140,8 +212,8 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn(GnParams p) {
     int64_t row = (int64_t)(blockIdx.x / p.tiles) * RPW + (WPG == 1 ? threadIdx.x >> 6 : 0);
     typename Raw8<T>::type rx, rz;
     auto fetch = [&](int64_t i) {
-        rx = raw8<T, VEC>((const T *)p.x + i * p.x_row + l.col, l.c, l.n);
-        if (gn_gated(ACT)) rz = raw8<T, VEC>((const T *)p.z + i * p.z_row + l.col, l.c, l.n);
+        rx = gn_raw<T, VEC>((const T *)p.x + i * p.x_row, l, p.dim);
+        if (gn_gated(ACT)) rz = gn_raw<T, VEC>((const T *)p.z + i * p.z_row, l, p.dim);
     };
     if (row < p.rows) fetch(row);
     float w[kNV], b[kNV];
@@ -150,18 +222,19 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn(GnParams p) {
         w[e] = 1.f;
         b[e] = 0.f;
     }
-    if (p.w) load8<float, VEC>(w, p.w + l.col, l.c, l.n);
-    if (p.b) load8<float, VEC>(b, p.b + l.col, l.c, l.n);
+    if (p.w) gn_floats<VEC>(w, p.w, l, p.dim);
+    if (p.b) gn_floats<VEC>(b, p.b, l, p.dim);
     int turn = 0;
     for (; row < p.rows; row += step) {
         float t[kNV], f[kNV], r;
 #pragma unroll
         for (int e = 0; e < kNV; e++) {
-            t[e] = to_f(rx[e]);
+            const bool in = VEC || l.c + e < l.n;        // (VEC: zeros behind the group's end)
+            t[e] = in ? to_f(rx[e]) : 0.f;
             if constexpr (gn_gated(ACT)) {
                 const float z = to_f(rz[e]);
                 f[e] = z * sigmoid_hw(z);
-                if (ACT == MAMBA3_GN_PREGATE) t[e] *= f[e];
+                if (ACT == MAMBA3_GN_PREGATE) t[e] = in ? t[e] * f[e] : 0.f;
             }
         }
         if (row + step < p.rows) fetch(row + step);
@@ -173,12 +246,14 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn(GnParams p) {
             if (ACT == MAMBA3_GN_GATE) v *= f[e];
             t[e] = v;
         }
-        store8<T, VEC>((T *)p.y + row * p.dim + l.col, l.c, l.n, t);
+        gn_store<T, VEC>((T *)p.y + row * p.dim, l, t);
     }
 }
 
+// Four waves a SIMD, where that spills little: rows of odd lengths (groups of 100 bf16 values 133 -> 107 us), not fp32
+// in whole pieces (groups of 2048 140 -> 149).
 template <typename T, int ACT, int WPG, bool VEC>
-__global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p) {
+__global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG, sizeof(T) == 2 || !VEC ? 4 : 1) void k_gn_bwd(GnParams p) {
     __shared__ float red[2][2][16];
     __shared__ float4 join[WPG == 1 ? 4 * 256 : 1];
     constexpr int RPW = WPG == 1 ? 4 : 1;
@@ -187,9 +262,9 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p
     int64_t row = rb * RPW + (WPG == 1 ? threadIdx.x >> 6 : 0);
     typename Raw8<T>::type rx, rz, rd;
     auto fetch = [&](int64_t i) {
-        rx = raw8<T, VEC>((const T *)p.x + i * p.x_row + l.col, l.c, l.n);
-        rd = raw8<T, VEC>((const T *)p.dy + i * p.dy_row + l.col, l.c, l.n);
-        if (gn_gated(ACT)) rz = raw8<T, VEC>((const T *)p.z + i * p.z_row + l.col, l.c, l.n);
+        rx = gn_raw<T, VEC>((const T *)p.x + i * p.x_row, l, p.dim);
+        rd = gn_raw<T, VEC>((const T *)p.dy + i * p.dy_row, l, p.dim);
+        if (gn_gated(ACT)) rz = gn_raw<T, VEC>((const T *)p.z + i * p.z_row, l, p.dim);
     };
     if (row < p.rows) fetch(row);
     float w[kNV], b[kNV], dw[kNV], db[kNV];
@@ -198,19 +273,20 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p
         w[e] = 1.f;
         b[e] = dw[e] = db[e] = 0.f;
     }
-    if (p.w) load8<float, VEC>(w, p.w + l.col, l.c, l.n);
-    if (p.b) load8<float, VEC>(b, p.b + l.col, l.c, l.n);
+    if (p.w) gn_floats<VEC>(w, p.w, l, p.dim);
+    if (p.b) gn_floats<VEC>(b, p.b, l, p.dim);
     int turn = 0;
     for (; row < p.rows; row += step) {
         float t[kNV], d[kNV], r;
         typename Raw8<T>::type cx = rx, cz = rz;
 #pragma unroll
         for (int e = 0; e < kNV; e++) {
-            t[e] = to_f(rx[e]);
-            d[e] = to_f(rd[e]);
+            const bool in = VEC || l.c + e < l.n;        // (VEC: zeros behind the group's end)
+            t[e] = in ? to_f(rx[e]) : 0.f;
+            d[e] = in ? to_f(rd[e]) : 0.f;
             if (ACT == MAMBA3_GN_PREGATE) {
                 const float z = to_f(rz[e]);
-                t[e] *= z * sigmoid_hw(z);
+                t[e] = in ? t[e] * (z * sigmoid_hw(z)) : 0.f;
             }
         }
         if (row + step < p.rows) fetch(row + step);
@@ -226,7 +302,7 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p
             if (ACT == MAMBA3_GN_GATE) {
                 const float z = to_f(cz[e]), q = sigmoid_hw(z);
                 dz[e] = d[e] * fmaf(t[e], w[e], b[e]) * dsilu_of(z, q);
-                d[e] *= silu_of(z, q);
+                d[e] = VEC || l.c + e < l.n ? d[e] * silu_of(z, q) : 0.f;
             }
             db[e] += d[e];
             dw[e] = fmaf(d[e], t[e], dw[e]);
@@ -245,8 +321,8 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p
                 d[e] *= silu_of(z, q);
             }
         }
-        store8<T, VEC>((T *)p.dx + row * p.dim + l.col, l.c, l.n, d);
-        if (gn_gated(ACT) && p.dz) store8<T, VEC>((T *)p.dz + row * p.dim + l.col, l.c, l.n, dz);
+        gn_store<T, VEC>((T *)p.dx + row * p.dim, l, d);
+        if (gn_gated(ACT) && p.dz) gn_store<T, VEC>((T *)p.dz + row * p.dim, l, dz);
     }
     if (!p.part) return;
     // one row of partial sums a workgroup: with several rows at once, those of its waves in order
@@ -268,8 +344,8 @@ __global__ __launch_bounds__(WPG == 1 ? 256 : 64 * WPG) void k_gn_bwd(GnParams p
             db[4] += b1.x; db[5] += b1.y; db[6] += b1.z; db[7] += b1.w;
         }
     }
-    store8<float, VEC>(p.part + rb * 2 * p.dim + l.col, l.c, l.n, dw);
-    store8<float, VEC>(p.part + (rb * 2 + 1) * p.dim + l.col, l.c, l.n, db);
+    gn_store<float, VEC>(p.part + rb * 2 * p.dim, l, dw);
+    gn_store<float, VEC>(p.part + (rb * 2 + 1) * p.dim, l, db);
 }
 
 // dweight (blockIdx.y 0) and dbias from `n` rows of partial sums: 16 columns a workgroup, 16 threads over the rows of
@@ -296,7 +372,7 @@ __global__ __launch_bounds__(256) void k_gn_reduce(const float *part, int n, int
 namespace {
 
 bool wide(const void *q, int64_t row, int64_t es) { return ((uintptr_t)q & 15u) == 0 && row * es % 16 == 0; }
-int gn_waves(int size) { return size <= 512 ? 1 : size <= 2048 ? 4 : 16; }
+int gn_waves(int size) { return size <= 512 ? 1 : size <= 1024 ? 2 : size <= 2048 ? 4 : size <= 4096 ? 8 : 16; }
 
 GnParams gn_params(const mamba3_groupnorm_args *a) {
     GnParams p{};
@@ -317,7 +393,7 @@ GnParams gn_params(const mamba3_groupnorm_args *a) {
 // twice that for the forward
 int64_t gn_row_blocks(const GnParams &p, bool back) {
     const int w = gn_waves(p.size);
-    const int64_t most = std::max<int64_t>((back ? 1 : 2) * (w == 16 ? 256 : 1024) / p.tiles, 1);
+    const int64_t most = std::max<int64_t>((back ? 4096 : 8192) / (w == 1 ? 4 : w) / p.tiles, 1);
     return std::min<int64_t>(w == 1 ? (p.rows + 3) / 4 : p.rows, most);
 }
 
@@ -336,7 +412,9 @@ template <typename T, int ACT>
 void gn_act(const GnParams &p, bool vec, bool back, hipStream_t st) {
     const int w = gn_waves(p.size);
     if (w == 1) gn_launch<T, ACT, 1>(p, vec, back, st);
+    else if (w == 2) gn_launch<T, ACT, 2>(p, vec, back, st);
     else if (w == 4) gn_launch<T, ACT, 4>(p, vec, back, st);
+    else if (w == 8) gn_launch<T, ACT, 8>(p, vec, back, st);
     else gn_launch<T, ACT, 16>(p, vec, back, st);
 }
 template <typename T>
