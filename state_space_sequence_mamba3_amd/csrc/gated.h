@@ -31,7 +31,8 @@ struct GateParams {
     const int4 *table;          // the rows of a packed batch of more than 64 sequences, t0, t1, sequence (-1: no run)
     const int32_t *seq_row;     // [nseq + 1] a sequence's first row in the table
     float *P;                   // [rows][D] a run's product of decays
-    float *H;                   // [rows][D] its last state from zero (after k_gate_chain: the state entering it)
+    float *H;                   // [rows][D] its last state from zero (after k_gate_chain: the state entering it); `alone`,
+                                // forwards, h_in in the place of a sequence's last run
     float *E;                   // [rows][D] its share of the gradient that enters the run before (after: the one entering it)
     float *channel;             // [D] the channels' first constants, for the backward's second pass
     float *part;                // [rows][D] partial sums of dweight
@@ -248,7 +249,13 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     if (BACK && r == 0 && wave == 0 && c < p.dim)
 #pragma unroll
         for (int e = 0; e < V; e++) p.channel[c + e] = c0[e];
-    if (row.seq < 0 || (!BACK && row.k == row.n - 1)) return;     // (nothing takes up a last run's end)
+    if (row.seq < 0) return;
+    if (!BACK && row.k == row.n - 1) {          // nothing takes up a last run's end: its place is the sequence's first state's
+        if (p.alone && p.h_in && wave == 0 && c < p.dim)
+#pragma unroll
+            for (int e = 0; e < V; e++) p.H[(int64_t)r * p.dim + c + e] = p.h_in[(int64_t)row.seq * p.dim + c + e];
+        return;
+    }
     const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
     const int begin = (int)min((int64_t)row.t0 + (int64_t)wave * share, (int64_t)row.t1);
     const int end = (int)min((int64_t)begin + share, (int64_t)row.t1);

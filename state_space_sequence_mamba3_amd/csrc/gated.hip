@@ -42,7 +42,9 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
 #pragma unroll
     for (int e = 0; e < V; e++) {
         gate_channel<FORM>(p, cc + e, c0[e], c1[e]);
-        h[e] = p.H && !p.alone ? p.H[(int64_t)r * p.dim + cc + e] : p.h_in ? p.h_in[(int64_t)row.seq * p.dim + cc + e] : 0.f;
+        // (of rows that join those before them, from k_gate_part: in place the sequence's last row overwrites h_in)
+        const int from = p.alone ? r - row.k + row.n - 1 : r;
+        h[e] = !p.h_in && (p.alone || !p.H) ? 0.f : p.H ? p.H[(int64_t)from * p.dim + cc + e] : p.h_in[(int64_t)row.seq * p.dim + cc + e];
     }
     int turn = 0;
     if (p.alone && row.k > 0) {                          // (the same for the workgroup)

@@ -239,6 +239,25 @@ def test_reproducible_and_in_place():
     assert out.data_ptr() == h.data_ptr() and torch.equal(h, one["h_out"]) and torch.equal(y, one["y"])
 
 
+# segments whose rows join those before them, a chain over them, one pass, whole; padded and packed
+IN_PLACE = [(4, 700, 96, None), (2, 4000, 128, None), (1, 2048, 1024, None), (1, 3000, 512, [0, 1000, 1000, 2900]),
+            (1, 30000, 130, None), (1, 1300, 8192, None), (300, 40, 16, None)]
+
+
+@pytest.mark.parametrize("case", IN_PLACE)
+def test_state_in_place(case):
+    """h_out in h_in's place has what it has elsewhere, whichever of a sequence's rows ends first."""
+    c, _ = inputs(*case, "forget", BF16, True, False, True)
+    a = {k: up(c[k]) for k in ("x", "gate", "weight", "i")}
+    a.update(form="forget", cu_seqlens=up(torch.tensor(c["cu"], dtype=torch.int32)) if c["cu"] else None)
+    h = up(c["h_in"])
+    y, out = m3.mamba3_gated_scan_fwd(**a, h_in=h.clone())
+    for _ in range(10):
+        again = h.clone()
+        got, _ = m3.mamba3_gated_scan_fwd(**a, h_in=again, h_out=again)
+        assert torch.equal(again, out) and torch.equal(got, y)
+
+
 def test_empty():
     for b, L, cu in ((0, 9, None), (2, 0, None), (1, 0, [0, 0, 0])):
         c, back = inputs(b, L, 10, cu, "decay", F32, True, True, True)
