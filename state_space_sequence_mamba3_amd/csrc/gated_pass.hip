@@ -3,13 +3,19 @@
 // A workgroup has a run of W K tokens of 64 V channels with all of its operands in registers. It publishes the
 // run's product of decays and its state from zero, takes the state that enters it from the runs before it, and
 // writes its outputs: every input is read once, where segments in two passes (gated.hip) read all but z twice.
-// The state that enters run k is joined from the last checkpoint, the state behind every 16th run, and the
-// published pairs of the up to 15 runs after that, in order: a fixed sequence of operations, whatever the timing.
+// The state that enters run k is joined from the last checkpoint, the state behind every 8th run, and the
+// published pairs of the up to 7 runs after that, in order: a fixed sequence of operations, whatever the timing.
+//
+// 32768 tokens of 2048 channels, bf16, with i, from a state (110 us at the rate of a large copy): 124 us, in
+// two passes 167; six packed sequences of 16384 tokens of 4096 140, 218 in two passes; 2048 of 4096 29.3, 32.3. 16 waves
+// and checkpoints every 8 runs: every 4 132 us, every 16 127; 8 waves (runs of 64 tokens, 16 to a checkpoint) 138,
+// 4 waves 230. What is above the copy's time is the chain of checkpoints, one memory latency for 1024 tokens.
 //
 // Waiting. Runs are handed out by a counter, in an order in which every run a workgroup waits for has a smaller
 // number: its workgroup has started, holds its CU until it ends, and waits only for still smaller ones, so the
 // smallest unfinished one never waits and every wait ends. (A wait gives up after kPassPolls polls all the
-// same and goes on with NaN, so that a workspace that another call overwrites cannot hang the GPU.) A
+// same and goes on with NaN, and a number behind the last ends, so that a workspace that another call overwrites neither
+// hangs the GPU nor leads out of the arrays.) A
 // published word is one 64-bit store that carries its own validity: a kernel fills the words with ones before,
 // which no published word is. So no fence is needed, and nothing but these words crosses workgroups.
 #include <algorithm>
@@ -51,6 +57,7 @@ __global__ __launch_bounds__(64 * kPassWaves, 8) void k_gate_pass(GateParams p) 
     if (threadIdx.x == 0) number = atomicAdd(p.counter, 1u) + 1u;       // (from ones on)
     __syncthreads();
     const uint32_t mine = __builtin_amdgcn_readfirstlane(number);
+    if (mine >= gridDim.x) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // a padded batch's sequences side by side, a packed batch's rows in their order
     const int q = mine / p.tiles, tile = mine % p.tiles;
@@ -129,7 +136,7 @@ __global__ __launch_bounds__(64 * kPassWaves, 8) void k_gate_pass(GateParams p) 
             before[0][j][lane] = to_piece<V>(A);
             before[1][j][lane] = to_piece<V>(B);
         }
-        // (a sequence's checkpoints lie from its first row / 16 + its number on: no two share one)
+        // (a sequence's checkpoints lie from its first row / 8 + its number on: no two share one)
         const int64_t first = (r - row.k) / kPassGroup + row.seq;
         if (wave == W - 1 && group > 0) {
             float A[V], B[V];
