@@ -11,15 +11,27 @@
 // enters it from behind, and k_gate_bwd reads the inputs again, joins its waves' shares of the run in both
 // directions, and goes over its tokens forwards for the states and backwards for the gradients. Nothing walks a
 // sequence, so that one long sequence fills the GPU as a batch does, for a second read of the inputs.
+//
+// 8 x 2048 tokens of 4096 channels, decay, i, bf16: 322 us (k_gate_part 124, k_gate_chain 13, k_gate_bwd 187,
+// k_gate_reduce 5), 1.55 GB, 4.8 TB/s: HBM-bound with the inputs read twice; read once the floor would be 193. Both
+// directions need the whole sequence before its first token's gradient is known. Runs walked by k_gate_bwd with the next
+// tokens' loads in flight spilled; six waves a SIMD, sequences grouped for the last-level cache, and a first pass of one
+// wave a run or with a prefetch were all slower.
 #include <algorithm>
 
 #include "gated.h"
 
 namespace m3 {
 
-constexpr int kGateBwdWaves = 8, kGateBwdTokens = 4;      // a workgroup's waves, a wave's tokens
+// A workgroup's waves, a wave's tokens. 8 x 2048 tokens of 4096 channels: 325 us; 4 and 4 344, 16 and 4 442, 8 and 8
+// (two waves a SIMD) 424; 1024 of 4096: 31.1, 34.7, 35.0, 33.3.
+constexpr int kGateBwdWaves = 8, kGateBwdTokens = 4;
 constexpr int kGateBwdOccupancy = 4;                      // waves a SIMD: two workgroups a CU
-constexpr int kGateAlone = 32;
+// Rows join those around them by themselves, without k_gate_chain and its launch, where a sequence has at most 32 and
+// all are at most 2048 workgroups: 512 tokens of 1024 channels 22.4 us (with the chain 24.7), 4 x 512 of 2048 30.5 (32.9),
+// 1024 of 4096 31.1 (32.4). Reading the others' runs in every row costs more with more of them: 8 x 1024 of 4096, 8192
+// workgroups, 182 (172); 8 x 2048 of 4096 399 (325), 2048 of 4096 56.6 (50.1).
+constexpr int kGateAlone = 32, kGateAloneGroups = 2048;
 
 template <typename T, int V, int FORM, bool IG, bool ZG>
 __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_bwd(GateParams p) {
@@ -228,8 +240,8 @@ GateParams bwd_plan(const mamba3_gated_scan_bwd_args *b) {
     // (at least one run a sequence, also of a sequence without tokens)
     p.nseg = std::max((p.seqlen + p.seg_tokens - 1) / p.seg_tokens, 1);
     const int64_t runs = ((int64_t)p.total + p.seg_tokens - 1) / p.seg_tokens;
-    p.alone = (p.cu ? runs : p.nseg) <= kGateAlone;
     const int64_t rows = p.cu ? p.nseq + runs : (int64_t)p.nseq * p.nseg;
+    p.alone = (p.cu ? runs : p.nseg) <= kGateAlone && rows * p.tiles <= kGateAloneGroups;
     p.rows = (int32_t)std::min<int64_t>(rows, INT32_MAX);      // (more are refused for their workgroups)
     if (p.cu) p.nseg = 0;
     return p;
