@@ -1,7 +1,7 @@
 // Shared parts of the gated linear recurrence's forward and backward kernels.
 //
-// A wave holds 64 V consecutive channels, V a lane (2 where the channel count is even, so that a token's
-// load is 4 bytes of bf16 or 8 of fp32 a lane, else 1), and K consecutive tokens of each in registers.
+// A wave holds 64 V consecutive channels, V a lane (2 but where gate_two says 1, so that a token's load is 4 bytes of
+// bf16 or 8 of fp32 a lane, at any element), and K consecutive tokens of each in registers.
 // The recurrence over a run of tokens is h -> P h + H with P the product of their decays and H their
 // state from zero; the gradient's, from its end to its start, is g -> P g + E with the same P. Runs are joined in
 // order: (P2 P1, P2 H1 + H2) and (P1 P2, E1 + P1 E2).
@@ -101,6 +101,12 @@ __device__ __forceinline__ GateRow gate_row(const GateParams &p, int r) {
     o.n = __builtin_amdgcn_readfirstlane(o.n);
     return o;
 }
+
+// Whether a lane takes two channels. With an odd count the last lane takes the last two, one of which is the lane's before
+// too: both compute and write the same, and no other workgroup does (which might read a state that this one replaced).
+// 8 x 2048 tokens of 4095 channels, decay, i, bf16, with one channel a lane 164 us and backward 445; with two 144 and 397
+// (4096 channels 117 and 325).
+__host__ __device__ inline bool gate_two(int dim) { return dim % 2 == 0 || (dim > 1 && dim % 128 != 1); }
 
 // V elements of a token, at any element: global memory takes loads and stores of 4 and 8 bytes there.
 template <typename T, int V> struct PieceOf { typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T)))); };
@@ -248,12 +254,12 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
     }
     if (BACK && r == 0 && wave == 0 && c < p.dim)
 #pragma unroll
-        for (int e = 0; e < V; e++) p.channel[c + e] = c0[e];
+        for (int e = 0; e < V; e++) p.channel[cc + e] = c0[e];
     if (row.seq < 0) return;
     if (!BACK && row.k == row.n - 1) {          // nothing takes up a last run's end: its place is the sequence's first state's
         if (p.alone && p.h_in && wave == 0 && c < p.dim)
 #pragma unroll
-            for (int e = 0; e < V; e++) p.H[(int64_t)r * p.dim + c + e] = p.h_in[(int64_t)row.seq * p.dim + c + e];
+            for (int e = 0; e < V; e++) p.H[(int64_t)r * p.dim + cc + e] = p.h_in[(int64_t)row.seq * p.dim + cc + e];
         return;
     }
     const int share = ((row.t1 - row.t0 + W - 1) / W + K - 1) / K * K;
@@ -309,7 +315,7 @@ __global__ __launch_bounds__(64 * W) void k_gate_part(GateParams p) {
             H[e] = fmaf(a, H[e], join[1][w][e][lane]);
             P[e] *= a;
         }
-    const int64_t o = (int64_t)r * p.dim + c;
+    const int64_t o = (int64_t)r * p.dim + cc;
 #pragma unroll
     for (int e = 0; e < V; e++) {
         p.P[o + e] = P[e];
@@ -357,7 +363,7 @@ __device__ __forceinline__ void join_runs(float (&v)[V], const piece32<V> (*join
 // Template arguments from a call's values: V, FORM, IG, ZG
 #define M3_GATE_DISPATCH(p, form, CALL)                                        \
     do {                                                                       \
-        const bool two_ = (p).dim % 2 == 0, ig_ = (p).i, zg_ = (p).z;          \
+        const bool two_ = gate_two((p).dim), ig_ = (p).i, zg_ = (p).z;          \
         if ((form) == MAMBA3_GATE_DECAY) {                                     \
             if (two_) M3_GATE_D2(2, MAMBA3_GATE_DECAY, CALL);                  \
             else M3_GATE_D2(1, MAMBA3_GATE_DECAY, CALL);                       \

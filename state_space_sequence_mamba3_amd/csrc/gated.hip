@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
     }
     if (row.k == row.n - 1 && p.h_out && wave == 0 && c < p.dim)
 #pragma unroll
-        for (int e = 0; e < V; e++) p.h_out[(int64_t)row.seq * p.dim + c + e] = h[e];
+        for (int e = 0; e < V; e++) p.h_out[(int64_t)row.seq * p.dim + cc + e] = h[e];
 }
 
 // The runs of a sequence joined: the state that enters each in place of H, and the gradient that enters
@@ -303,7 +303,7 @@ GateParams gate_params(const mamba3_gated_scan_args *a) {
     p.seqlen = a->seqlen;
     p.total = a->batch * a->seqlen;
     p.dim = a->dim;
-    const int channels = a->dim % 2 ? 64 : 128;
+    const int channels = gate_two(a->dim) ? 128 : 64;
     p.tiles = (a->dim + channels - 1) / channels;
     p.rate = a->rate;
     p.rows = p.nseq;

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
             for (int e = 0; e < V; e++) {
                 if (p.part) p.part[o + e] = 0.f;
                 if (p.alone && p.dh_in && row.seq >= 0) {
-                    const int64_t h = (int64_t)row.seq * p.dim + c + e;
+                    const int64_t h = (int64_t)row.seq * p.dim + cc + e;
                     p.dh_in[h] = p.dh_out ? p.dh_out[h] : 0.f;
                 }
             }
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
         join_runs<V, W>(g, around + 2);
         if (row.k == 0 && p.dh_in && wave == 0 && c < p.dim)
 #pragma unroll
-            for (int e = 0; e < V; e++) p.dh_in[(int64_t)row.seq * p.dim + c + e] = fmaf(p.P[o + e], g[e], p.E[o + e]);
+            for (int e = 0; e < V; e++) p.dh_in[(int64_t)row.seq * p.dim + cc + e] = fmaf(p.P[o + e], g[e], p.E[o + e]);
     }
 #pragma unroll
     for (int w = 0; w < W - 1; w++)

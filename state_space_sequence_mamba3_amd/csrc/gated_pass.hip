@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * kPassWaves, 8) void k_gate_pass(GateParams p) 
         }
         if (follows && !checkpoint && c < p.dim)
 #pragma unroll
-            for (int e = 0; e < V; e++) publish(p.runs + (int64_t)r * p.dim + c + e, P[e], H[e]);
+            for (int e = 0; e < V; e++) publish(p.runs + (int64_t)r * p.dim + cc + e, P[e], H[e]);
     }
     if (row.k > 0) {                                     // (the same for the workgroup)
         // a wave's share of what comes before: every W-th run of the group, the checkpoint by the last wave
@@ -161,8 +161,8 @@ __global__ __launch_bounds__(64 * kPassWaves, 8) void k_gate_pass(GateParams p) 
 #pragma unroll
         for (int e = 0; e < V; e++) {
             const float h = fmaf(P[e], s[e], H[e]);
-            if (follows && checkpoint) publish(p.checkpoints + (first + group / kPassGroup) * p.dim + c + e, h, 0.f);
-            if (!follows && p.h_out) p.h_out[(int64_t)row.seq * p.dim + c + e] = h;
+            if (follows && checkpoint) publish(p.checkpoints + (first + group / kPassGroup) * p.dim + cc + e, h, 0.f);
+            if (!follows && p.h_out) p.h_out[(int64_t)row.seq * p.dim + cc + e] = h;
         }
     }
 #pragma unroll

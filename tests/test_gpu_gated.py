@@ -296,6 +296,23 @@ def test_one_pass(case, form, dtype):
     assert float(room[0]) == 7.0 and float(room[-1]) == 7.0
 
 
+@pytest.mark.parametrize("form", ["decay", "forget"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", [(1, 1300, 8191, None), (2, 700, 4095, None), (1, 2048, 1023, None), (70, 33, 255, None),
+                                  (3, 40, 3, None), (1, 65, 131, None), (1, 1399, 2047, [0, 700, 700, 1399])])
+def test_odd_channels(case, form, dtype):
+    """An odd count of channels, whose last lane shares one with the lane before it: whole, segments, one pass."""
+    c, back = inputs(*case, form, dtype, True, True, True)
+    check(c, back)
+    if case[0] == 1:
+        h = up(c["h_in"])
+        a = {k: up(c[k]) for k in ("x", "gate", "weight", "i", "z")}
+        a.update(form=form, cu_seqlens=up(torch.tensor(c["cu"], dtype=torch.int32)) if c["cu"] else None)
+        y, out = m3.mamba3_gated_scan_fwd(**a, h_in=h.clone())
+        got, _ = m3.mamba3_gated_scan_fwd(**a, h_in=h, h_out=h)
+        assert torch.equal(got, y) and torch.equal(h, out)
+
+
 def test_one_pass_repeats():
     """The same bits however the runs are timed: alone, beside other work on another stream, with h_out in h_in's
     place; a workspace of any content."""
