@@ -330,15 +330,20 @@ constexpr int64_t kGatePass = 1 << 22;
 enum Plan { WHOLE, SEGMENTS, PASS };
 Plan fwd_plan(GateParams &p, bool f32) {
     const int64_t whole = (int64_t)p.nseq * p.tiles, tokens = p.cu ? p.total : p.seqlen;
-    if (p.nseq == 0 || whole >= (p.cu ? 512 : 256) || tokens <= 256) return WHOLE;
+    const int64_t run = gate_pass_tokens(f32);
+    // Packed sequences differ in length, and whole the longest is the call's time: PASS up to 1536 workgroups, too. 20
+    // sequences of 820 tokens on average of 4096 channels whole 177 us, so 139; 64 of 328 of 2048 128, 102; 60 of 1000 of
+    // 4096 (1920 workgroups) 436, 459. (Up to 64 sequences: their rows are counted without a table.)
+    const bool packed = p.cu && p.nseq <= 64 && whole < 1536 && p.total >= (int64_t)p.nseq * 2 * run;
+    if (p.nseq == 0 || (whole >= (p.cu ? 512 : 256) && !packed) || tokens <= 256) return WHOLE;
     const int64_t cut = std::max<int64_t>(1024 / (p.cu ? p.tiles : whole), 2);
     auto length = [&](int64_t unit) { return ((tokens + cut - 1) / cut + unit - 1) / unit * unit; };
     auto count = [&](int64_t len) { return (tokens + len - 1) / len; };
     int64_t len = length(32);
     if (count(len) > kGateAlone) len = length(128);
-    const int64_t run = gate_pass_tokens(f32);
-    const bool pass = (int64_t)p.total * p.dim >= kGatePass && (p.cu ? 1 : (int64_t)p.nseq) * p.dim >= 1024 &&
+    const bool pass = (!p.cu || p.nseq <= 64) && (int64_t)p.total * p.dim >= kGatePass && (p.cu ? 1 : (int64_t)p.nseq) * p.dim >= 1024 &&
                       count(run) * whole < (1 << 23);
+    if (!pass && whole >= 512) return WHOLE;
     if (pass) len = run;
     if (len >= tokens) return WHOLE;
     p.seg_tokens = (int32_t)len;
@@ -365,10 +370,15 @@ void part_go(const GateParams &p, int form, hipStream_t st) {
 template <typename T>
 void scan_go(const GateParams &p, int form, hipStream_t st) {
     const int64_t groups = (int64_t)p.rows * p.tiles;
+    // 16 waves a row where there are few, or where packed sequences differ, so that the longest ends sooner; 4 where
+    // a row is less than a round of 16. 40 x 400 tokens of 4096 channels, 4 waves 118 us, 16 150; packed 60 sequences of
+    // 1000 on average 575 and 436, 40 of 200 103 and 94; 24 of 60 24 and 33, 100 of 60 of 1024 channels 28 and 38.
+    const bool ragged = p.cu && p.nseg == 1 && p.nseq;
+    const bool narrow = ragged ? groups >= 2048 || p.total / p.nseq < 128 : groups >= 1024 || p.seg_tokens < 128;
     const dim3 grid((uint32_t)groups);
 #define M3_GO(V, FORM, IG, ZG)                                                                              \
     do {                                                                                                    \
-        if (groups >= 1024 || p.seg_tokens < 128)                                                                     \
+        if (narrow)                                                                                         \
             hipLaunchKernelGGL((k_gated<T, V, FORM, IG, ZG, 4>), grid, dim3(64 * 4), 0, st, p);             \
         else hipLaunchKernelGGL((k_gated<T, V, FORM, IG, ZG, 16>), grid, dim3(64 * 16), 0, st, p);          \
     } while (0)
@@ -434,7 +444,7 @@ mamba3_status launch_gated_scan(const mamba3_gated_scan_args *a, hipStream_t st)
     GateParams p = gate_params(a);
     const bool f32 = a->dtype == MAMBA3_F32;
     const Plan plan = fwd_plan(p, f32);
-    if (plan == PASS) {                                 // (1024 channels are at most 64 sequences: no table)
+    if (plan == PASS) {                                 // (at most 64 packed sequences: no table)
         launch_gate_pass(p, a->dtype, a->form, (char *)a->workspace, st);
         return hipGetLastError() == hipSuccess ? MAMBA3_OK : MAMBA3_EHIP;
     }

@@ -313,6 +313,20 @@ def test_odd_channels(case, form, dtype):
         assert torch.equal(got, y) and torch.equal(h, out)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_pass_many_sequences(dtype):
+    """60 packed sequences, some empty, some of one token, a few long ones: more workgroups than whole sequences need."""
+    total = 60 * (128 if dtype == F32 else 256) + 20
+    cuts = sorted([0, 0, 1, 2, 130, 130, total - 1, total] + [total // 2 + 7 * k for k in range(53)])
+    assert len(cuts) == 61
+    c, back = inputs(1, total, 1152, cuts, "decay", dtype, True, False, True)
+    ref = R.scan(**c, **back)
+    got = call(c)
+    again = call(c)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+    assert R.off(got["y"], ref["y"]) <= 1 and R.off(got["h_out"], ref["h_out"]) <= 1
+
+
 def test_one_pass_repeats():
     """The same bits however the runs are timed: alone, beside other work on another stream, with h_out in h_in's
     place; a workspace of any content."""
