@@ -857,7 +857,7 @@ def mamba3_state_store(h, *, kind="int8", block=64, slots=None, entries=None, q=
     (32, 64, 128, 256) consecutive values. kind "e4m3" and "int8": q [nentries, values]; "int4": uint8
     [nentries, (values + 1) // 2], two values a byte; scale [nentries, blocks] fp32. Without q a
     cache of as many entries as rows is made. slots, entries: int32 [n] on the device; rows with either
-    outside its range are skipped. Returns (q, scale)."""
+    outside its range are skipped, and rows name different entries. Returns (q, scale)."""
     if stream is not None:
         with _on(stream, h):
             return mamba3_state_store(h, kind=kind, block=block, slots=slots, entries=entries, q=q, scale=scale)
@@ -868,7 +868,7 @@ def mamba3_state_store(h, *, kind="int8", block=64, slots=None, entries=None, q=
 
 def mamba3_state_load(q, scale, *, h, kind="int8", block=64, slots=None, entries=None, stream=None):
     """Reads cache entries back into the pool h [nslots, ...]: entry entries[k] into state slots[k], as
-    mamba3_state_store wrote them. Other states stay as they were. Returns h."""
+    mamba3_state_store wrote them; rows name different slots. Other states stay as they were. Returns h."""
     if stream is not None:
         with _on(stream, h):
             return mamba3_state_load(q, scale, h=h, kind=kind, block=block, slots=slots, entries=entries)
