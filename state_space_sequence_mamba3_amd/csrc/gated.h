@@ -151,7 +151,8 @@ template <int FORM> __device__ __forceinline__ float gate_second(float c0) {
 template <int FORM>
 __device__ __forceinline__ void gate_channel(const GateParams &p, int c, float &c0, float &c1) {
     if constexpr (FORM == MAMBA3_GATE_DECAY) {
-        const float w = p.weight[c], e = exp_full(fminf(w, 30.f)), u = 1.f + e, r = e - (u - 1.f);
+        // (a choice and no minimum, which would take a NaN for 30)
+        const float w = p.weight[c], e = exp_full(w > 30.f ? 30.f : w), u = 1.f + e, r = e - (u - 1.f);
         const float l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, r * __builtin_amdgcn_rcpf(u));
         // below 2^-12 the logarithm of 1 + e is e - e^2 / 2, which log2 of a number next to 1 is not
         const float soft = w > 20.f ? w : e < 0x1p-12f ? fmaf(-0.5f * e, e, e) : l;

@@ -218,8 +218,8 @@ __global__ __launch_bounds__(256) void k_gate_reduce(GateParams p, float *dweigh
 #pragma unroll
     for (int i = 0; i < 16; i++) s += red[i][x];
     if constexpr (FORM == MAMBA3_GATE_DECAY) {
-        // sigmoid(w) / softplus(w): 1 - e^w / 2 .. where both are e^w
-        const float w = p.weight[c], e = exp_full(fminf(w, 80.f));
+        // sigmoid(w) / softplus(w): 1 - e^w / 2 .. where both are e^w (a NaN passes the choice, not a minimum)
+        const float w = p.weight[c], e = exp_full(w > 80.f ? 80.f : w);
         const float u = 1.f + e, l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
         s *= w > 20.f ? 1.f / w : e < 0x1p-12f ? 1.f - 0.5f * e : e / (u * l);
     }

@@ -1,0 +1,41 @@
+"""The decay form of the gated recurrence with weights that are not finite: the scan whole, in segments, packed and in
+one pass, its backward, and the step."""
+import pytest
+import torch
+
+import state_space_sequence_mamba3_amd as m3
+from tests.gpu_util import note
+from tests.test_gpu_gated import BF16, F32, call, inputs, up
+
+pytestmark = pytest.mark.gpu
+
+# whole sequences, two that are joined by their own rows, packed ones, an odd count of channels, one pass
+CASES = [(2, 37, 64, None), (1, 1000, 12, None), (1, 700, 20, [0, 64, 65, 300, 700]), (3, 40, 13, None), (1, 1200, 4096, None)]
+HIT = [2, 5, 11]
+
+
+def all_of(c, back):
+    return {**call(c), **call(c, back)}
+
+
+def step_of(c):
+    w, h = up(c["weight"]), up(c["h_in"])[:c["x"].shape[0]].clone()
+    t = {k: up(c[k][:, 0].contiguous()) for k in ("x", "gate", "i", "z")}
+    y = m3.mamba3_gated_step(t["x"], t["gate"], w, h=h, i=t["i"], z=t["z"])
+    return dict(y=y, h=h)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", CASES)
+def test_nan_weights_show(case, dtype):
+    """A weight that is NaN makes everything of its channel NaN, and nothing of another."""
+    note(f"NaN weights {case} {dtype}")
+    c, back = inputs(*case, "decay", dtype, True, True, True)
+    clean = [all_of(c, back), step_of(c)]
+    c["weight"][HIT] = float("nan")
+    keep = torch.ones(case[2], dtype=torch.bool)
+    keep[HIT] = False
+    for got, want in zip([all_of(c, back), step_of(c)], clean):
+        for k in got:
+            assert bool(got[k][..., HIT].isnan().all()), k
+            assert torch.equal(got[k][..., keep], want[k][..., keep]), k
