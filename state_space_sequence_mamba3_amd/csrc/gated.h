@@ -135,8 +135,10 @@ template <int V> __device__ __forceinline__ piece32<V> to_piece(const float (&v)
     return o;
 }
 
-// e^v to an ulp or so for any v: what the product v log2(e) rounds away is put back.
+// e^v to an ulp or so for any v: what the product v log2(e) rounds away is put back. (Below -150, where e^v is zero, the
+// product of a v far out would be infinite, and what it rounds away no number; a choice, which keeps a NaN.)
 __device__ __forceinline__ float exp_full(float v) {
+    v = v < -150.f ? -150.f : v;
     const float hi = v * kLog2e, lo = fmaf(v, kLog2e, -hi) + v * 1.92596299e-8f;
     const float e = __builtin_amdgcn_exp2f(hi);
     return fmaf(e, lo * 0.69314718056f, e);

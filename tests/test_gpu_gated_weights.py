@@ -1,10 +1,11 @@
-"""The decay form of the gated recurrence with weights that are not finite: the scan whole, in segments, packed and in
-one pass, its backward, and the step."""
+"""The decay form of the gated recurrence with weights that are not finite or far below zero: the scan
+whole, in segments, packed and in one pass, its backward, and the step."""
 import pytest
 import torch
 
 import state_space_sequence_mamba3_amd as m3
-from tests.gpu_util import note
+from tests import gated_ref as R
+from tests.gpu_util import device, note
 from tests.test_gpu_gated import BF16, F32, call, inputs, up
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +40,22 @@ def test_nan_weights_show(case, dtype):
         for k in got:
             assert bool(got[k][..., HIT].isnan().all()), k
             assert torch.equal(got[k][..., keep], want[k][..., keep]), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", CASES[:4])
+def test_weights_far_below(case, dtype):
+    """softplus(w) is zero: a = 1 and u = 0, the state stays and no gradient reaches input, gates and weight."""
+    note(f"weights far below {case} {dtype}")
+    c, back = inputs(*case, "decay", dtype, True, True, True)
+    far = torch.tensor([float("-inf"), -3.3e38, -2.5e38])
+    c["weight"][HIT] = -200.0
+    ref = R.scan(**c, **back)                   # (a softplus of 1e-87, whose u counts as zero)
+    c["weight"][HIT] = far
+    got = all_of(c, back)
+    for k in got:
+        assert R.off(got[k], ref[k]) <= 1, k
+    assert torch.equal(got["h_out"].cpu()[:, HIT], c["h_in"][:, HIT])
+    for k in ("dx", "dgate", "di", "dweight"):
+        assert not got[k][..., HIT].any(), k
+    assert torch.equal(step_of(c)["h"].cpu()[:, HIT], c["h_in"][:case[0], HIT])
