@@ -158,7 +158,9 @@ __device__ __forceinline__ void gate_channel(const GateParams &p, int c, float &
         const float l = fmaf(__builtin_amdgcn_logf(u), 0.69314718056f, r * __builtin_amdgcn_rcpf(u));
         // below 2^-12 the logarithm of 1 + e is e - e^2 / 2, which log2 of a number next to 1 is not
         const float soft = w > 20.f ? w : e < 0x1p-12f ? fmaf(-0.5f * e, e, e) : l;
-        c0 = -p.rate * soft;
+        // (kept finite: zero, a decay or a sigmoid, times an infinity would be no number)
+        const float c = -p.rate * soft;
+        c0 = c < -0x1p126f ? -0x1p126f : c;
     } else {
         c0 = p.weight ? p.weight[c] : 0.f;
     }

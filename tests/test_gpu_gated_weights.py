@@ -1,5 +1,5 @@
-"""The decay form of the gated recurrence with weights that are not finite or far below zero: the scan
-whole, in segments, packed and in one pass, its backward, and the step."""
+"""The decay form of the gated recurrence with weights that are not finite or far out: the scan whole, in segments,
+packed and in one pass, its backward, and the step."""
 import pytest
 import torch
 
@@ -59,3 +59,26 @@ def test_weights_far_below(case, dtype):
     for k in ("dx", "dgate", "di", "dweight"):
         assert not got[k][..., HIT].any(), k
     assert torch.equal(step_of(c)["h"].cpu()[:, HIT], c["h_in"][:case[0], HIT])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", CASES[:4])
+@pytest.mark.parametrize("rate", [8.0, 3e38])
+def test_weights_far_above(case, rate, dtype):
+    """rate softplus(w) leaves fp32's range: a = 0 and u = 1, a state is its own token's, and no gradient reaches gate and
+    weight."""
+    note(f"weights far above {case} {dtype} rate {rate}")
+    c, back = inputs(*case, "decay", dtype, True, True, True)
+    c["rate"] = rate
+    c["weight"][HIT] = 1e30
+    if rate > 8:
+        c["weight"][:] = 10.0                   # (every channel's decay is zero)
+    ref = R.scan(**c, **back)
+    if rate == 8:
+        c["weight"][HIT] = torch.tensor([1e38, 3e38, float("inf")])
+    got = all_of(c, back)
+    for k in got:
+        assert R.off(got[k], ref[k]) <= 1, k
+    for k in ("dgate", "dweight", "dh_in"):
+        assert not got[k][..., HIT].any(), k
+    assert bool(step_of(c)["h"].isfinite().all())
