@@ -28,6 +28,7 @@ struct GateParams {
     // of them in a padded sequence and as many as it needs in a packed one (nseg 0).
     int32_t rows, nseg, seg_tokens;
     int32_t alone;              // whether a row joins the runs around it itself, without k_gate_chain
+    int32_t first;              // the launch's first row (k_gate_bwd, which goes down from it) or sequence (k_gate_chain)
     const int4 *table;          // the rows of a packed batch of more than 64 sequences, t0, t1, sequence (-1: no run)
     const int32_t *seq_row;     // [nseq + 1] a sequence's first row in the table
     float *P;                   // [rows][D] a run's product of decays
@@ -385,12 +386,15 @@ __device__ __forceinline__ void join_runs(float (&v)[V], const piece32<V> (*join
         else CALL(V, FORM, false, false);                                      \
     } while (0)
 
+// Workgroups of a launch: below 2^32 threads. A call may have 2^24 workgroups, so those of more than 256 threads go in parts.
+constexpr int64_t gate_most(int threads) { return ((1LL << 32) - 1) / threads; }
+
 GateParams gate_params(const mamba3_gated_scan_args *a);
 // The parts of a call's workspace that the runs take, and the table's launch
 size_t gate_run_bytes(const GateParams &p, bool back);
 char *gate_runs(GateParams &p, char *ws, bool back);
 void launch_gate_table(const GateParams &p, hipStream_t st);
-void launch_gate_chain(const GateParams &p, hipStream_t st);
+void launch_gate_chain(GateParams p, hipStream_t st);
 // The scan in one pass over runs of gate_pass_tokens tokens, and its workspace
 int gate_pass_tokens(bool f32);
 size_t gate_pass_bytes(const GateParams &p);

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * W) void k_gated(GateParams p) {
 constexpr int kChainWaves = 16, kChainLoads = 8;
 __global__ __launch_bounds__(64 * kChainWaves) void k_gate_chain(GateParams p) {
     __shared__ float join[2][kChainWaves][64];
-    const int blocks = (p.dim + 63) / 64, s = blockIdx.x / blocks;
+    const int blocks = (p.dim + 63) / 64, s = p.first + blockIdx.x / blocks;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = blockIdx.x % blocks * 64 + lane, cc = min(c, p.dim - 1);
     int r0 = s * p.nseg, r1 = r0 + p.nseg;
@@ -435,9 +435,14 @@ void launch_gate_table(const GateParams &p, hipStream_t st) {
 
 static int64_t chain_blocks(const GateParams &p) { return (int64_t)p.nseq * ((p.dim + 63) / 64); }
 
-void launch_gate_chain(const GateParams &p, hipStream_t st) {
+void launch_gate_chain(GateParams p, hipStream_t st) {
     if (p.alone) return;
-    hipLaunchKernelGGL(k_gate_chain, dim3((uint32_t)chain_blocks(p), p.E ? 2 : 1), dim3(64 * kChainWaves), 0, st, p);
+    const int64_t blocks = (p.dim + 63) / 64, part = gate_most(2 * 64 * kChainWaves) / blocks;     // sequences of a launch
+    for (int64_t s = 0; s < p.nseq; s += part) {
+        p.first = (int32_t)s;
+        const dim3 grid((uint32_t)(std::min<int64_t>(part, p.nseq - s) * blocks), p.E ? 2 : 1);
+        hipLaunchKernelGGL(k_gate_chain, grid, dim3(64 * kChainWaves), 0, st, p);
+    }
 }
 
 mamba3_status launch_gated_scan(const mamba3_gated_scan_args *a, hipStream_t st) {

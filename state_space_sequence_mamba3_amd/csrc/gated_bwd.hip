@@ -39,7 +39,7 @@ __global__ __launch_bounds__(64 * kGateBwdWaves, kGateBwdOccupancy) void k_gate_
     __shared__ piece32<V> join[3][W][64], around[4][W][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the last runs first: they were read last and may still lie in the cache
-    const int r = p.rows - 1 - (int)(blockIdx.x / p.tiles);
+    const int r = p.first - (int)(blockIdx.x / p.tiles);
     const GateRow row = gate_row(p, r);
     const int c = (blockIdx.x % p.tiles * 64 + lane) * V, cc = min(c, p.dim - V);
     const int64_t o = (int64_t)r * p.dim + cc;
@@ -248,17 +248,21 @@ GateParams bwd_plan(const mamba3_gated_scan_bwd_args *b) {
 }
 
 template <typename T>
-void bwd_go(const GateParams &p, int form, hipStream_t st) {
-    const dim3 grid((uint32_t)((int64_t)p.rows * p.tiles));
+void bwd_go(GateParams p, int form, hipStream_t st) {
+    dim3 grid((uint32_t)((int64_t)p.rows * p.tiles));
 #define M3_GO(V, FORM, IG, ZG) \
     hipLaunchKernelGGL((k_gate_part<T, V, FORM, IG, ZG, true, 4>), grid, dim3(256), 0, st, p)
     M3_GATE_DISPATCH(p, form, M3_GO);
 #undef M3_GO
     launch_gate_chain(p, st);
+    const int part = (int)(gate_most(64 * kGateBwdWaves) / p.tiles);                  // rows of a launch
+    for (p.first = p.rows - 1; p.first >= 0; p.first -= part) {
+        grid.x = (uint32_t)(std::min((int64_t)part, (int64_t)p.first + 1) * p.tiles);
 #define M3_GO(V, FORM, IG, ZG) \
     hipLaunchKernelGGL((k_gate_bwd<T, V, FORM, IG, ZG>), grid, dim3(64 * kGateBwdWaves), 0, st, p)
-    M3_GATE_DISPATCH(p, form, M3_GO);
+        M3_GATE_DISPATCH(p, form, M3_GO);
 #undef M3_GO
+    }
 }
 
 }  // namespace
