@@ -446,7 +446,7 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *   RMS norm        its rows
  * and for the operators of the gated layer
  *   gated scan      S ceil(D / 128), ceil(D / 64) for ceil(D / 128) where D is 1 above a multiple of
- *                   128, or fewer than 2^23 where few sequences are cut
+ *                   128, or fewer than 2^22 where few sequences are cut
  *     backward      the same with S ceil(seqlen / 32) (padded) or S + ceil(seqlen / 32) (packed) for S; and
  *                   S ceil(D / 64)
  *     step          ceil(batch ceil(D / 4) / 256)

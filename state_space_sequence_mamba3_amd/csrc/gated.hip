@@ -341,8 +341,10 @@ Plan fwd_plan(GateParams &p, bool f32) {
     auto count = [&](int64_t len) { return (tokens + len - 1) / len; };
     int64_t len = length(32);
     if (count(len) > kGateAlone) len = length(128);
+    // (its workgroups have 1024 threads, and all are one launch: the runs' numbers are its own)
+    const int64_t runs = p.cu ? p.nseq + count(run) : p.nseq * count(run);
     const bool pass = (!p.cu || p.nseq <= 64) && (int64_t)p.total * p.dim >= kGatePass && (p.cu ? 1 : (int64_t)p.nseq) * p.dim >= 1024 &&
-                      count(run) * whole < (1 << 23);
+                      runs * p.tiles <= gate_most(1024);
     if (!pass && whole >= 512) return WHOLE;
     if (pass) len = run;
     if (len >= tokens) return WHOLE;
