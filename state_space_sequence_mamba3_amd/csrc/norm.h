@@ -75,9 +75,11 @@ __device__ __forceinline__ float wave_sum(float v) {
     return sum_across_rows(v);
 }
 // Squares leave fp32's range long before the values do: a row whose mean square + eps is no number of
-// [2^-80, infinity) is summed again with its values times a power of two, `row_scale` of that mean, which
-// brings every finite row back inside.
-constexpr float kLeastMean = 0x1p-80f;
+// [2^-98, infinity) is summed again with its values times a power of two, `row_scale` of that mean, which
+// brings every finite row back inside, whatever its length (2^25 at most): below, 2^25 squares of a mean of 2^-98 scaled by
+// 2^200 add up to 2^127, and one least subnormal value alone, squared and scaled, has a mean of 2^-123. At 2^-98
+// unscaled squares that are subnormal or lost are 2^-28 of the mean at most.
+constexpr float kLeastMean = 0x1p-98f;
 __device__ __forceinline__ bool in_range(float mean) { return mean >= kLeastMean && mean < INFINITY; }
 __device__ __forceinline__ float row_scale(float mean) { return mean < kLeastMean ? 0x1p100f : 0x1p-80f; }
 
