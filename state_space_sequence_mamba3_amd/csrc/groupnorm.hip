@@ -161,12 +161,16 @@ __device__ __forceinline__ GnLane gn_lane(const GnParams &p, int tile) {
 }
 
 // t -> t - mean (in place, times a power of two where squares would leave fp32's range), and 1 / deviation of
-// it. Returns that power.
+// it. Returns that power. Where most of the differences is what the mean's rounding left (a group of equal values far from
+// zero), the squares' mean less that of the differences has no digits, may be negative and says nothing of the values'
+// size: the differences are the group from then on, until their mean is within the deviation. Each time it falls
+// by 2^-20 or so: a group next to the end of fp32's range needs eight rounds with the least eps.
+constexpr int kGnRounds = 16;
 template <int WPG>
 __device__ __forceinline__ float gn_stats(const GnParams &p, const GnLane &l, float (&t)[kNV], float &r,
                                           float (*red)[2][16], int &turn) {
     float k = 1.f;
-    for (;;) {
+    for (int round = 1;; round++) {
         float d[kNV], s[2] = {0.f, 0.f};
         if (p.center) {
 #pragma unroll
@@ -188,7 +192,9 @@ __device__ __forceinline__ float gn_stats(const GnParams &p, const GnLane &l, fl
         group_sums<WPG, 2>(s, p.lanes, red, turn);
         const float rest = p.center ? s[0] * p.inv : 0.f;
         const float mean = fmaf(s[1], p.inv, -rest * rest) + p.eps * k * k;
-        const bool again = k == 1.f && !in_range(mean) && l.n;
+        // (scaled down, a group without deviation has lost eps: in its own size it has it)
+        const bool rough = rest * rest > mean || (k < 1.f && mean < kLeastMean);
+        const bool again = l.n && round < kGnRounds && (rough || (k == 1.f && !in_range(mean)));
         if (WPG == 1 ? !__any(again) : !again) {         // (the same for all lanes of a group)
             r = __builtin_amdgcn_rsqf(mean);
 #pragma unroll
@@ -196,9 +202,12 @@ __device__ __forceinline__ float gn_stats(const GnParams &p, const GnLane &l, fl
             return k;
         }
         if (again) {
-            k = row_scale(mean);
+            const float by = rough ? (k > 1.f ? 0x1p-100f : k < 1.f ? 0x1p80f : 1.f) : row_scale(mean);
+            // (differences where they are small, values where their sums are too large)
+            const bool take = rough || mean < kLeastMean;
 #pragma unroll
-            for (int e = 0; e < kNV; e++) t[e] *= k;
+            for (int e = 0; e < kNV; e++) t[e] = (take ? d[e] : t[e]) * by;
+            k = rough ? 1.f : by;
         }
     }
 }

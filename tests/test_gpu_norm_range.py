@@ -1,9 +1,10 @@
-"""The norms where squares are at the ends of what fp32 holds: rows of small values whose squares, scaled up, add up past
-the range."""
+"""The norms where squares or differences are at the ends of what fp32 holds: rows of small values whose squares, scaled up,
+add up past the range; centered groups of equal values far from zero."""
 import pytest
 import torch
 
 import state_space_sequence_mamba3_amd as m3
+from tests import gated_ref as R
 from tests import layer_bounds as LB
 from tests import layer_ref as LR
 from tests.gpu_util import note
@@ -45,3 +46,42 @@ def test_small_rows(dim, types):
     got = m3.mamba3_rmsnorm_bwd(up(s), up(w), dy=up(dy), eps=0.0)
     LR.check(got["dx"], ref[0], mag[0], LB.norm_bwd_count(dim), "dx")
     LR.check(got["dweight"], ref[1], mag[1], LB.dweight_count(rows, dim), "dweight")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("eps", [1e-5, 1e-26, 1e-30])
+@pytest.mark.parametrize("act", ["none", "gate"])
+@pytest.mark.parametrize("size", [24, 100, 600, 5000])
+def test_equal_values_far_from_zero(size, act, eps, dtype):
+    """A centered group of equal values is its bias, wherever it lies: what the rounding of its mean leaves is no
+    deviation. Its gradient is that of a group of zeros."""
+    note(f"group norm equal values size {size} {act} eps {eps} {dtype}")
+    far = [1e3, 1e6, 3e8, 1e9, -3.3e9, 1e12, 1e20, -1.7e30, 3e38]
+    rows, groups = 6, len(far)
+    c, dy = inputs(rows, groups, size, act, dtype)
+    x = c["x"].view(rows, groups, size)
+    x[::2] = 0.0
+    ref = R.groupnorm(c["x"], c["weight"], c["bias"], groups, c["z"], act, True, eps, dy)
+    x[::2] = torch.tensor(far, dtype=dtype)[:, None]
+    a = dict(groups=groups, z=up(c["z"]), act=act, eps=eps)
+    got = dict(y=m3.mamba3_groupnorm_fwd(up(c["x"]), up(c["weight"]), up(c["bias"]), **a),
+               **m3.mamba3_groupnorm_bwd(up(c["x"]), up(c["weight"]), up(c["bias"]), dy=up(dy), **a))
+    # The differences that are summed at last are equal and within the deviation (their mean's square is at most the
+    # variance with eps), and their mean is off by DEPTH + 4 roundings of them: so much n is off, in deviations.
+    # That mean's square is taken off the squares' mean with as many roundings, twice, halved by the root.
+    n, r = R.DEPTH + 4, eps ** -0.5
+    sh = lambda t: t.double().view(rows, groups, size)   # noqa: E731
+    sz = dsz = torch.ones(rows, groups, size).double()
+    if act == "gate":
+        sz, _, dsz, _ = R.silu(sh(c["z"]))
+    w, d = c["weight"].double().view(groups, size).abs(), sh(dy) * sz
+    more = dict(y=n * w * sz.abs(), dz=n * w * (sh(dy) * dsz).abs(), dbias=0 * w, dweight=n * d[::2].abs().sum(0))
+    dn = (d * w).abs()
+    more["dx"] = (2 * n + 1) * r * (dn + dn.mean(-1, keepdim=True))
+    for k in got:
+        v, e = ref[k]
+        extra = more[k].clone()
+        if extra.dim() == 3:
+            extra[1::2] = 0
+        assert not got[k].isnan().any(), k
+        assert R.off(got[k], (v, e + extra.reshape(e.shape))) <= 1, k
