@@ -49,6 +49,18 @@ __device__ __forceinline__ float cache_quotient(float v, float scale, float r) {
     return fmaf(fmaf(-scale, q, v), r, q);
 }
 
+// q scale rounded once to the states' type: to fp32 as it is; to bf16 from the exact product, which has at most 31 bits, by
+// way of an fp32 that is odd where it is not exact (so that no middle of two bf16 comes from rounding before).
+template <typename T> __device__ __forceinline__ T cache_value(float q, float scale);
+template <> __device__ __forceinline__ float cache_value<float>(float q, float scale) { return q * scale; }
+template <> __device__ __forceinline__ bf16 cache_value<bf16>(float q, float scale) {
+    const double v = (double)q * (double)scale;
+    const float f = (float)v;
+    uint32_t u = __float_as_uint(f);
+    if ((double)f != v) u = (u - (fabs((double)f) > fabs(v) ? 1u : 0u)) | 1u;
+    return from_f<bf16>(__uint_as_float(u));
+}
+
 // A lane's values from value c of a state on; zeros behind its end
 template <typename T>
 __device__ __forceinline__ typename CacheLane<T>::type cache_values(const T *h, int c, int values) {
@@ -173,12 +185,12 @@ __global__ __launch_bounds__(256) void k_state_load(CacheParams p) {
         if (c + L <= p.values) {
             typename CacheLane<T>::type o;
 #pragma unroll
-            for (int e = 0; e < L; e++) o[e] = from_f<T>(v[e] * scale[u]);
+            for (int e = 0; e < L; e++) o[e] = cache_value<T>(v[e], scale[u]);
             *(typename CacheLane<T>::type *)(h + c) = o;
         } else {
 #pragma unroll
             for (int e = 0; e < L; e++)
-                if (c + e < p.values) h[c + e] = from_f<T>(v[e] * scale[u]);
+                if (c + e < p.values) h[c + e] = cache_value<T>(v[e], scale[u]);
         }
     }
 }
