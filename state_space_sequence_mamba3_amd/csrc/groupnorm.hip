@@ -164,7 +164,7 @@ __device__ __forceinline__ GnLane gn_lane(const GnParams &p, int tile) {
 // it. Returns that power. Where most of the differences is what the mean's rounding left (a group of equal values far from
 // zero), the squares' mean less that of the differences has no digits, may be negative and says nothing of the values'
 // size: the differences are the group from then on, until their mean is within the deviation. Each time it falls
-// by 2^-20 or so: a group next to the end of fp32's range needs eight rounds with the least eps.
+// by 2^-20 or so: groups next to the end of fp32's range need up to eight rounds with eps 1e-5, twelve with the least one.
 constexpr int kGnRounds = 16;
 template <int WPG>
 __device__ __forceinline__ float gn_stats(const GnParams &p, const GnLane &l, float (&t)[kNV], float &r,

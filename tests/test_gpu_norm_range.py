@@ -85,3 +85,24 @@ def test_equal_values_far_from_zero(size, act, eps, dtype):
             extra[1::2] = 0
         assert not got[k].isnan().any(), k
         assert R.off(got[k], (v, e + extra.reshape(e.shape))) <= 1, k
+
+
+@pytest.mark.parametrize("size", [100, 600, 5000])
+def test_neighbours_far_from_zero(size):
+    """Groups of two neighbouring fp32 values keep their deviations, which are below what the mean's rounding leaves."""
+    note(f"group norm neighbours size {size}")
+    g = torch.Generator().manual_seed(size)
+    far = torch.tensor([1e3, -1e6, 1.1e9, 1e20, -1.7e30])
+    rows, groups = 6, len(far)
+    x = far[:, None].expand(groups, size).repeat(rows, 1, 1)
+    up_ = torch.rand(x.shape, generator=g) < torch.tensor([0.5, 0.2, 0.05, 0.5, 0.3, 0.1]).view(rows, 1, 1)
+    up_[..., 3] = True
+    x = torch.where(up_, torch.nextafter(x, torch.tensor(float("inf"))), x)
+    d = x.double() - far.double()[:, None]                  # (exact; the mean of so small numbers loses nothing in 64 bits)
+    d = d - d.mean(-1, keepdim=True)
+    n = d / torch.sqrt((d * d).mean(-1, keepdim=True) + 1e-30)
+    y = m3.mamba3_groupnorm_fwd(up(x.reshape(rows, -1)), groups=groups, eps=1e-30).view(n.shape)
+    # differences of neighbours are exact; their mean, within the deviation, is off by DEPTH + 4 roundings of it; three
+    # more of n itself, and its deviation's: the squares' sum, root and what is taken off it
+    c = R.DEPTH + 4
+    assert R.off(y, (n, c + n.abs() * (3 + (R.DEPTH + 6) / 2 + 4 + c))) <= 1
