@@ -450,7 +450,7 @@ mamba3_status mamba3_decode_step(const mamba3_decode_args *args, void *stream);
  *     backward      the same with S ceil(seqlen / 32) (padded) or S + ceil(seqlen / 32) (packed) for S; and
  *                   S ceil(D / 64)
  *     step          ceil(batch ceil(D / 4) / 256)
- *   group norm      at most 2048 or G, whatever its rows (fewer than 2^31)
+ *   group norm      at most 4096 or G, whatever its rows (fewer than 2^31)
  *   state cache     n ceil(values / 2048), 4096 with bf16
  */
 
@@ -697,11 +697,14 @@ mamba3_status mamba3_rmsnorm_bwd(const mamba3_rmsnorm_bwd_args *args, void *stre
  * h_in, h_out       [S, D] fp32 or NULL (zero, not written)
  * Token rows, cu_seqlens, nseq and tokens outside the sequences are as above. A sigmoid
  * below 2^-126 may count as 0. States are fp32, and 1 - a^2 keeps its relative
- * precision where a is next to 1, down to 2^-126 (a u below 2^-63 may count as 0). y overlaps no input; h_out may be h_in
+ * precision where a is next to 1, down to 2^-126 (a u below 2^-63 may count as 0). A weight that is NaN makes
+ * its channel NaN. y overlaps no input; h_out may be h_in
  * exactly. workspace: at least mamba3_gated_scan_workspace_size(args) bytes (0 for
  * many shapes), 256-byte aligned: where few sequences would leave the GPU empty, they run
- * as segments and it holds what those hand on, at most 9 bytes for a channel of 32 tokens
- * or of a sequence. Results do not depend on timing (bitwise reproducible). */
+ * as segments and it holds what those hand on: for a run and channel 8 or 9 bytes, and
+ * with more than 64 packed sequences a table of the runs. Results do not depend on timing (bitwise
+ * reproducible). Runs may wait for words that others write there, a bounded time: a program that lets
+ * another call write the workspace meanwhile gets NaN, or what lies there, and no error status. */
 typedef enum { MAMBA3_GATE_DECAY = 0, MAMBA3_GATE_FORGET = 1 } mamba3_gate_form;
 
 typedef struct {
@@ -734,8 +737,8 @@ mamba3_status mamba3_gated_scan_fwd(const mamba3_gated_scan_args *args, void *st
  * through it. No output overlaps an input or another
  * output. workspace: at least mamba3_gated_scan_bwd_workspace_size(args) bytes, 256-byte
  * aligned: decays, states and gradients between runs of 32 tokens and partial
- * sums of dweight, 16 bytes a run and channel; all sums have a fixed order
- * (bitwise reproducible). */
+ * sums of dweight, 16 bytes a run and channel, with more than 64 packed sequences a table
+ * of the runs; all sums have a fixed order (bitwise reproducible). */
 typedef struct {
     mamba3_gated_scan_args fwd;
     int64_t dy_row;
@@ -782,7 +785,8 @@ mamba3_status mamba3_gated_step(const mamba3_gated_step_args *args, void *stream
  * x, z, y       [rows, dim] token dtype; z with MAMBA3_GN_GATE and MAMBA3_GN_PREGATE only
  * weight, bias  [dim] fp32 or NULL (ones, zeros)
  * groups divides dim, M <= 8192; rows < 2^31; eps is finite and >= 0. The mean is taken off before
- * squares are summed. As in the RMS norm, a group whose mean square leaves fp32's range is
+ * squares are summed, until it is within the deviation: a group of equal values is its bias with any
+ * eps above 0. As in the RMS norm, a group whose mean square leaves fp32's range is
  * summed scaled by a power of two. Outputs overlap neither each other nor any input. */
 typedef enum { MAMBA3_GN_NONE = 0, MAMBA3_GN_SILU = 1, MAMBA3_GN_GATE = 2, MAMBA3_GN_PREGATE = 3 } mamba3_gn_act;
 
