@@ -13,8 +13,9 @@
 // over short runs (gated_pass.hip), or as segments: k_gate_part reads the inputs for the segments' (P, H), a row
 // joins those before it or k_gate_chain does for all, and the walk starts from the states that enter the segments.
 //
-// 8 x 4096 tokens of 4096 channels, decay, i, bf16: 209 us, 1075 MB, 5.1 TB/s (a large copy runs at 4.88), the vector
-// unit 78 % busy. A step of 256 x 4096 from slots takes 6.0 us, of 4 x 2048 3.7: a few memory latencies.
+// 8 x 4096 tokens of 4096 channels, decay, i, bf16: 209 us a call among others, 1075 MB, 5.1 TB/s (a large copy runs at
+// 4.88), the vector unit 77 % busy; in traces of single calls medians of 212 to 240, as the GPU's clocks go. A step of
+// 256 x 4096 from slots takes 6.0 us, of 4 x 2048 3.8: a few memory latencies.
 #include <algorithm>
 
 #include "gated.h"

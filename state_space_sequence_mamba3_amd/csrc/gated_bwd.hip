@@ -12,11 +12,12 @@
 // directions, and goes over its tokens forwards for the states and backwards for the gradients. Nothing walks a
 // sequence, so that one long sequence fills the GPU as a batch does, for a second read of the inputs.
 //
-// 8 x 2048 tokens of 4096 channels, decay, i, bf16: 322 us (k_gate_part 124, k_gate_chain 13, k_gate_bwd 187,
-// k_gate_reduce 5), 1.55 GB, 4.8 TB/s: HBM-bound with the inputs read twice; read once the floor would be 193. Both
-// directions need the whole sequence before its first token's gradient is known. Runs walked by k_gate_bwd with the next
-// tokens' loads in flight spilled; six waves a SIMD, sequences grouped for the last-level cache, and a first pass of one
-// wave a run or with a prefetch were all slower.
+// 8 x 2048 tokens of 4096 channels, decay, i, bf16: 326 us (k_gate_part 128, k_gate_chain 13, k_gate_bwd 185,
+// k_gate_reduce 5), 1.55 GB, 4.8 TB/s: HBM-bound with the inputs read twice; read once the floor would be 193. A
+// token's gradient needs the state from before its run and the gradient from behind it: the first read is for these. (A
+// forward that kept its runs' states, 4 bytes a channel every 32 tokens, would save the states' part of it; it keeps
+// nothing.) Runs walked by k_gate_bwd with the next tokens' loads in flight spilled; six waves a SIMD, sequences grouped for
+// the last-level cache, and a first pass of one wave a run or with a prefetch were all slower.
 #include <algorithm>
 
 #include "gated.h"

@@ -5,7 +5,8 @@
 // One pass: a lane holds 16 bytes of consecutive values, a block 4 to 64 consecutive lanes, so that a block's largest
 // value needs no memory. HBM-bound; a workgroup's index and load latencies are a good part of its life, which two
 // pieces with their loads together share (64 states of 262144 fp32 values to 8 bits and back, with 1, 2, 4 pieces
-// 43.8, 39.6, 41.8 us, 152 MB; 8 values a lane, 32 bytes apart, 40.4). Read back from 4 bits 15.6 us, 78 MB: 5.0 TB/s.
+// 43.8, 39.6, 41.8 us, 152 MB; 8 values a lane, 32 bytes apart, 40.4). Read back from 4 bits 15.9 us, 78 MB: 4.9 TB/s,
+// a large copy's rate (a call among others 17).
 #include "layer.h"
 
 namespace m3 {
